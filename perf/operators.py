@@ -60,8 +60,10 @@ def _log(rng, lo, hi):
 
 
 def draw(rng):
-    """A case of the listed ones' ranges (sizes of 1536 and 3072 are moved on by one step of 8)."""
-    return {k: v + 8 if type(v) is int and v in (1536, 3072) else v for k, v in _draw(rng).items()}
+    """A case of the listed ones' ranges (sizes of 1536 and 3072 are moved on by one step of 8, but for the
+    layer whose sizes are multiples of 128)."""
+    c = _draw(rng)
+    return c if c["op"] == "moe" else {k: v + 8 if type(v) is int and v in (1536, 3072) else v for k, v in c.items()}
 
 
 def _draw(rng):
