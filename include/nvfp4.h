@@ -356,6 +356,181 @@ nvfp4_status nvfp4_linear_noalloc(const void *x_bf16, int64_t m, int64_t k, int6
                                   const float *alpha_dev, const void *bias_bf16,
                                   void *out_bf16, int64_t ldo, nvfp4_stream_t stream);
 
+/* ---- the operators around the linear layer -------------------------------
+ * A transformer block's FFN, dense or mixture-of-experts, with no elementwise
+ * pass over memory between its GEMMs: the norm in front quantizes, activation
+ * and residual run in the GEMM's epilogue, and the expert layer's tokens are
+ * sorted, copied and combined by one kernel each. */
+
+/* Activations of the GEMM epilogue (v = alpha * acc + bias, in fp32):
+ *   RELU    max(v, 0)
+ *   GELU    0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))
+ *   SILU    v / (1 + e^-v)
+ *   SWIGLU  silu(gate) * up      gated: output column j comes from the weight
+ *   GEGLU   gelu(gate) * up      rows 2j (gate) and 2j + 1 (up), interleaved
+ *                                before nvfp4_prepare_weight */
+typedef enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_RELU = 1,
+    NVFP4_ACT_GELU = 2,
+    NVFP4_ACT_SILU = 3,
+    NVFP4_ACT_SWIGLU = 4,
+    NVFP4_ACT_GEGLU = 5
+} nvfp4_activation;
+
+/* nvfp4_gemm with an activation and a residual in its epilogue:
+ *   out[i, j] = bf16( act(alpha * acc[i, j] + bias[j]) + residual[i, j] ),
+ * all in fp32, one rounding.  With a gated activation acc and bias have
+ * 2 * n_out columns (2 * n_out <= n_w) and
+ *   out[i, j] = bf16( g(v[i, 2j]) * v[i, 2j+1] + residual[i, j] ).
+ *   act            an nvfp4_activation
+ *   residual_bf16  in   NULL or [m, ldr] bf16 (rows on 16-byte boundaries);
+ *                       like every input it may not overlap out
+ *   n_out          in   output columns
+ *   bias_bf16      in   NULL or one bf16 per accumulator column
+ * Everything else as for nvfp4_gemm; with NVFP4_ACT_NONE and no residual the
+ * result is nvfp4_gemm's bit for bit. */
+nvfp4_status nvfp4_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m,
+                            const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n_w, int64_t n_out,
+                            int64_t k, const float *alpha_dev, const void *bias_bf16,
+                            int act, const void *residual_bf16, int64_t ldr,
+                            void *out_bf16, int64_t ldo, nvfp4_stream_t stream);
+
+/* nvfp4_linear with the same epilogue, on every path of it (the single-launch
+ * small-m linear, split K, the transform). */
+nvfp4_status nvfp4_linear_act(const void *x_bf16, int64_t m, int64_t k, int64_t ldx,
+                              const float *gs_dev, const void *transform_bf16, int bs,
+                              const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n_w, int64_t n_out,
+                              const float *alpha_dev, const void *bias_bf16,
+                              int act, const void *residual_bf16, int64_t ldr,
+                              void *out_bf16, int64_t ldo,
+                              void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* nvfp4_mxfp4_gemm and nvfp4_mxfp4_linear with the same epilogue (no alpha). */
+nvfp4_status nvfp4_mxfp4_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m,
+                                  const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n_w, int64_t n_out,
+                                  int64_t k, const void *bias_bf16,
+                                  int act, const void *residual_bf16, int64_t ldr,
+                                  void *out_bf16, int64_t ldo, nvfp4_stream_t stream);
+nvfp4_status nvfp4_mxfp4_linear_act(const void *x_bf16, int64_t m, int64_t k, int64_t ldx,
+                                    const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n_w, int64_t n_out,
+                                    const void *bias_bf16, int act, const void *residual_bf16, int64_t ldr,
+                                    void *out_bf16, int64_t ldo, void *workspace, size_t workspace_bytes,
+                                    nvfp4_stream_t stream);
+
+/* nvfp4_grouped_gemm with an activation: n counts output columns, so with a
+ * gated activation each expert has 2 * n interleaved weight rows (and bias
+ * entries).  A group's weight rows are a multiple of 128. */
+nvfp4_status nvfp4_grouped_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,
+                                    const int32_t *group_offsets_dev, int num_groups,
+                                    const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n, int64_t k,
+                                    const float *alpha_dev, const void *bias_bf16, int act,
+                                    void *out_bf16, int64_t ldo, nvfp4_stream_t stream);
+
+/* Quantized formats of the norm's output.  NVFP4 and MXFP4 are the operands of
+ * nvfp4_gemm and nvfp4_mxfp4_gemm.  MXFP8 (OCP Microscaling) is for layers kept
+ * in 8 bits: per 32 elements s = clamp(floor(log2(amax)) - 8, -127, 127)
+ * (-127 for an all-zero block), code s + 127 (E8M0), and
+ * q_i = e4m3_rne_satfinite(v_i * 2^-s), one byte per element in rows of
+ * roundup(k, 32) bytes; scales in the tiled layout, as MXFP4's. */
+typedef enum {
+    NVFP4_FORMAT_NVFP4 = 0,
+    NVFP4_FORMAT_MXFP4 = 1,
+    NVFP4_FORMAT_MXFP8 = 2
+} nvfp4_format;
+
+/* Bytes of an MXFP8 operand's codes: rows * roundup(k, 32) (its scales:
+ * nvfp4_mxfp4_scale_bytes). */
+size_t nvfp4_mxfp8_bytes(int64_t rows, int64_t k);
+
+/* Residual addition, RMS norm and quantization in one pass over the rows:
+ *   s = x + residual (fp32; s = x without a residual),  h = bf16(s),
+ *   y = (s / sqrt(mean(s^2) + eps)) * gamma   (fp32, sums in fp32),
+ *   x_q, x_sf = the quantization of y (fp32, not rounded to bf16 first).
+ * A row with a non-finite element yields unspecified codes for that row only.
+ *   x_bf16         in   [m, ldx] bf16, k columns used
+ *   residual_bf16  in   NULL or [m, ldr] bf16
+ *   gamma_bf16     in   [k] bf16, 16-byte aligned
+ *   eps            >= 0
+ *   k              1 <= k <= 65536
+ *   format         an nvfp4_format
+ *   gs_dev         in   device fp32 (NVFP4 only, else ignored)
+ *   h_bf16         out  NULL, or with a residual [m, ldh] bf16: the updated
+ *                       residual stream; may be x or residual itself (same
+ *                       pointer and row stride)
+ *   x_q            out  nvfp4_packed_bytes(m, k), or nvfp4_mxfp8_bytes for MXFP8
+ *   x_sf           out  nvfp4_scale_bytes(m, k), or nvfp4_mxfp4_scale_bytes for
+ *                       the MX formats (padding rows and columns zero) */
+nvfp4_status nvfp4_add_rmsnorm_quant(const void *x_bf16, int64_t ldx, const void *residual_bf16, int64_t ldr,
+                                     const void *gamma_bf16, float eps, int64_t m, int64_t k, int format,
+                                     const float *gs_dev, void *h_bf16, int64_t ldh,
+                                     uint8_t *x_q, uint8_t *x_sf, nvfp4_stream_t stream);
+
+/* Mixture-of-experts token movement around nvfp4_grouped_gemm.
+ *
+ * nvfp4_moe_sort places assignment (t, j), token t's j-th expert, into groups
+ * by expert, each group padded to a multiple of 128 rows, assignments of an
+ * expert in token order:
+ *   expert_ids     in   [tokens, topk] int32 (id_bytes 4) or int64 (8); ids
+ *                       outside [0, experts) (e.g. -1) mark dropped assignments
+ *   group_offsets  out  int32 [experts + 1], as nvfp4_grouped_gemm takes them
+ *   group_counts   out  int32 [experts], assignments of each expert
+ *   dest           out  int32 [tokens, topk], the row of each assignment, -1
+ *                       for a dropped one
+ *   workspace      device scratch, nvfp4_moe_sort_workspace_bytes
+ * nvfp4_moe_rows bounds the rows for any routing (a multiple of 128): the row
+ * count of the buffers below.  1 <= topk <= 64, 1 <= experts <= 1024.  With
+ * tokens == 0 the offsets and counts are still written (zeros). */
+int64_t nvfp4_moe_rows(int64_t tokens, int topk, int experts);
+size_t nvfp4_moe_sort_workspace_bytes(int64_t tokens, int topk, int experts);
+nvfp4_status nvfp4_moe_sort(const void *expert_ids, int id_bytes, int64_t tokens, int topk, int experts,
+                            int32_t *group_offsets, int32_t *group_counts, int32_t *dest,
+                            void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* out[dest[t, j]] = x[t] for every assignment that is not dropped; the padding
+ * rows of each group are set to zero, rows at or past group_offsets[experts]
+ * are left alone.
+ *   x_bf16    in   [tokens, ldx] bf16, h columns
+ *   dest, group_offsets, group_counts   in   from nvfp4_moe_sort
+ *   out_bf16  out  [rows, ldo] bf16, rows >= nvfp4_moe_rows
+ * Its gradient is nvfp4_moe_combine of the rows' gradient without weights. */
+nvfp4_status nvfp4_moe_dispatch(const void *x_bf16, int64_t ldx, const int32_t *dest, int64_t tokens, int topk,
+                                int64_t rows, int64_t h, const int32_t *group_offsets,
+                                const int32_t *group_counts, int experts, void *out_bf16, int64_t ldo,
+                                nvfp4_stream_t stream);
+
+/* The same with each row quantized as nvfp4_quant_act would (no transform), read
+ * and quantized once per token, straight into nvfp4_grouped_gemm's operand:
+ *   x_fp4  out  nvfp4_packed_bytes(rows, h)
+ *   x_sf   out  nvfp4_scale_bytes(rows, h)
+ * Padding rows are not written: the grouped GEMM computes them, and their
+ * output is unspecified and read by nobody. */
+nvfp4_status nvfp4_moe_dispatch_quant(const void *x_bf16, int64_t ldx, const float *gs_dev, const int32_t *dest,
+                                      int64_t tokens, int topk, int64_t rows, int64_t h,
+                                      uint8_t *x_fp4, uint8_t *x_sf, nvfp4_stream_t stream);
+
+/* out[t] = bf16( sum_j weights[t, j] * y[dest[t, j]] + residual[t] ), summed in
+ * fp32 in the order of j; dropped assignments contribute nothing (their rows
+ * and weights are not read into the sum, whatever they hold).
+ *   y_bf16         in   [rows, ldy] bf16
+ *   weights        in   NULL (all 1) or fp32 [tokens, topk]
+ *   residual_bf16  in   NULL or [tokens, ldr] bf16
+ *   out_bf16       out  [tokens, ldo] bf16 */
+nvfp4_status nvfp4_moe_combine(const void *y_bf16, int64_t ldy, const float *weights, const int32_t *dest,
+                               int64_t tokens, int topk, int64_t rows, int64_t h, const void *residual_bf16,
+                               int64_t ldr, void *out_bf16, int64_t ldo, nvfp4_stream_t stream);
+
+/* Gradient of nvfp4_moe_combine with weights:
+ *   dy[dest[t, j]] = bf16( weights[t, j] * dout[t] ),
+ *   dweights[t, j] = sum_c dout[t, c] * y[dest[t, j], c]   (fp32; 0 if dropped)
+ * Padding rows of dy are set to zero and rows past the last group left alone,
+ * as in nvfp4_moe_dispatch.  (The residual's gradient is dout itself.) */
+nvfp4_status nvfp4_moe_combine_backward(const void *dout_bf16, int64_t ldd, const void *y_bf16, int64_t ldy,
+                                        const float *weights, const int32_t *dest, int64_t tokens, int topk,
+                                        int64_t rows, int64_t h, const int32_t *group_offsets,
+                                        const int32_t *group_counts, int experts, void *dy_bf16, int64_t lddy,
+                                        float *dweights, nvfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,6 +25,12 @@ __all__ = [
     "nvfp4_prepare_weight", "nvfp4_quant_act", "nvfp4_quant_act_export_y", "nvfp4_act_global_scale", "nvfp4_mxfp4_scale_bytes", "nvfp4_mxfp4_quant_act",
     "nvfp4_mxfp4_gemm", "nvfp4_mxfp4_linear_workspace_bytes", "nvfp4_mxfp4_linear", "mxfp4_linear",
     "nvfp4_gemm", "nvfp4_gemm_ex", "nvfp4_grouped_gemm", "nvfp4_linear", "nvfp4_linear_noalloc",
+    "nvfp4_gemm_act", "nvfp4_linear_act", "nvfp4_mxfp4_gemm_act", "nvfp4_mxfp4_linear_act", "nvfp4_grouped_gemm_act",
+    "nvfp4_mxfp8_bytes", "nvfp4_add_rmsnorm_quant", "nvfp4_moe_rows", "nvfp4_moe_sort_workspace_bytes",
+    "nvfp4_moe_sort", "nvfp4_moe_dispatch", "nvfp4_moe_dispatch_quant", "nvfp4_moe_combine",
+    "nvfp4_moe_combine_backward", "ACTIVATIONS", "NVFP4_FORMAT_NVFP4", "NVFP4_FORMAT_MXFP4", "NVFP4_FORMAT_MXFP8",
+    "interleave_gate_up", "add_rmsnorm_quant", "moe_sort", "moe_dispatch", "moe_dispatch_quant", "moe_combine",
+    "moe_combine_backward",
     "padded_k", "scale_shape", "quant_act", "quant_act_mx", "prepare_weight", "linear", "act_global_scale",
 ]
 
@@ -37,6 +43,11 @@ NVFP4_OK = 0
 STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_INVALID_ARG", 2: "NVFP4_ERR_UNSUPPORTED_DEVICE",
                 3: "NVFP4_ERR_ALIGNMENT", 4: "NVFP4_ERR_ALIAS", 5: "NVFP4_ERR_CUDA", 6: "NVFP4_ERR_TIMEOUT",
                 7: "NVFP4_ERR_WORKSPACE"}
+
+# Values of nvfp4_activation (gated ones halve the columns) and nvfp4_format.
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4, "geglu": 5}
+GATED_ACTIVATIONS = ("swiglu", "geglu")
+NVFP4_FORMAT_NVFP4, NVFP4_FORMAT_MXFP4, NVFP4_FORMAT_MXFP8 = 0, 1, 2
 
 # (name, restype, argtypes) of every exported symbol of include/nvfp4.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -65,6 +76,24 @@ EXPORTS = [
                             _P, _SZ, _P]),
     ("nvfp4_linear_noalloc", _I32, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _I64, _I64, _P, _P, _P, _I64,
                                     _P]),
+    ("nvfp4_gemm_act", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _I32, _P, _I64, _P, _I64, _P]),
+    ("nvfp4_linear_act", _I32, [_P, _I64, _I64, _I64, _P, _P, _I32, _P, _P, _I64, _I64, _P, _P, _I32, _P, _I64, _P,
+                                _I64, _P, _SZ, _P]),
+    ("nvfp4_mxfp4_gemm_act", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _I64, _P, _I64, _P]),
+    ("nvfp4_mxfp4_linear_act", _I32, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _I32, _P, _I64, _P, _I64, _P, _SZ,
+                                      _P]),
+    ("nvfp4_grouped_gemm_act", _I32, [_P, _P, _I64, _P, _I32, _P, _P, _I64, _I64, _P, _P, _I32, _P, _I64, _P]),
+    ("nvfp4_mxfp8_bytes", _SZ, [_I64, _I64]),
+    ("nvfp4_add_rmsnorm_quant", _I32, [_P, _I64, _P, _I64, _P, ctypes.c_float, _I64, _I64, _I32, _P, _P, _I64, _P, _P,
+                                       _P]),
+    ("nvfp4_moe_rows", _I64, [_I64, _I32, _I32]),
+    ("nvfp4_moe_sort_workspace_bytes", _SZ, [_I64, _I32, _I32]),
+    ("nvfp4_moe_sort", _I32, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    ("nvfp4_moe_dispatch", _I32, [_P, _I64, _P, _I64, _I32, _I64, _I64, _P, _P, _I32, _P, _I64, _P]),
+    ("nvfp4_moe_dispatch_quant", _I32, [_P, _I64, _P, _P, _I64, _I32, _I64, _I64, _P, _P, _P]),
+    ("nvfp4_moe_combine", _I32, [_P, _I64, _P, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _I64, _P]),
+    ("nvfp4_moe_combine_backward", _I32, [_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I64, _I64, _P, _P, _I32, _P, _I64,
+                                          _P, _P]),
 ]
 
 
@@ -257,6 +286,92 @@ def nvfp4_linear_noalloc(x, m: int, k: int, ldx: int, gs, transform, bs: int, w_
                                                _stream(stream)))
 
 
+def nvfp4_gemm_act(a_fp4, a_sf, m: int, w_fp4, w_sf, n_w: int, n_out: int, k: int, alpha, bias, act: int, residual,
+                   ldr: int, out, ldo: int, stream=None) -> None:
+    _check(load_library().nvfp4_gemm_act(_ptr(a_fp4), _ptr(a_sf), m, _ptr(w_fp4), _ptr(w_sf), n_w, n_out, k,
+                                         _ptr(alpha), _ptr(bias), act, _ptr(residual), ldr, _ptr(out), ldo,
+                                         _stream(stream)))
+
+
+def nvfp4_linear_act(x, m: int, k: int, ldx: int, gs, transform, bs: int, w_fp4, w_sf, n_w: int, n_out: int, alpha,
+                     bias, act: int, residual, ldr: int, out, ldo: int, workspace, workspace_bytes: int,
+                     stream=None) -> None:
+    _check(load_library().nvfp4_linear_act(_ptr(x), m, k, ldx, _ptr(gs), _ptr(transform), bs, _ptr(w_fp4), _ptr(w_sf),
+                                           n_w, n_out, _ptr(alpha), _ptr(bias), act, _ptr(residual), ldr, _ptr(out),
+                                           ldo, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def nvfp4_mxfp4_gemm_act(a_fp4, a_sf, m: int, w_fp4, w_sf, n_w: int, n_out: int, k: int, bias, act: int, residual,
+                         ldr: int, out, ldo: int, stream=None) -> None:
+    _check(load_library().nvfp4_mxfp4_gemm_act(_ptr(a_fp4), _ptr(a_sf), m, _ptr(w_fp4), _ptr(w_sf), n_w, n_out, k,
+                                               _ptr(bias), act, _ptr(residual), ldr, _ptr(out), ldo, _stream(stream)))
+
+
+def nvfp4_mxfp4_linear_act(x, m: int, k: int, ldx: int, w_fp4, w_sf, n_w: int, n_out: int, bias, act: int, residual,
+                           ldr: int, out, ldo: int, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().nvfp4_mxfp4_linear_act(_ptr(x), m, k, ldx, _ptr(w_fp4), _ptr(w_sf), n_w, n_out, _ptr(bias),
+                                                 act, _ptr(residual), ldr, _ptr(out), ldo, _ptr(workspace),
+                                                 workspace_bytes, _stream(stream)))
+
+
+def nvfp4_grouped_gemm_act(a_fp4, a_sf, rows: int, group_offsets, num_groups: int, w_fp4, w_sf, n: int, k: int, alpha,
+                           bias, act: int, out, ldo: int, stream=None) -> None:
+    _check(load_library().nvfp4_grouped_gemm_act(_ptr(a_fp4), _ptr(a_sf), rows, _ptr(group_offsets), num_groups,
+                                                 _ptr(w_fp4), _ptr(w_sf), n, k, _ptr(alpha), _ptr(bias), act,
+                                                 _ptr(out), ldo, _stream(stream)))
+
+
+def nvfp4_mxfp8_bytes(rows: int, k: int) -> int:
+    return load_library().nvfp4_mxfp8_bytes(rows, k)
+
+
+def nvfp4_add_rmsnorm_quant(x, ldx: int, residual, ldr: int, gamma, eps: float, m: int, k: int, fmt: int, gs, h,
+                            ldh: int, x_q, x_sf, stream=None) -> None:
+    _check(load_library().nvfp4_add_rmsnorm_quant(_ptr(x), ldx, _ptr(residual), ldr, _ptr(gamma), eps, m, k, fmt,
+                                                  _ptr(gs), _ptr(h), ldh, _ptr(x_q), _ptr(x_sf), _stream(stream)))
+
+
+def nvfp4_moe_rows(tokens: int, topk: int, experts: int) -> int:
+    return load_library().nvfp4_moe_rows(tokens, topk, experts)
+
+
+def nvfp4_moe_sort_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
+    return load_library().nvfp4_moe_sort_workspace_bytes(tokens, topk, experts)
+
+
+def nvfp4_moe_sort(expert_ids, id_bytes: int, tokens: int, topk: int, experts: int, group_offsets, group_counts, dest,
+                   workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().nvfp4_moe_sort(_ptr(expert_ids), id_bytes, tokens, topk, experts, _ptr(group_offsets),
+                                         _ptr(group_counts), _ptr(dest), _ptr(workspace), workspace_bytes,
+                                         _stream(stream)))
+
+
+def nvfp4_moe_dispatch(x, ldx: int, dest, tokens: int, topk: int, rows: int, h: int, group_offsets, group_counts,
+                       experts: int, out, ldo: int, stream=None) -> None:
+    _check(load_library().nvfp4_moe_dispatch(_ptr(x), ldx, _ptr(dest), tokens, topk, rows, h, _ptr(group_offsets),
+                                             _ptr(group_counts), experts, _ptr(out), ldo, _stream(stream)))
+
+
+def nvfp4_moe_dispatch_quant(x, ldx: int, gs, dest, tokens: int, topk: int, rows: int, h: int, x_fp4, x_sf,
+                             stream=None) -> None:
+    _check(load_library().nvfp4_moe_dispatch_quant(_ptr(x), ldx, _ptr(gs), _ptr(dest), tokens, topk, rows, h,
+                                                   _ptr(x_fp4), _ptr(x_sf), _stream(stream)))
+
+
+def nvfp4_moe_combine(y, ldy: int, weights, dest, tokens: int, topk: int, rows: int, h: int, residual, ldr: int, out,
+                      ldo: int, stream=None) -> None:
+    _check(load_library().nvfp4_moe_combine(_ptr(y), ldy, _ptr(weights), _ptr(dest), tokens, topk, rows, h,
+                                            _ptr(residual), ldr, _ptr(out), ldo, _stream(stream)))
+
+
+def nvfp4_moe_combine_backward(dout, ldd: int, y, ldy: int, weights, dest, tokens: int, topk: int, rows: int, h: int,
+                               group_offsets, group_counts, experts: int, dy, lddy: int, dweights,
+                               stream=None) -> None:
+    _check(load_library().nvfp4_moe_combine_backward(_ptr(dout), ldd, _ptr(y), ldy, _ptr(weights), _ptr(dest), tokens,
+                                                     topk, rows, h, _ptr(group_offsets), _ptr(group_counts), experts,
+                                                     _ptr(dy), lddy, _ptr(dweights), _stream(stream)))
+
+
 # --------------------------------------------- tensor-level conveniences ----
 # Thin helpers that allocate the caller-owned outputs with torch and call the
 # entry points above; they add no computation.
@@ -293,9 +408,11 @@ def quant_act_mx(x, stream=None):
     return x_fp4, x_sf
 
 
-def mxfp4_linear(x, w_fp4, w_sf, k: int, n_out: int, bias=None, out=None, workspace=None, stream=None):
+def mxfp4_linear(x, w_fp4, w_sf, k: int, n_out: int, bias=None, out=None, workspace=None, act: str = "none",
+                 residual=None, stream=None):
     """out[m, n_out] = MXFP4 linear of a [m, k] bf16 CUDA tensor against a weight
-    quantized by quant_act_mx (allocates out/workspace if not given)."""
+    quantized by quant_act_mx, with the epilogue of linear() (allocates
+    out/workspace if not given)."""
     import torch
     m = x.shape[0]
     n_w = w_fp4.shape[0]
@@ -304,8 +421,9 @@ def mxfp4_linear(x, w_fp4, w_sf, k: int, n_out: int, bias=None, out=None, worksp
     if workspace is None:
         workspace = torch.empty(max(nvfp4_mxfp4_linear_workspace_bytes(m, k, n_w), 1), dtype=torch.uint8,
                                 device=x.device)
-    nvfp4_mxfp4_linear(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, out, _ld(out, "out"), workspace,
-                       workspace.numel(), stream)
+    nvfp4_mxfp4_linear_act(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, ACTIVATIONS[act], residual,
+                           _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,
+                           workspace.numel(), stream)
     return out
 
 
@@ -320,8 +438,10 @@ def prepare_weight(w, w_gs, stream=None):
 
 
 def linear(x, w_fp4, w_sf, k: int, n_out: int, gs, alpha, bias=None, transform=None, bs: int = 0,
-           out=None, workspace=None, stream=None):
-    """out[m, n_out] = NVFP4 linear of a [m, k] bf16 CUDA tensor (allocates out/workspace if not given)."""
+           out=None, workspace=None, act: str = "none", residual=None, stream=None):
+    """out[m, n_out] = act(NVFP4 linear of a [m, k] bf16 CUDA tensor + bias) + residual
+    (allocates out/workspace if not given).  act is a key of ACTIVATIONS; the
+    gated ones take a weight of interleave_gate_up."""
     import torch
     m = x.shape[0]
     n_w = w_fp4.shape[0]
@@ -330,6 +450,97 @@ def linear(x, w_fp4, w_sf, k: int, n_out: int, gs, alpha, bias=None, transform=N
     need = nvfp4_linear_workspace_bytes(m, k, n_w)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
-    nvfp4_linear(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
-                 alpha, bias, out, _ld(out, "out"), workspace, workspace.numel(), stream)
+    nvfp4_linear_act(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
+                     alpha, bias, ACTIVATIONS[act], residual,
+                     _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,
+                     workspace.numel(), stream)
     return out
+
+
+def interleave_gate_up(gate, up):
+    """[2n, ...] with rows gate[0], up[0], gate[1], up[1], ...: the weight (or bias)
+    order of the gated activations."""
+    import torch
+    return torch.stack((gate, up), dim=1).reshape(2 * gate.shape[0], *gate.shape[1:])
+
+
+def add_rmsnorm_quant(x, gamma, eps: float, residual=None, gs=None, fmt: int = NVFP4_FORMAT_NVFP4, h=None,
+                      stream=None):
+    """Residual addition + RMS norm + quantization of a [m, k] bf16 CUDA tensor;
+    returns (x_q, flat x_sf, h).  h (the updated residual stream, None without a
+    residual) is allocated unless given; pass residual itself to update it in place."""
+    import torch
+    m, k = x.shape
+    cols = padded_k(k) if fmt == NVFP4_FORMAT_MXFP8 else padded_k(k) // 2
+    n_sf = nvfp4_scale_bytes(m, k) if fmt == NVFP4_FORMAT_NVFP4 else nvfp4_mxfp4_scale_bytes(m, k)
+    x_q = torch.empty((m, cols), dtype=torch.uint8, device=x.device)
+    x_sf = torch.empty(max(n_sf, 1), dtype=torch.uint8, device=x.device)
+    if h is None and residual is not None:
+        h = torch.empty((m, k), dtype=torch.bfloat16, device=x.device)
+    nvfp4_add_rmsnorm_quant(x, _ld(x, "x"), residual, _ld(residual, "residual") if residual is not None else 0, gamma,
+                            eps, m, k, fmt, gs, h, _ld(h, "h") if h is not None else 0, x_q, x_sf, stream)
+    return x_q, x_sf, h
+
+
+def moe_sort(expert_ids, experts: int, stream=None):
+    """Sort [tokens, topk] int32/int64 expert ids (contiguous, CUDA); returns
+    (group_offsets, group_counts, dest), int32."""
+    import torch
+    tokens, topk = expert_ids.shape
+    if not expert_ids.is_contiguous() or expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expert_ids must be a contiguous int32 or int64 tensor")
+    new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=expert_ids.device)  # noqa: E731
+    offsets, counts, dest = new(experts + 1), new(experts), new(tokens, topk)
+    ws = new(nvfp4_moe_sort_workspace_bytes(tokens, topk, experts), dtype=torch.uint8)
+    nvfp4_moe_sort(expert_ids, expert_ids.element_size(), tokens, topk, experts, offsets, counts, dest, ws, ws.numel(),
+                   stream)
+    return offsets, counts, dest
+
+
+def moe_dispatch(x, dest, group_offsets, group_counts, out=None, stream=None):
+    """Rows of a [tokens, h] bf16 CUDA tensor in the order of moe_sort, [nvfp4_moe_rows, h]."""
+    import torch
+    tokens, topk = dest.shape
+    experts, h = group_counts.numel(), x.shape[1]
+    if out is None:
+        out = torch.empty((nvfp4_moe_rows(tokens, topk, experts), h), dtype=torch.bfloat16, device=x.device)
+    nvfp4_moe_dispatch(x, _ld(x, "x"), dest, tokens, topk, out.shape[0], h, group_offsets, group_counts, experts, out,
+                       _ld(out, "out"), stream)
+    return out
+
+
+def moe_dispatch_quant(x, gs, dest, experts: int, stream=None):
+    """The same as the NVFP4 operand of nvfp4_grouped_gemm; returns (x_fp4, flat x_sf)."""
+    import torch
+    tokens, topk = dest.shape
+    h = x.shape[1]
+    rows = nvfp4_moe_rows(tokens, topk, experts)
+    x_fp4 = torch.empty((rows, padded_k(h) // 2), dtype=torch.uint8, device=x.device)
+    x_sf = torch.empty(max(nvfp4_scale_bytes(rows, h), 1), dtype=torch.uint8, device=x.device)
+    nvfp4_moe_dispatch_quant(x, _ld(x, "x"), gs, dest, tokens, topk, rows, h, x_fp4, x_sf, stream)
+    return x_fp4, x_sf
+
+
+def moe_combine(y, dest, weights=None, residual=None, out=None, stream=None):
+    """[tokens, h] bf16: each token's expert rows, weighted and summed, plus residual."""
+    import torch
+    tokens, topk = dest.shape
+    h = y.shape[1]
+    if out is None:
+        out = torch.empty((tokens, h), dtype=torch.bfloat16, device=y.device)
+    nvfp4_moe_combine(y, _ld(y, "y"), weights, dest, tokens, topk, y.shape[0], h, residual,
+                      _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), stream)
+    return out
+
+
+def moe_combine_backward(dout, y, weights, dest, group_offsets, group_counts, dy=None, stream=None):
+    """Gradients (dy [rows, h] bf16, dweights [tokens, topk] fp32) of moe_combine."""
+    import torch
+    tokens, topk = dest.shape
+    rows, h = y.shape
+    if dy is None:
+        dy = torch.empty((rows, h), dtype=torch.bfloat16, device=y.device)
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
+    nvfp4_moe_combine_backward(dout, _ld(dout, "dout"), y, _ld(y, "y"), weights, dest, tokens, topk, rows, h,
+                               group_offsets, group_counts, group_counts.numel(), dy, _ld(dy, "dy"), dweights, stream)
+    return dy, dweights

@@ -8,30 +8,15 @@
 #include <mutex>
 #include <string>
 
+#include "api_util.h"
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "quant_launch.cuh"
 #include "nvfp4.h"
 
 namespace {
 
 thread_local std::string g_last_error;
-
-nvfp4_status fail(nvfp4_status st, const char *fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
-
-nvfp4_status ok()
-{
-    g_last_error.clear();
-    return NVFP4_OK;
-}
 
 constexpr int kMaxDevices = 64;
 struct DeviceInfo {
@@ -68,6 +53,28 @@ const DeviceInfo *device_info(int dev)
     return &d;
 }
 
+}  // namespace
+
+namespace nvfp4 {
+namespace api {
+
+nvfp4_status fail(nvfp4_status st, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return st;
+}
+
+nvfp4_status ok()
+{
+    g_last_error.clear();
+    return NVFP4_OK;
+}
+
 nvfp4_status current_device(int *num_sms)
 {
     int dev = -1;
@@ -83,27 +90,7 @@ nvfp4_status current_device(int *num_sms)
     return NVFP4_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-    const char *name;
-};
-
-Range range(const void *p, size_t bytes, const char *name)
-{
-    uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, lo + bytes, name};
-}
-
-// Strided 2-D bf16 matrix: rows x cols elements, row stride ld elements.
-Range range2d(const void *p, int64_t rows, int64_t cols, int64_t ld, const char *name)
-{
-    size_t bytes = rows > 0 ? (size_t)((rows - 1) * ld + cols) * 2 : 0;
-    return range(p, bytes, name);
-}
-
-bool overlap(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
+static bool overlap(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi && a.hi > a.lo && b.hi > b.lo; }
 
 nvfp4_status check_aliases(const Range *outs, int n_out, const Range *ins, int n_in)
 {
@@ -118,7 +105,31 @@ nvfp4_status check_aliases(const Range *outs, int n_out, const Range *ins, int n
     return NVFP4_OK;
 }
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+nvfp4_status check_rows(const void *p, int64_t cols, int64_t ld, const char *name)
+{
+    if (p == nullptr) return fail(NVFP4_ERR_INVALID_ARG, "%s is null", name);
+    if (ld < cols)
+        return fail(NVFP4_ERR_INVALID_ARG, "row stride of %s (%lld) < its columns (%lld)", name, (long long)ld, (long long)cols);
+    if (!aligned16(p) || ld % 8 != 0)
+        return fail(NVFP4_ERR_ALIGNMENT, "%s rows must start on 16-byte boundaries (pointer and ld %% 8 == 0)", name);
+    return NVFP4_OK;
+}
+
+nvfp4_status launch_status(cudaError_t e, const char *what)
+{
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(NVFP4_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
+    }
+    return ok();
+}
+
+}  // namespace api
+}  // namespace nvfp4
+
+using namespace nvfp4::api;
+
+namespace {
 
 nvfp4_status check_quant_args(const void *x, int64_t m, int64_t k, int64_t ldx, const float *gs, const void *t,
                               int bs, const uint8_t *x_fp4, const uint8_t *x_sf, const char *xname)
@@ -166,15 +177,6 @@ nvfp4::QuantParams quant_params(const void *x, int64_t m, int64_t k, int64_t ldx
     return p;
 }
 
-nvfp4_status launch_status(cudaError_t e, const char *what)
-{
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return fail(NVFP4_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString(e));
-    }
-    return ok();
-}
-
 nvfp4_status run_quant(nvfp4::QuantParams p, int num_sms, cudaStream_t s)
 {
     if (p.bs) {
@@ -188,13 +190,28 @@ nvfp4_status run_quant(nvfp4::QuantParams p, int num_sms, cudaStream_t s)
     return launch_status(nvfp4::launch_quant(p, num_sms, s), "quantize kernel");
 }
 
+// The epilogue after alpha and bias: an nvfp4_activation and a residual
+// [m, ldr] (or null).
+struct Epilogue {
+    int act = nvfp4::kActNone;
+    const void *residual = nullptr;
+    int64_t ldr = 0;
+    // accumulator columns of n output columns
+    int64_t acc_cols(int64_t n) const { return nvfp4::act_gated(act) ? 2 * n : n; }
+};
+
 nvfp4_status check_gemm_args(const uint8_t *a, const uint8_t *a_sf, int64_t m, const uint8_t *w, const uint8_t *w_sf,
                              int64_t n_w, int64_t n_out, int64_t k, const float *alpha, const void *bias, void *out,
-                             int64_t ldo)
+                             int64_t ldo, const Epilogue &epi = {})
 {
+    if (epi.act < nvfp4::kActNone || epi.act > nvfp4::kActGeglu)
+        return fail(NVFP4_ERR_INVALID_ARG, "unknown activation %d", epi.act);
     if (m < 0 || m > kMaxDim) return fail(NVFP4_ERR_INVALID_ARG, "m out of range: %lld", (long long)m);
     if (k < 1 || k > kMaxDim) return fail(NVFP4_ERR_INVALID_ARG, "k out of range: %lld", (long long)k);
     if (n_w < 1 || n_w > kMaxDim) return fail(NVFP4_ERR_INVALID_ARG, "n_w out of range: %lld", (long long)n_w);
+    if (nvfp4::act_gated(epi.act) && (n_out < 1 || 2 * n_out > n_w))
+        return fail(NVFP4_ERR_INVALID_ARG, "a gated activation needs 1 <= n_out <= n_w / 2 (got %lld, n_w %lld)",
+                    (long long)n_out, (long long)n_w);
     if (n_out < 1 || n_out > n_w)
         return fail(NVFP4_ERR_INVALID_ARG, "n_out must satisfy 1 <= n_out <= n_w (got %lld, n_w %lld)", (long long)n_out, (long long)n_w);
     if (ldo < n_out) return fail(NVFP4_ERR_INVALID_ARG, "ldo (%lld) < n_out (%lld)", (long long)ldo, (long long)n_out);
@@ -208,6 +225,7 @@ nvfp4_status check_gemm_args(const uint8_t *a, const uint8_t *a_sf, int64_t m, c
         if (!a || !a_sf) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
         if (!aligned16(a) || !aligned16(a_sf)) return fail(NVFP4_ERR_ALIGNMENT, "activation buffers must be 16-byte aligned");
     }
+    if (epi.residual != nullptr) return check_rows(epi.residual, n_out, epi.ldr, "residual");
     return NVFP4_OK;
 }
 
@@ -220,19 +238,23 @@ int64_t scale_cols_of(int64_t k, bool mx)
 
 nvfp4::GemmParams gemm_params(const uint8_t *a_sf, int64_t m, const uint8_t *w_sf, int64_t n_w, int64_t n_out,
                               int64_t k, const float *alpha, const void *bias, void *out, int64_t ldo,
-                              unsigned int *err, bool mx = false)
+                              unsigned int *err, bool mx = false, const Epilogue &epi = {})
 {
     nvfp4::GemmParams g;
     g.m = (int32_t)m;
     g.n_w = (int32_t)n_w;
-    g.n_out = (int32_t)n_out;
+    g.n_out = (int32_t)epi.acc_cols(n_out);
+    g.out_cols = (int32_t)n_out;
+    g.act = epi.act;
+    g.residual = static_cast<const uint16_t *>(epi.residual);
+    g.ldr = epi.ldr;
     g.kp = (int32_t)nvfp4::padded_k(k);
     const int64_t nbp = scale_cols_of(k, mx);
     g.num_k64 = (int32_t)((g.kp + 63) / 64);
     g.sf_tiles = (int32_t)(nbp / 4);
     g.mx = mx ? 1 : 0;
     g.num_m_blk = (int32_t)((m + 127) / 128);
-    g.num_n_blk = (int32_t)((n_out + 255) / 256);
+    g.num_n_blk = (g.n_out + 255) / 256;
     g.sfa = a_sf;
     g.sfb = w_sf;
     g.sfa_band_bytes = 128 * nbp;
@@ -305,12 +327,12 @@ nvfp4_status run_gemm(const uint8_t *a, const uint8_t *a_sf, int64_t m, const ui
                       int64_t n_w, int64_t n_out, int64_t k, const float *alpha, const void *bias, void *out,
                       int64_t ldo, int num_sms, cudaStream_t s, bool allow_split = false,
                       bool after_quant = false, int kernel = kGemmAuto, uint64_t wait_ns = 0, int drill = 0,
-                      bool mx = false, const nvfp4::QuantParams *fuse_quant = nullptr)
+                      bool mx = false, const nvfp4::QuantParams *fuse_quant = nullptr, const Epilogue &epi = {})
 {
     unsigned int *err = nullptr;
     cudaError_t e = nvfp4::device_error_word(&err);
     if (e != cudaSuccess) return launch_status(e, "GEMM (error word)");
-    nvfp4::GemmParams g = gemm_params(a_sf, m, w_sf, n_w, n_out, k, alpha, bias, out, ldo, err, mx);
+    nvfp4::GemmParams g = gemm_params(a_sf, m, w_sf, n_w, n_out, k, alpha, bias, out, ldo, err, mx, epi);
     if (wait_ns != 0) g.wait_ns = wait_ns;
     g.drill = drill;
     if (allow_split && !(kernel == kGemmPair || (kernel == kGemmAuto && m > 128))) {
@@ -356,6 +378,192 @@ int nvfp4::record_error(int st, const char *msg)
     g_last_error = msg;
     return st;
 }
+
+namespace {
+
+// nvfp4_gemm, nvfp4_gemm_ex and nvfp4_gemm_act.
+nvfp4_status gemm_impl(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m, const uint8_t *w_fp4, const uint8_t *w_sf,
+                       int64_t n_w, int64_t n_out, int64_t k, const float *alpha_dev, const void *bias_bf16,
+                       void *out_bf16, int64_t ldo, int kernel, uint64_t wait_limit_ns, int drill,
+                       const Epilogue &epi, nvfp4_stream_t stream)
+{
+    nvfp4_status st = check_gemm_args(m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, m, w_fp4, w_sf, n_w, n_out, k,
+                                      alpha_dev, bias_bf16, out_bf16, ldo, epi);
+    if (st != NVFP4_OK) return st;
+    if (m == 0) return ok();
+    if (!a_fp4 || !a_sf || !alpha_dev) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+    Range outs[1] = {range2d(out_bf16, m, n_out, ldo, "out")};
+    Range ins[7] = {range(a_fp4, nvfp4_packed_bytes(m, k), "a_fp4"), range(a_sf, nvfp4_scale_bytes(m, k), "a_sf"),
+                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"), range(w_sf, nvfp4_scale_bytes(n_w, k), "w_sf"),
+                    range(alpha_dev, 4, "alpha"), range(bias_bf16, bias_bf16 ? (size_t)epi.acc_cols(n_out) * 2 : 0, "bias"),
+                    range2d(epi.residual, m, n_out, epi.ldr, "residual")};
+    if ((st = check_aliases(outs, 1, ins, 7)) != NVFP4_OK) return st;
+    int num_sms = 0;
+    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
+    // kernel 3: the one-CTA kernel with the linear's split-K plan (test hook)
+    const bool split = kernel == kGemmOneCtaSplit;
+    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms,
+                    reinterpret_cast<cudaStream_t>(stream), split, false, split ? (int)kGemmOneCta : kernel,
+                    wait_limit_ns, drill, false, nullptr, epi);
+}
+
+// nvfp4_linear and nvfp4_linear_act.
+nvfp4_status linear_impl(const void *x_bf16, int64_t m, int64_t k, int64_t ldx, const float *gs_dev,
+                         const void *transform_bf16, int bs, const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n_w,
+                         int64_t n_out, const float *alpha_dev, const void *bias_bf16, const Epilogue &epi,
+                         void *out_bf16, int64_t ldo, void *workspace, size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t need = nvfp4::linear_min_workspace_bytes(m, k);   // quantized activation + scales
+    uint8_t *a_fp4 = ws;
+    uint8_t *a_sf = ws ? ws + align256(nvfp4_packed_bytes(m, k)) : nullptr;
+    nvfp4_status st = check_quant_args(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, m > 0 ? a_fp4 : nullptr,
+                                       m > 0 ? a_sf : nullptr, "x");
+    if (st == NVFP4_ERR_INVALID_ARG && m > 0 && workspace == nullptr)
+        return fail(NVFP4_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+    if (st != NVFP4_OK) return st;
+    st = check_gemm_args(nullptr, nullptr, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, epi);
+    if (st != NVFP4_OK) return st;
+    if (m == 0) return ok();
+    if (!alpha_dev) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+    if (workspace_bytes < need)
+        return fail(NVFP4_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    Range outs[2] = {range2d(out_bf16, m, n_out, ldo, "out"), range(workspace, workspace_bytes, "workspace")};
+    Range ins[8] = {range2d(x_bf16, m, k, ldx, "x"), range(gs_dev, 4, "gs"),
+                    range(transform_bf16, transform_bf16 ? (size_t)bs * bs * 2 : 0, "transform"),
+                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"), range(w_sf, nvfp4_scale_bytes(n_w, k), "w_sf"),
+                    range(alpha_dev, 4, "alpha"), range(bias_bf16, bias_bf16 ? (size_t)epi.acc_cols(n_out) * 2 : 0, "bias"),
+                    range2d(epi.residual, m, n_out, epi.ldr, "residual")};
+    if ((st = check_aliases(outs, 2, ins, 8)) != NVFP4_OK) return st;
+    int num_sms = 0;
+    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const nvfp4::QuantParams qp = quant_params(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, a_fp4, a_sf);
+    // Decode sizes: the GEMM quantizes its own activation (its eight epilogue
+    // warps, each K stage as its slice lands, one 16-element block per lane).
+    if (m <= kFusedLinearMaxRows && transform_bf16 == nullptr)
+        return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms,
+                        s, true, false, kGemmAuto, 0, 0, false, &qp, epi);
+    st = run_quant(qp, num_sms, s);
+    if (st != NVFP4_OK) return st;
+    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms, s,
+                    true, true, kGemmAuto, 0, 0, false, nullptr, epi);
+}
+
+// nvfp4_mxfp4_gemm and nvfp4_mxfp4_gemm_act.
+nvfp4_status mxfp4_gemm_impl(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m, const uint8_t *w_fp4,
+                             const uint8_t *w_sf, int64_t n_w, int64_t n_out, int64_t k, const void *bias_bf16,
+                             const Epilogue &epi, void *out_bf16, int64_t ldo, nvfp4_stream_t stream)
+{
+    nvfp4_status st = check_gemm_args(m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, m, w_fp4, w_sf, n_w, n_out, k,
+                                      nullptr, bias_bf16, out_bf16, ldo, epi);
+    if (st != NVFP4_OK) return st;
+    if (m == 0) return ok();
+    if (!a_fp4 || !a_sf) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+    Range outs[1] = {range2d(out_bf16, m, n_out, ldo, "out")};
+    Range ins[6] = {range(a_fp4, nvfp4_packed_bytes(m, k), "a_fp4"), range(a_sf, nvfp4_mxfp4_scale_bytes(m, k), "a_sf"),
+                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"),
+                    range(w_sf, nvfp4_mxfp4_scale_bytes(n_w, k), "w_sf"),
+                    range(bias_bf16, bias_bf16 ? (size_t)epi.acc_cols(n_out) * 2 : 0, "bias"),
+                    range2d(epi.residual, m, n_out, epi.ldr, "residual")};
+    if ((st = check_aliases(outs, 1, ins, 6)) != NVFP4_OK) return st;
+    int num_sms = 0;
+    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
+    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms,
+                    reinterpret_cast<cudaStream_t>(stream), false, false, kGemmAuto, 0, 0, true, nullptr, epi);
+}
+
+// nvfp4_mxfp4_linear and nvfp4_mxfp4_linear_act.
+nvfp4_status mxfp4_linear_impl(const void *x_bf16, int64_t m, int64_t k, int64_t ldx, const uint8_t *w_fp4,
+                               const uint8_t *w_sf, int64_t n_w, int64_t n_out, const void *bias_bf16,
+                               const Epilogue &epi, void *out_bf16, int64_t ldo, void *workspace,
+                               size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t need = mx_min_workspace_bytes(m, k);           // MXFP4 activation + scales
+    uint8_t *a_fp4 = ws;
+    uint8_t *a_sf = ws ? ws + align256(nvfp4_packed_bytes(m, k)) : nullptr;
+    // the quantizer's checks, with a_sf standing in for the (absent) global scale
+    nvfp4_status st = check_quant_args(x_bf16, m, k, ldx, reinterpret_cast<const float *>(a_sf), nullptr, 0,
+                                       m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, "x");
+    if (st == NVFP4_ERR_INVALID_ARG && m > 0 && workspace == nullptr)
+        return fail(NVFP4_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+    if (st != NVFP4_OK) return st;
+    st = check_gemm_args(nullptr, nullptr, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, epi);
+    if (st != NVFP4_OK) return st;
+    if (m == 0) return ok();
+    if (workspace_bytes < need)
+        return fail(NVFP4_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
+    Range outs[2] = {range2d(out_bf16, m, n_out, ldo, "out"), range(workspace, workspace_bytes, "workspace")};
+    Range ins[5] = {range2d(x_bf16, m, k, ldx, "x"), range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"),
+                    range(w_sf, nvfp4_mxfp4_scale_bytes(n_w, k), "w_sf"),
+                    range(bias_bf16, bias_bf16 ? (size_t)epi.acc_cols(n_out) * 2 : 0, "bias"),
+                    range2d(epi.residual, m, n_out, epi.ldr, "residual")};
+    if ((st = check_aliases(outs, 2, ins, 5)) != NVFP4_OK) return st;
+    int num_sms = 0;
+    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    nvfp4::QuantParams p = quant_params(x_bf16, m, k, ldx, nullptr, nullptr, 0, a_fp4, a_sf);
+    p.nb = (int32_t)(nvfp4::padded_k(k) / 32);
+    p.nbp = (p.nb + 3) / 4 * 4;
+    // decode sizes: the GEMM quantizes its own activation, as nvfp4_linear's fused path
+    if (m <= kFusedLinearMaxRows)
+        return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms, s,
+                        true, false, kGemmAuto, 0, 0, true, &p, epi);
+    st = launch_status(nvfp4::launch_quant_mx(p, num_sms, s), "MXFP4 quantize kernel");
+    if (st != NVFP4_OK) return st;
+    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms, s,
+                    true, true, kGemmAuto, 0, 0, true, nullptr, epi);
+}
+
+// nvfp4_grouped_gemm and nvfp4_grouped_gemm_act.
+nvfp4_status grouped_gemm_impl(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,
+                               const int32_t *group_offsets_dev, int num_groups, const uint8_t *w_fp4,
+                               const uint8_t *w_sf, int64_t n, int64_t k, const float *alpha_dev,
+                               const void *bias_bf16, int act, void *out_bf16, int64_t ldo, nvfp4_stream_t stream)
+{
+    if (num_groups < 1 || num_groups > (1 << 16))
+        return fail(NVFP4_ERR_INVALID_ARG, "num_groups must be in [1, 65536] (got %d)", num_groups);
+    const Epilogue epi = {act, nullptr, 0};
+    const int64_t n_acc = epi.acc_cols(n);                      // weight rows of a group
+    if (n < 1 || n > kMaxDim || n_acc % 128 != 0 || n_acc * num_groups > kMaxDim)
+        return fail(NVFP4_ERR_INVALID_ARG,
+                    "a group's weight rows must be a positive multiple of 128 with num_groups times them < 2^31 "
+                    "(got n = %lld, %lld rows)",
+                    (long long)n, (long long)n_acc);
+    nvfp4_status st = check_gemm_args(rows > 0 ? a_fp4 : nullptr, rows > 0 ? a_sf : nullptr, rows, w_fp4, w_sf,
+                                      n_acc * num_groups, n, k, alpha_dev, bias_bf16, out_bf16, ldo, epi);
+    if (st != NVFP4_OK) return st;
+    if (rows == 0) return ok();
+    if (!a_fp4 || !a_sf || !alpha_dev || !group_offsets_dev)
+        return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
+    if ((reinterpret_cast<uintptr_t>(group_offsets_dev) & 3) || (reinterpret_cast<uintptr_t>(alpha_dev) & 3))
+        return fail(NVFP4_ERR_ALIGNMENT, "group offsets and alphas must be 4-byte aligned");
+    const int64_t wrows = n_acc * num_groups;
+    Range outs[1] = {range2d(out_bf16, rows, n, ldo, "out")};
+    Range ins[7] = {range(a_fp4, nvfp4_packed_bytes(rows, k), "a_fp4"), range(a_sf, nvfp4_scale_bytes(rows, k), "a_sf"),
+                    range(w_fp4, nvfp4_packed_bytes(wrows, k), "w_fp4"),
+                    range(w_sf, nvfp4_scale_bytes(wrows, k), "w_sf"),
+                    range(alpha_dev, (size_t)num_groups * 4, "alpha"),
+                    range(bias_bf16, bias_bf16 ? (size_t)wrows * 2 : 0, "bias"),
+                    range(group_offsets_dev, (size_t)(num_groups + 1) * 4, "group_offsets")};
+    if ((st = check_aliases(outs, 1, ins, 7)) != NVFP4_OK) return st;
+    int num_sms = 0;
+    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
+    unsigned int *err = nullptr;
+    cudaError_t e = nvfp4::device_error_word(&err);
+    if (e != cudaSuccess) return launch_status(e, "grouped GEMM (error word)");
+    nvfp4::GemmParams g = gemm_params(a_sf, rows, w_sf, wrows, n, k, alpha_dev, bias_bf16, out_bf16, ldo, err, false, epi);
+    g.group_offsets = group_offsets_dev;
+    g.num_groups = num_groups;
+    g.group_n = (int32_t)n_acc;
+    const char *why = nullptr;
+    e = nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, reinterpret_cast<cudaStream_t>(stream), &why, false);
+    if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
+    return launch_status(e, "grouped GEMM kernel");
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -544,23 +752,8 @@ nvfp4_status nvfp4_gemm_ex(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m,
         return fail(NVFP4_ERR_INVALID_ARG, "wait_limit_ns must be 0 or within [1e6, 1e10] (got %llu)",
                     (unsigned long long)wait_limit_ns);
     if (drill != 0 && drill != 1) return fail(NVFP4_ERR_INVALID_ARG, "drill must be 0 or 1 (got %d)", drill);
-    nvfp4_status st = check_gemm_args(m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, m, w_fp4, w_sf, n_w, n_out, k,
-                                      alpha_dev, bias_bf16, out_bf16, ldo);
-    if (st != NVFP4_OK) return st;
-    if (m == 0) return ok();
-    if (!a_fp4 || !a_sf || !alpha_dev) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
-    Range outs[1] = {range2d(out_bf16, m, n_out, ldo, "out")};
-    Range ins[6] = {range(a_fp4, nvfp4_packed_bytes(m, k), "a_fp4"), range(a_sf, nvfp4_scale_bytes(m, k), "a_sf"),
-                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"), range(w_sf, nvfp4_scale_bytes(n_w, k), "w_sf"),
-                    range(alpha_dev, 4, "alpha"), range(bias_bf16, bias_bf16 ? (size_t)n_out * 2 : 0, "bias")};
-    if ((st = check_aliases(outs, 1, ins, 6)) != NVFP4_OK) return st;
-    int num_sms = 0;
-    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
-    // kernel 3: the one-CTA kernel with the linear's split-K plan (test hook)
-    const bool split = kernel == kGemmOneCtaSplit;
-    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms,
-                    reinterpret_cast<cudaStream_t>(stream), split, false, split ? (int)kGemmOneCta : kernel,
-                    wait_limit_ns, drill);
+    return gemm_impl(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, kernel,
+                     wait_limit_ns, drill, {}, stream);
 }
 
 nvfp4_status nvfp4_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m, const uint8_t *w_fp4,
@@ -576,40 +769,27 @@ nvfp4_status nvfp4_linear(const void *x_bf16, int64_t m, int64_t k, int64_t ldx,
                           int64_t n_out, const float *alpha_dev, const void *bias_bf16, void *out_bf16, int64_t ldo,
                           void *workspace, size_t workspace_bytes, nvfp4_stream_t stream)
 {
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t need = nvfp4::linear_min_workspace_bytes(m, k);   // quantized activation + scales
-    uint8_t *a_fp4 = ws;
-    uint8_t *a_sf = ws ? ws + align256(nvfp4_packed_bytes(m, k)) : nullptr;
-    nvfp4_status st = check_quant_args(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, m > 0 ? a_fp4 : nullptr,
-                                       m > 0 ? a_sf : nullptr, "x");
-    if (st == NVFP4_ERR_INVALID_ARG && m > 0 && workspace == nullptr)
-        return fail(NVFP4_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
-    if (st != NVFP4_OK) return st;
-    st = check_gemm_args(nullptr, nullptr, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo);
-    if (st != NVFP4_OK) return st;
-    if (m == 0) return ok();
-    if (!alpha_dev) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
-    if (workspace_bytes < need)
-        return fail(NVFP4_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
-    Range outs[2] = {range2d(out_bf16, m, n_out, ldo, "out"), range(workspace, workspace_bytes, "workspace")};
-    Range ins[7] = {range2d(x_bf16, m, k, ldx, "x"), range(gs_dev, 4, "gs"),
-                    range(transform_bf16, transform_bf16 ? (size_t)bs * bs * 2 : 0, "transform"),
-                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"), range(w_sf, nvfp4_scale_bytes(n_w, k), "w_sf"),
-                    range(alpha_dev, 4, "alpha"), range(bias_bf16, bias_bf16 ? (size_t)n_out * 2 : 0, "bias")};
-    if ((st = check_aliases(outs, 2, ins, 7)) != NVFP4_OK) return st;
-    int num_sms = 0;
-    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const nvfp4::QuantParams qp = quant_params(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, a_fp4, a_sf);
-    // Decode sizes: the GEMM quantizes its own activation (its eight epilogue
-    // warps, each K stage as its slice lands, one 16-element block per lane).
-    if (m <= kFusedLinearMaxRows && transform_bf16 == nullptr)
-        return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms,
-                        s, true, false, kGemmAuto, 0, 0, false, &qp);
-    st = run_quant(qp, num_sms, s);
-    if (st != NVFP4_OK) return st;
-    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, num_sms, s,
-                    true, true);
+    return linear_impl(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, w_fp4, w_sf, n_w, n_out, alpha_dev, bias_bf16, {},
+                       out_bf16, ldo, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_linear_act(const void *x_bf16, int64_t m, int64_t k, int64_t ldx, const float *gs_dev,
+                              const void *transform_bf16, int bs, const uint8_t *w_fp4, const uint8_t *w_sf,
+                              int64_t n_w, int64_t n_out, const float *alpha_dev, const void *bias_bf16, int act,
+                              const void *residual_bf16, int64_t ldr, void *out_bf16, int64_t ldo, void *workspace,
+                              size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    return linear_impl(x_bf16, m, k, ldx, gs_dev, transform_bf16, bs, w_fp4, w_sf, n_w, n_out, alpha_dev, bias_bf16,
+                       {act, residual_bf16, ldr}, out_bf16, ldo, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m, const uint8_t *w_fp4,
+                            const uint8_t *w_sf, int64_t n_w, int64_t n_out, int64_t k, const float *alpha_dev,
+                            const void *bias_bf16, int act, const void *residual_bf16, int64_t ldr, void *out_bf16,
+                            int64_t ldo, nvfp4_stream_t stream)
+{
+    return gemm_impl(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, alpha_dev, bias_bf16, out_bf16, ldo, kGemmAuto, 0, 0,
+                     {act, residual_bf16, ldr}, stream);
 }
 
 size_t nvfp4_mxfp4_linear_workspace_bytes(int64_t m, int64_t k, int64_t n_w)
@@ -623,21 +803,16 @@ nvfp4_status nvfp4_mxfp4_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t
                               const uint8_t *w_sf, int64_t n_w, int64_t n_out, int64_t k, const void *bias_bf16,
                               void *out_bf16, int64_t ldo, nvfp4_stream_t stream)
 {
-    nvfp4_status st = check_gemm_args(m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, m, w_fp4, w_sf, n_w, n_out, k,
-                                      nullptr, bias_bf16, out_bf16, ldo);
-    if (st != NVFP4_OK) return st;
-    if (m == 0) return ok();
-    if (!a_fp4 || !a_sf) return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
-    Range outs[1] = {range2d(out_bf16, m, n_out, ldo, "out")};
-    Range ins[5] = {range(a_fp4, nvfp4_packed_bytes(m, k), "a_fp4"), range(a_sf, nvfp4_mxfp4_scale_bytes(m, k), "a_sf"),
-                    range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"),
-                    range(w_sf, nvfp4_mxfp4_scale_bytes(n_w, k), "w_sf"),
-                    range(bias_bf16, bias_bf16 ? (size_t)n_out * 2 : 0, "bias")};
-    if ((st = check_aliases(outs, 1, ins, 5)) != NVFP4_OK) return st;
-    int num_sms = 0;
-    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
-    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms,
-                    reinterpret_cast<cudaStream_t>(stream), false, false, kGemmAuto, 0, 0, true);
+    return mxfp4_gemm_impl(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, bias_bf16, {}, out_bf16, ldo, stream);
+}
+
+nvfp4_status nvfp4_mxfp4_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m, const uint8_t *w_fp4,
+                                  const uint8_t *w_sf, int64_t n_w, int64_t n_out, int64_t k, const void *bias_bf16,
+                                  int act, const void *residual_bf16, int64_t ldr, void *out_bf16, int64_t ldo,
+                                  nvfp4_stream_t stream)
+{
+    return mxfp4_gemm_impl(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, bias_bf16, {act, residual_bf16, ldr}, out_bf16,
+                           ldo, stream);
 }
 
 nvfp4_status nvfp4_mxfp4_linear(const void *x_bf16, int64_t m, int64_t k, int64_t ldx, const uint8_t *w_fp4,
@@ -645,40 +820,17 @@ nvfp4_status nvfp4_mxfp4_linear(const void *x_bf16, int64_t m, int64_t k, int64_
                                 void *out_bf16, int64_t ldo, void *workspace, size_t workspace_bytes,
                                 nvfp4_stream_t stream)
 {
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t need = mx_min_workspace_bytes(m, k);           // MXFP4 activation + scales
-    uint8_t *a_fp4 = ws;
-    uint8_t *a_sf = ws ? ws + align256(nvfp4_packed_bytes(m, k)) : nullptr;
-    // the quantizer's checks, with a_sf standing in for the (absent) global scale
-    nvfp4_status st = check_quant_args(x_bf16, m, k, ldx, reinterpret_cast<const float *>(a_sf), nullptr, 0,
-                                       m > 0 ? a_fp4 : nullptr, m > 0 ? a_sf : nullptr, "x");
-    if (st == NVFP4_ERR_INVALID_ARG && m > 0 && workspace == nullptr)
-        return fail(NVFP4_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
-    if (st != NVFP4_OK) return st;
-    st = check_gemm_args(nullptr, nullptr, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo);
-    if (st != NVFP4_OK) return st;
-    if (m == 0) return ok();
-    if (workspace_bytes < need)
-        return fail(NVFP4_ERR_WORKSPACE, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, need);
-    Range outs[2] = {range2d(out_bf16, m, n_out, ldo, "out"), range(workspace, workspace_bytes, "workspace")};
-    Range ins[4] = {range2d(x_bf16, m, k, ldx, "x"), range(w_fp4, nvfp4_packed_bytes(n_w, k), "w_fp4"),
-                    range(w_sf, nvfp4_mxfp4_scale_bytes(n_w, k), "w_sf"),
-                    range(bias_bf16, bias_bf16 ? (size_t)n_out * 2 : 0, "bias")};
-    if ((st = check_aliases(outs, 2, ins, 4)) != NVFP4_OK) return st;
-    int num_sms = 0;
-    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    nvfp4::QuantParams p = quant_params(x_bf16, m, k, ldx, nullptr, nullptr, 0, a_fp4, a_sf);
-    p.nb = (int32_t)(nvfp4::padded_k(k) / 32);
-    p.nbp = (p.nb + 3) / 4 * 4;
-    // decode sizes: the GEMM quantizes its own activation, as nvfp4_linear's fused path
-    if (m <= kFusedLinearMaxRows)
-        return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms, s,
-                        true, false, kGemmAuto, 0, 0, true, &p);
-    st = launch_status(nvfp4::launch_quant_mx(p, num_sms, s), "MXFP4 quantize kernel");
-    if (st != NVFP4_OK) return st;
-    return run_gemm(a_fp4, a_sf, m, w_fp4, w_sf, n_w, n_out, k, nullptr, bias_bf16, out_bf16, ldo, num_sms, s,
-                    true, true, kGemmAuto, 0, 0, true);
+    return mxfp4_linear_impl(x_bf16, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias_bf16, {}, out_bf16, ldo, workspace,
+                             workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_mxfp4_linear_act(const void *x_bf16, int64_t m, int64_t k, int64_t ldx, const uint8_t *w_fp4,
+                                    const uint8_t *w_sf, int64_t n_w, int64_t n_out, const void *bias_bf16, int act,
+                                    const void *residual_bf16, int64_t ldr, void *out_bf16, int64_t ldo,
+                                    void *workspace, size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    return mxfp4_linear_impl(x_bf16, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias_bf16, {act, residual_bf16, ldr}, out_bf16,
+                             ldo, workspace, workspace_bytes, stream);
 }
 
 nvfp4_status nvfp4_grouped_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,
@@ -686,41 +838,17 @@ nvfp4_status nvfp4_grouped_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64
                                 const uint8_t *w_sf, int64_t n, int64_t k, const float *alpha_dev,
                                 const void *bias_bf16, void *out_bf16, int64_t ldo, nvfp4_stream_t stream)
 {
-    if (num_groups < 1 || num_groups > (1 << 16))
-        return fail(NVFP4_ERR_INVALID_ARG, "num_groups must be in [1, 65536] (got %d)", num_groups);
-    if (n < 128 || n % 128 != 0 || n * (int64_t)num_groups > kMaxDim)
-        return fail(NVFP4_ERR_INVALID_ARG, "n must be a positive multiple of 128 with num_groups * n < 2^31 (got %lld)",
-                    (long long)n);
-    nvfp4_status st = check_gemm_args(rows > 0 ? a_fp4 : nullptr, rows > 0 ? a_sf : nullptr, rows, w_fp4, w_sf,
-                                      n * num_groups, n, k, alpha_dev, bias_bf16, out_bf16, ldo);
-    if (st != NVFP4_OK) return st;
-    if (rows == 0) return ok();
-    if (!a_fp4 || !a_sf || !alpha_dev || !group_offsets_dev)
-        return fail(NVFP4_ERR_INVALID_ARG, "null pointer argument");
-    if ((reinterpret_cast<uintptr_t>(group_offsets_dev) & 3) || (reinterpret_cast<uintptr_t>(alpha_dev) & 3))
-        return fail(NVFP4_ERR_ALIGNMENT, "group offsets and alphas must be 4-byte aligned");
-    const int64_t wrows = n * num_groups;
-    Range outs[1] = {range2d(out_bf16, rows, n, ldo, "out")};
-    Range ins[7] = {range(a_fp4, nvfp4_packed_bytes(rows, k), "a_fp4"), range(a_sf, nvfp4_scale_bytes(rows, k), "a_sf"),
-                    range(w_fp4, nvfp4_packed_bytes(wrows, k), "w_fp4"),
-                    range(w_sf, nvfp4_scale_bytes(wrows, k), "w_sf"),
-                    range(alpha_dev, (size_t)num_groups * 4, "alpha"),
-                    range(bias_bf16, bias_bf16 ? (size_t)wrows * 2 : 0, "bias"),
-                    range(group_offsets_dev, (size_t)(num_groups + 1) * 4, "group_offsets")};
-    if ((st = check_aliases(outs, 1, ins, 7)) != NVFP4_OK) return st;
-    int num_sms = 0;
-    if ((st = current_device(&num_sms)) != NVFP4_OK) return st;
-    unsigned int *err = nullptr;
-    cudaError_t e = nvfp4::device_error_word(&err);
-    if (e != cudaSuccess) return launch_status(e, "grouped GEMM (error word)");
-    nvfp4::GemmParams g = gemm_params(a_sf, rows, w_sf, wrows, n, k, alpha_dev, bias_bf16, out_bf16, ldo, err);
-    g.group_offsets = group_offsets_dev;
-    g.num_groups = num_groups;
-    g.group_n = (int32_t)n;
-    const char *why = nullptr;
-    e = nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, reinterpret_cast<cudaStream_t>(stream), &why, false);
-    if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
-    return launch_status(e, "grouped GEMM kernel");
+    return grouped_gemm_impl(a_fp4, a_sf, rows, group_offsets_dev, num_groups, w_fp4, w_sf, n, k, alpha_dev, bias_bf16,
+                             NVFP4_ACT_NONE, out_bf16, ldo, stream);
+}
+
+nvfp4_status nvfp4_grouped_gemm_act(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,
+                                    const int32_t *group_offsets_dev, int num_groups, const uint8_t *w_fp4,
+                                    const uint8_t *w_sf, int64_t n, int64_t k, const float *alpha_dev,
+                                    const void *bias_bf16, int act, void *out_bf16, int64_t ldo, nvfp4_stream_t stream)
+{
+    return grouped_gemm_impl(a_fp4, a_sf, rows, group_offsets_dev, num_groups, w_fp4, w_sf, n, k, alpha_dev, bias_bf16,
+                             act, out_bf16, ldo, stream);
 }
 
 }  // extern "C"

@@ -74,6 +74,14 @@ struct GemmParams {
     const int32_t *group_offsets;
     int32_t num_groups;
     int32_t group_n;
+    // Epilogue beyond alpha and bias (the kernels' kEpi variants): activation
+    // (an Activation of epilogue.cuh) and residual.  n_out counts accumulator
+    // columns; a gated activation makes one output column of two of them, so
+    // out_cols (columns of out and residual) is then n_out / 2.
+    int32_t act;
+    int32_t out_cols;
+    const uint16_t *residual;        // bf16 bits [m, ldr] or nullptr
+    int64_t ldr;
     uint64_t wait_ns;                // bound of every pipeline barrier wait (ns of %globaltimer)
     int32_t drill;                   // 1: timeout drill, the producers issue no copies (test hook)
     // Fused small-m linear (one-CTA kernel): the activation the kernel

@@ -40,6 +40,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "gemm_common.cuh"
 #include "ptx.cuh"
 #include "quant_core.cuh"
@@ -131,6 +132,28 @@ __device__ __forceinline__ Work work_of(int item, const GemmParams &p, int num_k
 // floats (256 columns, padded by 4 so that the 32 rows a warp writes at once
 // fall on different banks).
 constexpr int kPartLd = kBN + 4;
+// Residual columns [col, col + 8 kG) of `row`, eight per uint4 (zeros past m,
+// out_cols, or without a residual; col % 8 == 0 and rows start on 16 bytes).
+// One row per thread: 32 or 64 consecutive bytes of it, whole sectors.
+template <int kG>
+__device__ __forceinline__ void load_residual_row(const GemmParams &p, uint4 (&res)[kG], int64_t row, int col)
+{
+    const bool ok = p.residual != nullptr && row < p.m;
+    const uint16_t *src = p.residual + row * p.ldr + col;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        res[g] = make_uint4(0, 0, 0, 0);
+        if (ok && col + 8 * g + 8 <= p.out_cols) {
+            res[g] = ld_stream_v4(src + 8 * g);
+        } else if (ok && col + 8 * g < p.out_cols) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = col + 8 * g + e < p.out_cols ? src[8 * g + e] : 0u;
+            res[g] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+        }
+    }
+}
+
 // Up to this many rows below m in an epilogue warp's 32, the rows are written
 // straight from registers instead of through the staging buffer and the TMA.
 constexpr int kDirectStoreRows = 16;
@@ -146,6 +169,9 @@ static_assert((uint32_t)kBM * kPartLd * 4 <= kOffSfa, "the partials fit in the i
 // Equal ranges rather than whole column chunks per rank: at m = 128 the
 // distributed-shared-memory reads (m x 1 KB per rank) set the reduction's
 // time, and chunks of 32 columns gave two ranks of six twice the reads.
+// With kEpiAct the activation and residual follow the bias; with kEpiGated a
+// group's four columns are two (gate, up) pairs and make two output columns.
+template <int kEpi>
 __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &t, uint32_t part_smem, uint32_t rank,
                                                int tid)
 {
@@ -178,20 +204,43 @@ __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &
         for (int sp = 1; sp < kMaxSplits; ++sp)
             if (sp < p.splits) { acc.x += v[sp].x; acc.y += v[sp].y; acc.z += v[sp].z; acc.w += v[sp].w; }
         const float a[4] = {acc.x, acc.y, acc.z, acc.w};
-        uint32_t h[4];
+        const int64_t row = t.mb * kBM + r;
+        float v4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float b = (p.bias != nullptr && gcol + e < p.n_out) ? __uint_as_float((uint32_t)p.bias[gcol + e] << 16)
                                                                      : 0.0f;
-            h[e] = bf16_bits_rn(__fmaf_rn(a[e], alpha, b));
+            v4[e] = __fmaf_rn(a[e], alpha, b);
         }
-        uint16_t *o = p.out + (int64_t)(t.mb * kBM + r) * p.ldo + gcol;
-        if (gcol + 4 <= p.n_out) {      // 8-byte aligned: rows start on 16 bytes, gcol % 4 == 0
-            *reinterpret_cast<uint2 *>(o) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-        } else {
+        if constexpr (kEpi == kEpiGated) {
+            // n_out is even, so a pair is inside or outside as a whole
+            const int oc = gcol >> 1;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (gcol + e < p.n_out) o[e] = (uint16_t)h[e];
+            for (int e = 0; e < 2; ++e)
+                if (oc + e < p.out_cols) {
+                    float o = apply_gate(v4[2 * e], v4[2 * e + 1], p.act);
+                    if (p.residual != nullptr) o += __uint_as_float((uint32_t)p.residual[row * p.ldr + oc + e] << 16);
+                    p.out[row * p.ldo + oc + e] = (uint16_t)bf16_bits_rn(o);
+                }
+        } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kEpi == kEpiAct) {
+                    v4[e] = apply_act(v4[e], p.act);
+                    if (p.residual != nullptr && gcol + e < p.n_out)
+                        v4[e] += __uint_as_float((uint32_t)p.residual[row * p.ldr + gcol + e] << 16);
+                }
+                h[e] = bf16_bits_rn(v4[e]);
+            }
+            uint16_t *o = p.out + row * p.ldo + gcol;
+            if (gcol + 4 <= p.n_out) {      // 8-byte aligned: rows start on 16 bytes, gcol % 4 == 0
+                *reinterpret_cast<uint2 *>(o) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (gcol + e < p.n_out) o[e] = (uint16_t)h[e];
+            }
         }
     }
 }
@@ -293,7 +342,8 @@ __device__ __forceinline__ bool fused_quant_stages(const GemmParams &p, uint8_t 
 // of the activation p.quant.x (the body of quant_kernel, or quant_mx_kernel,
 // for the stage's 256 columns of every row) straight into the stage's A tile
 // and scale tiles in shared memory.
-template <bool kMx, bool kFused>
+// kEpi: the epilogue variant (epilogue.cuh).
+template <bool kMx, bool kFused, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_nvf4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmX,
@@ -436,25 +486,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
 
-            uint32_t packed[kEpiCols / 2];
+            constexpr int kOutCols = kEpi == kEpiGated ? kEpiCols / 2 : kEpiCols;
+            constexpr int kOutChunk = kEpi == kEpiGated ? 16 : 32;   // output columns of 32 accumulator columns
+            const int out_col_base = kEpi == kEpiGated ? col_base / 2 : col_base;
+            const int out_cols_here = kEpi == kEpiGated ? cols_here / 2 : cols_here;
+            uint32_t packed[kOutCols / 2];
             if (cols_here > 0) tmem_ld_32cols(acc, r0);
 #pragma unroll
             for (int ch = 0; ch < kEpiCols / 32; ++ch) {
                 uint32_t(&cur)[32] = (ch & 1) ? r1 : r0;
                 uint32_t(&nxt)[32] = (ch & 1) ? r0 : r1;
                 if (ch * 32 < cols_here) {                      // uniform across the warp
+                    uint4 res[kOutChunk / 8];
+                    if constexpr (kEpi != kEpiPlain)
+                        load_residual_row(p, res, row, out_col_base + ch * kOutChunk);
                     tmem_ld_wait_regs(cur);
                     if (ch + 1 < kEpiCols / 32 && (ch + 1) * 32 < cols_here) tmem_ld_32cols(acc + (ch + 1) * 32, nxt);
+                    // eight output columns at a time (sixteen accumulator columns when gated)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float b0 = 0.0f, b1 = 0.0f;
-                        if (use_bias) {
-                            const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
-                            b0 = __uint_as_float(bw << 16);
-                            b1 = __uint_as_float(bw & 0xFFFF0000u);
+                    for (int g = 0; g < kOutChunk / 8; ++g) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += (kEpi == kEpiGated ? 1 : 2)) {
+                            const int j = kEpi == kEpiGated ? 16 * g + 2 * e : 8 * g + e;
+                            float b0 = 0.0f, b1 = 0.0f;
+                            if (use_bias) {
+                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
+                                b0 = __uint_as_float(bw << 16);
+                                b1 = __uint_as_float(bw & 0xFFFF0000u);
+                            }
+                            const float v0 = __fmaf_rn(__uint_as_float(cur[j]), alpha, b0);
+                            const float v1 = __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1);
+                            if constexpr (kEpi == kEpiGated) {
+                                v[e] = apply_gate(v0, v1, p.act);
+                            } else {
+                                v[e] = kEpi == kEpiAct ? apply_act(v0, p.act) : v0;
+                                v[e + 1] = kEpi == kEpiAct ? apply_act(v1, p.act) : v1;
+                            }
                         }
-                        packed[ch * 16 + j / 2] = bf16x2_rn(__fmaf_rn(__uint_as_float(cur[j]), alpha, b0),
-                                                            __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1));
+                        if constexpr (kEpi != kEpiPlain) add_residual8(v, res[g]);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) packed[ch * (kOutChunk / 2) + g * 4 + e / 2] = bf16x2_rn(v[e], v[e + 1]);
                     }
                 }
             }
@@ -466,21 +538,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             // A few rows (small m): each of their lanes writes its row from
-            // registers, 16 bytes at a time (rows start on 16 bytes, col_base
-            // % 128 == 0); no round trips through the staging buffer.
+            // registers, 16 bytes at a time (rows start on 16 bytes, out_col_base
+            // % 64 == 0); no round trips through the staging buffer.
             const int rows_here = min(32, p.m - row0);
             if (cols_here > 0 && rows_here <= kDirectStoreRows) {
                 if (lane < rows_here) {
-                    uint16_t *o = p.out + (int64_t)(row0 + lane) * p.ldo + col_base;
+                    uint16_t *o = p.out + (int64_t)(row0 + lane) * p.ldo + out_col_base;
 #pragma unroll
-                    for (int g = 0; g < kEpiCols / 8; ++g) {
-                        if (8 * g + 8 <= cols_here) {
+                    for (int g = 0; g < kOutCols / 8; ++g) {
+                        if (8 * g + 8 <= out_cols_here) {
                             *reinterpret_cast<uint4 *>(o + 8 * g) =
                                 make_uint4(packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
-                        } else if (8 * g < cols_here) {
+                        } else if (8 * g < out_cols_here) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                if (8 * g + e < cols_here)
+                                if (8 * g + e < out_cols_here)
                                     o[8 * g + e] = (uint16_t)(packed[4 * g + e / 2] >> (16 * (e & 1)));
                         }
                     }
@@ -490,12 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // Store through shared memory and the TMA: 16-column chunks of this
             // warp's 32 rows x 128 columns; the TMA clips rows >= m and
-            // columns >= n_out.  (Thread-per-row global stores would touch 32
+            // columns past the last whole 16 bytes, the rest is stored by the row's lane.  (Thread-per-row global stores would touch 32
             // rows per instruction and congest the SM's memory pipeline that
             // the MMA thread's barrier and issue traffic also uses.)
 #pragma unroll
-            for (int c = 0; c < kEpiCols / 16; ++c) {
-                if (c * 16 < cols_here) {                       // uniform across the warp
+            for (int c = 0; c < kOutCols / 16; ++c) {
+                if (c * 16 < out_cols_here) {                       // uniform across the warp
                     if (lane == 0) bulk_wait_group_read<0>();   // the previous chunk's store has read the buffer
                     __syncwarp();
                     st_shared_v4(out_stage + lane * 32, packed[c * 8], packed[c * 8 + 1], packed[c * 8 + 2],
@@ -504,10 +576,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  packed[c * 8 + 6], packed[c * 8 + 7]);
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmOut, out_stage, col_base + c * 16, row0, out_policy);
+                    const int col = out_col_base + c * 16, whole = tma_cols(p.out_cols);
+                    if (lane == 0 && col < whole) {
+                        tma_store_2d(&tmOut, out_stage, col, row0, out_policy);
                         bulk_commit_group();
                     }
+                    if (whole < p.out_cols && whole >= col && whole < col + 16 && row < p.m)
+                        store_tail_columns(p, row, ld_shared_v4(out_stage + lane * 32 + (whole - col) * 2));
                 }
             }
         }
@@ -520,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // until every peer has read them.
             cluster_arrive_release();
             cluster_wait_acquire();
-            cluster_reduce(p, work_of(blockIdx.x, p, num_ks).t, smem_u32(smem), cluster_ctarank(),
+            cluster_reduce<kEpi>(p, work_of(blockIdx.x, p, num_ks).t, smem_u32(smem), cluster_ctarank(),
                            (int)threadIdx.x - kEpiWarp0 * 32);
             cluster_arrive_release();
         }
@@ -746,6 +821,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
+using OneCtaKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                              const GemmParams);
+constexpr OneCtaKernel kOneCtaKernels[12] = {            // [epilogue variant * 4 + fused * 2 + MXFP4]
+    gemm_nvf4_kernel<false, false, kEpiPlain>, gemm_nvf4_kernel<true, false, kEpiPlain>,
+    gemm_nvf4_kernel<false, true, kEpiPlain>,  gemm_nvf4_kernel<true, true, kEpiPlain>,
+    gemm_nvf4_kernel<false, false, kEpiAct>,   gemm_nvf4_kernel<true, false, kEpiAct>,
+    gemm_nvf4_kernel<false, true, kEpiAct>,    gemm_nvf4_kernel<true, true, kEpiAct>,
+    gemm_nvf4_kernel<false, false, kEpiGated>, gemm_nvf4_kernel<true, false, kEpiGated>,
+    gemm_nvf4_kernel<false, true, kEpiGated>,  gemm_nvf4_kernel<true, true, kEpiGated>};
+
 // Launches the one-CTA kernel: the plain GEMM or, with `fused`, the fused
 // small-m linear, optionally as a programmatic dependent of the kernel before
 // it (only the activation side waits for that kernel; the weights stream at
@@ -757,18 +842,10 @@ cudaError_t launch_one_cta(const GemmParams &p, const uint8_t *a, const uint8_t 
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_nvf4_kernel<false, false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_kernel<true, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
+        for (OneCtaKernel k : kOneCtaKernels) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            if (e != cudaSuccess) return e;
+        }
         configured_device = dev;
     }
     CUtensorMap tmA, tmB, tmOut;
@@ -779,7 +856,7 @@ cudaError_t launch_one_cta(const GemmParams &p, const uint8_t *a, const uint8_t 
         return cudaErrorInvalidValue;
     }
     if (p.splits == 1) {
-        if (!make_output_map(&tmOut, p.out, (uint64_t)p.n_out, (uint64_t)p.m, (uint64_t)p.ldo)) {
+        if (!make_output_map(&tmOut, p.out, output_map_cols(p.out_cols), (uint64_t)p.m, (uint64_t)p.ldo)) {
             *why = "cuTensorMapEncodeTiled failed for the output";
             return cudaErrorInvalidValue;
         }
@@ -820,11 +897,8 @@ cudaError_t launch_one_cta(const GemmParams &p, const uint8_t *a, const uint8_t 
         *why = "cuTensorMapEncodeTiled failed for the activation";
         return cudaErrorInvalidValue;
     }
-    if (fused)
-        return p.mx ? cudaLaunchKernelEx(&cfg, gemm_nvf4_kernel<true, true>, tmA, tmB, tmOut, tmX, p)
-                    : cudaLaunchKernelEx(&cfg, gemm_nvf4_kernel<false, true>, tmA, tmB, tmOut, tmX, p);
-    return p.mx ? cudaLaunchKernelEx(&cfg, gemm_nvf4_kernel<true, false>, tmA, tmB, tmOut, tmX, p)
-                : cudaLaunchKernelEx(&cfg, gemm_nvf4_kernel<false, false>, tmA, tmB, tmOut, tmX, p);
+    return cudaLaunchKernelEx(&cfg, kOneCtaKernels[epilogue_variant(p) * 4 + (fused ? 2 : 0) + p.mx], tmA, tmB, tmOut,
+                              tmX, p);
 }
 
 }  // namespace
@@ -844,8 +918,7 @@ int gemm_split_clusters(int splits, int num_sms)
     }
     if (cached[splits] == 0) {
         int clusters = 0;
-        cudaError_t e = cudaFuncSetAttribute(gemm_nvf4_kernel<false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmemBytes);
+        cudaError_t e = cudaFuncSetAttribute(kOneCtaKernels[0], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e == cudaSuccess) {
             cudaLaunchConfig_t probe = {};
             cudaLaunchAttribute attr;
@@ -858,7 +931,7 @@ int gemm_split_clusters(int splits, int num_sms)
             probe.dynamicSmemBytes = kSmemBytes;
             probe.attrs = &attr;
             probe.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&clusters, gemm_nvf4_kernel<false, false>, &probe);
+            e = cudaOccupancyMaxActiveClusters(&clusters, kOneCtaKernels[0], &probe);
         }
         if (e != cudaSuccess || clusters < 1) {
             cudaGetLastError();

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 
 namespace nvfp4 {
 namespace gemm_detail {
@@ -46,6 +47,39 @@ __device__ __forceinline__ uint32_t bf16_bits_rn(float f)
 }
 
 
+// o[i] += the i-th of eight bf16 packed in `w`.
+__device__ __forceinline__ void add_residual8(float (&o)[8], const uint4 &w)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] += __uint_as_float(u[i] << 16);
+        o[2 * i + 1] += __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+// The TMA clips an output row at 16-byte granularity: the output maps cover the
+// first out_cols / 8 * 8 columns, and the up to seven columns past them are
+// written by the row's thread from its staged 16-byte piece `v`.
+__host__ __device__ constexpr int tma_cols(int out_cols) { return out_cols & ~7; }
+
+__device__ __forceinline__ void store_tail_columns(const GemmParams &p, int64_t row, const uint4 &v)
+{
+    const int c0 = tma_cols(p.out_cols), n = p.out_cols - c0;
+    uint16_t *o = p.out + row * p.ldo + c0;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+}
+
+// The epilogue variant a launch needs.
+inline int epilogue_variant(const GemmParams &p)
+{
+    if (act_gated(p.act)) return kEpiGated;
+    return p.act != kActNone || p.residual != nullptr ? kEpiAct : kEpiPlain;
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -78,9 +112,14 @@ inline bool make_operand_map(CUtensorMap *map, const void *base, uint64_t row_by
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Columns of an output map: the whole 16-byte pieces (an output narrower than
+// one is stored without the TMA; its map is not used).
+inline uint64_t output_map_cols(int out_cols) { return out_cols >= 8 ? (uint64_t)tma_cols(out_cols) : 8; }
+
 // Map of the bf16 output [m, n_out] (row stride ldo elements) for TMA stores
 // of 16-column x 32-row boxes, no swizzle.  The TMA skips elements outside
-// [0, n_out) x [0, m).  Requires a 16-B aligned base and ldo % 8 == 0.
+// [0, n_out) x [0, m), columns in units of 8: n_out is a multiple of 8 (from
+// output_map_cols).  Requires a 16-B aligned base and ldo % 8 == 0.
 inline bool make_output_map(CUtensorMap *map, void *base, uint64_t n_out, uint64_t m, uint64_t ldo)
 {
     auto encode = tensor_map_encoder();
@@ -96,8 +135,8 @@ inline bool make_output_map(CUtensorMap *map, void *base, uint64_t n_out, uint64
 
 // Map of the bf16 output [m, n_out] (row stride ldo elements) for TMA stores
 // of 64-column x 32-row boxes (128-byte rows) with the 128-byte swizzle; the
-// TMA skips elements outside [0, n_out) x [0, m).  Requires a 16-B aligned base
-// and ldo % 8 == 0.
+// TMA skips elements outside [0, n_out) x [0, m), columns in units of 8.
+// Requires a 16-B aligned base and ldo % 8 == 0.
 inline bool make_output_map_sw128(CUtensorMap *map, void *base, uint64_t n_out, uint64_t m, uint64_t ldo)
 {
     auto encode = tensor_map_encoder();

@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "gemm_common.cuh"
 #include "ptx.cuh"
 
@@ -79,12 +80,41 @@ static_assert(kOffOut % 1024 == 0, "128-byte-swizzled TMA store sources are 1024
 static_assert(kTmemSf + kStages * kSfColsPerStage <= kTmemCols, "TMEM budget");
 static_assert(128 * (kRegsCtl + kRegsSf + 2 * kRegsEpi) <= kThreads * 128, "register reallocation budget");
 
+// One warp requests a 32-row x 64-column chunk of the residual into its staging
+// buffer, once its previous store has read it; the copy completes on `bar`.
+__device__ __forceinline__ void request_residual(const CUtensorMap *map, uint8_t *stage, uint64_t *bar, int col, int row,
+                                                 int lane)
+{
+    __syncwarp();                                  // every lane is done with the buffer
+    if (lane == 0) {
+        bulk_wait_group_read<0>();
+        mbar_arrive_expect_tx(bar, kOutChunkBytes);
+        tma_load_2d(stage, map, bar, col, row, l2_policy_evict_first());
+    }
+}
+
+// One warp stores its staged 32-row x 64-column output chunk.
+__device__ __forceinline__ void store_chunk(const GemmParams &p, const CUtensorMap *map, uint32_t stage, int col, int row,
+                                            int lane, uint64_t policy)
+{
+    const int cols = tma_cols(p.out_cols);
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0 && col < cols) {
+        tma_store_2d(map, stage, col, row, policy);
+        bulk_commit_group();
+    }
+    if (cols < p.out_cols && cols >= col && cols < col + 64 && row + lane < p.m)
+        store_tail_columns(p, row + lane, ld_shared_v4(stage + lane * 128 + ((((cols - col) >> 3) ^ (lane & 7)) << 4)));
+}
+
 // kMx: MXFP4 operands (UE8M0 scales per 32 K-elements, scale_vec::2X), else NVFP4.
-template <bool kMx>
+// kEpi: the epilogue variant (epilogue.cuh).
+template <bool kMx, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmSfb, const __grid_constant__ CUtensorMap tmOut,
-                          const GemmParams p)
+                          const __grid_constant__ CUtensorMap tmRes, const GemmParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -96,7 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *mma_done = tmem_empty + 1;
     uint64_t *sf_full = mma_done + 1;                                 // the stage's scale tiles landed
     uint64_t *sf_empty = sf_full + kStages;                           // the scale warps have read them
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sf_empty + kStages);
+    uint64_t *res_full = sf_empty + kStages;                          // [kEpiWarps] a residual chunk landed
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_full + kEpiWarps);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -116,6 +147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sf_full[s], 1);          // the scale producer
             mbar_init(&sf_empty[s], 4);         // the four scale warps
         }
+        if constexpr (kEpi != kEpiPlain)
+            for (int w = 0; w < kEpiWarps; ++w) mbar_init(&res_full[w], 1);
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
         prefetch_tensormap(&tmB);
@@ -150,6 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = p.alpha != nullptr ? __ldg(p.alpha) : 1.0f;
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
         uint32_t acc_phase = 0;
+        uint64_t *my_res = res_full + (warp - kEpiWarp0);
+        uint32_t res_phase = 0;
+        bool res_pending = false;                               // a residual copy is in flight (all lanes agree)
         int it = 0;
         for (int tile = pair_id; tile < num_tiles; tile += num_pairs, ++it) {
             const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
@@ -172,6 +208,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2 *>(s_bias + 4 * lane) = bw;
                 __syncwarp();
             }
+            // The residual of the tile's first output chunk is requested now,
+            // into the staging buffer itself (no shared memory is left for
+            // another): it lands while the accumulator is still being computed.
+            const int row0 = t.mb * kTileM + (int)rank * kRowsCta + q * 32;
+            const int out_col = kEpi == kEpiGated ? col_base / 2 : col_base;
+            if constexpr (kEpi != kEpiPlain)
+                if (p.residual != nullptr && n_cols > 0) {
+                    request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res, out_col, row0,
+                                     lane);
+                    res_pending = true;
+                }
             if (!__all_sync(~0u, mbar_wait(tmem_full, acc_phase, p.err_flag, kErrTimeout, p.wait_ns))) break;
             tc_fence_after_sync();
             acc_phase ^= 1;
@@ -199,45 +246,112 @@ __global__ void __launch_bounds__(kThreads, 1)
             // x 64-column chunks (128-byte rows, the TMA's 128-byte swizzle:
             // 16-byte piece j of row r sits at piece j ^ (r % 8), which also
             // spreads the 32 lanes' writes over all banks).  Rows >= m and
-            // columns >= n_out are clipped by the TMA.
-            const int row0 = t.mb * kTileM + (int)rank * kRowsCta + q * 32;
+            // columns >= out_cols are clipped by the TMA (columns in units of 8).
+            if constexpr (kEpi == kEpiGated) {
+                // One output chunk: 64 columns of the warp's 128 accumulator
+                // columns, gate and up side by side in one thread's registers.
+                if (n_cols > 0) {                               // uniform across the warp
+                    if (p.residual != nullptr) {
+                        if (!__all_sync(~0u, mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns))) break;
+                        res_phase ^= 1;
+                        res_pending = false;
+                    } else {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                    }
 #pragma unroll
-            for (int c = 0; c < kEpiCols / 64; ++c) {
-                if (c * 64 < n_cols) {                          // uniform across the warp
-                    if (lane == 0) bulk_wait_group_read<0>();   // the previous store has read the buffer
-                    __syncwarp();
+                    for (int ch = 0; ch < kEpiCols / 32; ++ch) {
+                        float o[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int ch = c * 2 + h;
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
+                        for (int j = 0; j < 16; ++j) {
                             float b0 = 0.0f, b1 = 0.0f;
                             if (use_bias) {
-                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
+                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + 2 * j);
                                 b0 = __uint_as_float(bw << 16);
                                 b1 = __uint_as_float(bw & 0xFFFF0000u);
                             }
-                            pk[j / 2] = bf16x2_rn(__fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b0),
-                                                  __fmaf_rn(__uint_as_float(acc_regs[ch][j + 1]), alpha, b1));
+                            o[j] = apply_gate(__fmaf_rn(__uint_as_float(acc_regs[ch][2 * j]), alpha, b0),
+                                              __fmaf_rn(__uint_as_float(acc_regs[ch][2 * j + 1]), alpha, b1), p.act);
                         }
 #pragma unroll
-                        for (int j4 = 0; j4 < 4; ++j4) {
-                            const int piece = h * 4 + j4;
-                            st_shared_v4(out_stage + lane * 128 + ((piece ^ (lane & 7)) << 4), pk[j4 * 4],
-                                         pk[j4 * 4 + 1], pk[j4 * 4 + 2], pk[j4 * 4 + 3]);
+                        for (int j4 = 0; j4 < 2; ++j4) {
+                            const uint32_t at = out_stage + lane * 128 + (((ch * 2 + j4) ^ (lane & 7)) << 4);
+                            float(&o8)[8] = *reinterpret_cast<float(*)[8]>(o + 8 * j4);
+                            if (p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
+                            st_shared_v4(at, bf16x2_rn(o8[0], o8[1]), bf16x2_rn(o8[2], o8[3]), bf16x2_rn(o8[4], o8[5]),
+                                         bf16x2_rn(o8[6], o8[7]));
                         }
                     }
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmOut, out_stage, col_base + c * 64, row0, out_policy);
-                        bulk_commit_group();
+                    store_chunk(p, &tmOut, out_stage, out_col, row0, lane, out_policy);
+                }
+                __syncwarp();                                   // every lane has read the bias buffer
+                continue;
+            }
+            bool res_ok = true;
+#pragma unroll
+            for (int c = 0; c < kEpiCols / 64; ++c) {
+                if (c * 64 < n_cols) {                          // uniform across the warp
+                    if (kEpi == kEpiAct && p.residual != nullptr) {
+                        if (c > 0) {                            // (chunk 0 was requested before the accumulator's wait)
+                            request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res,
+                                             out_col + c * 64, row0, lane);
+                            res_pending = true;
+                        }
+                        res_ok = __all_sync(~0u, mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns));
+                        if (!res_ok) break;
+                        res_phase ^= 1;
+                        res_pending = false;
+                    } else {
+                        if (lane == 0) bulk_wait_group_read<0>();   // the previous store has read the buffer
+                        __syncwarp();
                     }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int ch = c * 2 + h;
+                        if constexpr (kEpi == kEpiAct) {
+#pragma unroll
+                            for (int j4 = 0; j4 < 4; ++j4) {
+                                float o8[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int j = j4 * 8 + e;
+                                    const float b = use_bias ? __uint_as_float((uint32_t)s_bias[ch * 32 + j] << 16) : 0.0f;
+                                    o8[e] = apply_act(__fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b), p.act);
+                                }
+                                const uint32_t at = out_stage + lane * 128 + (((h * 4 + j4) ^ (lane & 7)) << 4);
+                                if (p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
+                                st_shared_v4(at, bf16x2_rn(o8[0], o8[1]), bf16x2_rn(o8[2], o8[3]),
+                                             bf16x2_rn(o8[4], o8[5]), bf16x2_rn(o8[6], o8[7]));
+                            }
+                        } else {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                float b0 = 0.0f, b1 = 0.0f;
+                                if (use_bias) {
+                                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
+                                    b0 = __uint_as_float(bw << 16);
+                                    b1 = __uint_as_float(bw & 0xFFFF0000u);
+                                }
+                                pk[j / 2] = bf16x2_rn(__fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b0),
+                                                      __fmaf_rn(__uint_as_float(acc_regs[ch][j + 1]), alpha, b1));
+                            }
+#pragma unroll
+                            for (int j4 = 0; j4 < 4; ++j4) {
+                                const int piece = h * 4 + j4;
+                                st_shared_v4(out_stage + lane * 128 + ((piece ^ (lane & 7)) << 4), pk[j4 * 4],
+                                             pk[j4 * 4 + 1], pk[j4 * 4 + 2], pk[j4 * 4 + 3]);
+                            }
+                        }
+                    }
+                    store_chunk(p, &tmOut, out_stage, out_col + c * 64, row0, lane, out_policy);
                 }
             }
             __syncwarp();                                       // every lane has read the bias buffer
+            if (!res_ok) break;
         }
+        if constexpr (kEpi != kEpiPlain)                        // (after an expired wait) nothing may land after the exit
+            if (res_pending) mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns);
         if (lane == 0) bulk_wait_group<0>();                    // all output written before the CTA exits
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
@@ -443,6 +557,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
+using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                            const CUtensorMap, const GemmParams);
+constexpr PairKernel kPairKernels[6] = {                 // [epilogue variant * 2 + MXFP4]
+    gemm_nvf4_pair_kernel<false, kEpiPlain>, gemm_nvf4_pair_kernel<true, kEpiPlain>,
+    gemm_nvf4_pair_kernel<false, kEpiAct>,   gemm_nvf4_pair_kernel<true, kEpiAct>,
+    gemm_nvf4_pair_kernel<false, kEpiGated>, gemm_nvf4_pair_kernel<true, kEpiGated>};
+
 }  // namespace
 
 cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,
@@ -453,12 +574,10 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_nvf4_pair_kernel<false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(gemm_nvf4_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
+        for (PairKernel k : kPairKernels) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            if (e != cudaSuccess) return e;
+        }
         cudaLaunchConfig_t probe = {};
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -471,7 +590,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         probe.attrs = &attr;
         probe.numAttrs = 1;
         int clusters = 0;
-        e = cudaOccupancyMaxActiveClusters(&clusters, gemm_nvf4_pair_kernel<false>, &probe);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kPairKernels[0], &probe);
         if (e != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             clusters = num_sms / 2;
@@ -497,10 +616,18 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         *why = "cuTensorMapEncodeTiled failed for the weight scales";
         return cudaErrorInvalidValue;
     }
-    if (!make_output_map_sw128(&tmOut, p.out, (uint64_t)p.n_out, (uint64_t)p.m, (uint64_t)p.ldo)) {
+    if (!make_output_map_sw128(&tmOut, p.out, output_map_cols(p.out_cols), (uint64_t)p.m, (uint64_t)p.ldo)) {
         *why = "cuTensorMapEncodeTiled failed for the output";
         return cudaErrorInvalidValue;
     }
+    CUtensorMap tmRes = tmOut;                          // (not read without a residual)
+    if (p.residual != nullptr &&
+        !make_output_map_sw128(&tmRes, const_cast<uint16_t *>(p.residual), (uint64_t)p.out_cols, (uint64_t)p.m,
+                               (uint64_t)p.ldr)) {
+        *why = "cuTensorMapEncodeTiled failed for the residual";
+        return cudaErrorInvalidValue;
+    }
+    const int epi = epilogue_variant(p);
     const int tiles = p.num_m_blk * p.num_n_blk;
     const int pairs = tiles < max_pairs ? tiles : max_pairs;
     cudaLaunchConfig_t cfg = {};
@@ -517,8 +644,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = dependent ? 2 : 1;
-    return p.mx ? cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<true>, tmA, tmB, tmSfb, tmOut, p)
-                : cudaLaunchKernelEx(&cfg, gemm_nvf4_pair_kernel<false>, tmA, tmB, tmSfb, tmOut, p);
+    return cudaLaunchKernelEx(&cfg, kPairKernels[epi * 2 + p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
 }
 
 }  // namespace nvfp4
