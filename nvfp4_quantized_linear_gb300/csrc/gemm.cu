@@ -176,6 +176,7 @@ __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &
                                                int tid)
 {
     const float alpha = p.alpha != nullptr ? __ldg(p.alpha) : 1.0f;
+    const ActParams actp = act_params(p.act);
     const int rows = min(kBM, p.m - t.mb * kBM);
     const int cols = min(kBN, p.n_out - t.nb * kBN);
     const int quads = (cols + 3) >> 2;
@@ -215,19 +216,21 @@ __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &
         if constexpr (kEpi == kEpiGated) {
             // n_out is even, so a pair is inside or outside as a whole
             const int oc = gcol >> 1;
+            float o2[2];
+            apply_gate(o2, v4, actp);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (oc + e < p.out_cols) {
-                    float o = apply_gate(v4[2 * e], v4[2 * e + 1], p.act);
+                    float o = o2[e];
                     if (p.residual != nullptr) o += __uint_as_float((uint32_t)p.residual[row * p.ldr + oc + e] << 16);
                     p.out[row * p.ldo + oc + e] = (uint16_t)bf16_bits_rn(o);
                 }
         } else {
             uint32_t h[4];
+            if constexpr (kEpi == kEpiAct) apply_act(v4, actp);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (kEpi == kEpiAct) {
-                    v4[e] = apply_act(v4[e], p.act);
                     if (p.residual != nullptr && gcol + e < p.n_out)
                         v4[e] += __uint_as_float((uint32_t)p.residual[row * p.ldr + gcol + e] << 16);
                 }
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t out_stage = smem_u32(smem + kOffOut) + (warp - kEpiWarp0) * kOutChunkBytes;
         const bool use_bias = p.splits == 1 && p.bias != nullptr;
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
+        const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
         int it = 0;
         int q_stage = 0;                                        // fused linear: the quantized stages
@@ -505,24 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // eight output columns at a time (sixteen accumulator columns when gated)
 #pragma unroll
                     for (int g = 0; g < kOutChunk / 8; ++g) {
-                        float v[8];
+                        constexpr int kIn = kEpi == kEpiGated ? 16 : 8;
+                        float in[kIn], v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e += (kEpi == kEpiGated ? 1 : 2)) {
-                            const int j = kEpi == kEpiGated ? 16 * g + 2 * e : 8 * g + e;
+                        for (int e = 0; e < kIn; e += 2) {
+                            const int j = kIn * g + e;
                             float b0 = 0.0f, b1 = 0.0f;
                             if (use_bias) {
                                 const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
                                 b0 = __uint_as_float(bw << 16);
                                 b1 = __uint_as_float(bw & 0xFFFF0000u);
                             }
-                            const float v0 = __fmaf_rn(__uint_as_float(cur[j]), alpha, b0);
-                            const float v1 = __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1);
-                            if constexpr (kEpi == kEpiGated) {
-                                v[e] = apply_gate(v0, v1, p.act);
-                            } else {
-                                v[e] = kEpi == kEpiAct ? apply_act(v0, p.act) : v0;
-                                v[e + 1] = kEpi == kEpiAct ? apply_act(v1, p.act) : v1;
-                            }
+                            in[e] = __fmaf_rn(__uint_as_float(cur[j]), alpha, b0);
+                            in[e + 1] = __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1);
+                        }
+                        if constexpr (kEpi == kEpiGated) {
+                            apply_gate(v, in, actp);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = in[e];
+                            if constexpr (kEpi == kEpiAct) apply_act(v, actp);
                         }
                         if constexpr (kEpi != kEpiPlain) add_residual8(v, res[g]);
 #pragma unroll
@@ -577,11 +583,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_shared();
                     __syncwarp();
                     const int col = out_col_base + c * 16, whole = tma_cols(p.out_cols);
-                    if (lane == 0 && col < whole) {
+                    if (lane == 0 && (kEpi == kEpiPlain || col < whole)) {
                         tma_store_2d(&tmOut, out_stage, col, row0, out_policy);
                         bulk_commit_group();
                     }
-                    if (whole < p.out_cols && whole >= col && whole < col + 16 && row < p.m)
+                    if (kEpi != kEpiPlain && whole < p.out_cols && whole >= col && whole < col + 16 && row < p.m)
                         store_tail_columns(p, row, ld_shared_v4(out_stage + lane * 32 + (whole - col) * 2));
                 }
             }

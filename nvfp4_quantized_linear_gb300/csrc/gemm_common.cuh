@@ -73,11 +73,14 @@ __device__ __forceinline__ void store_tail_columns(const GemmParams &p, int64_t 
         if (e < n) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
 }
 
-// The epilogue variant a launch needs.
+// The epilogue variant a launch needs, and whether it needs the parts that the
+// kernels' kFull instances add: a residual, or output columns that end inside
+// 16 bytes.
+inline bool epilogue_full(const GemmParams &p) { return p.residual != nullptr || tma_cols(p.out_cols) != p.out_cols; }
+
 inline int epilogue_variant(const GemmParams &p)
 {
-    if (act_gated(p.act)) return kEpiGated;
-    return p.act != kActNone || p.residual != nullptr ? kEpiAct : kEpiPlain;
+    return act_gated(p.act) ? kEpiGated : p.act != kActNone || epilogue_full(p) ? kEpiAct : kEpiPlain;
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()

@@ -93,24 +93,31 @@ __device__ __forceinline__ void request_residual(const CUtensorMap *map, uint8_t
     }
 }
 
-// One warp stores its staged 32-row x 64-column output chunk.
+// One warp stores its staged 32-row x 64-column output chunk (kTail: the
+// output's last columns may end inside 16 bytes).
+template <bool kTail>
 __device__ __forceinline__ void store_chunk(const GemmParams &p, const CUtensorMap *map, uint32_t stage, int col, int row,
                                             int lane, uint64_t policy)
 {
-    const int cols = tma_cols(p.out_cols);
     fence_proxy_async_shared();
     __syncwarp();
-    if (lane == 0 && col < cols) {
+    if (lane == 0 && (!kTail || col < tma_cols(p.out_cols))) {
         tma_store_2d(map, stage, col, row, policy);
         bulk_commit_group();
     }
-    if (cols < p.out_cols && cols >= col && cols < col + 64 && row + lane < p.m)
-        store_tail_columns(p, row + lane, ld_shared_v4(stage + lane * 128 + ((((cols - col) >> 3) ^ (lane & 7)) << 4)));
+    if (kTail && (p.out_cols & 7) != 0) {           // uniform: the chunk that holds the last columns
+        const int piece = (tma_cols(p.out_cols) - col) >> 3;
+        if (piece >= 0 && piece < 8 && row + lane < p.m)
+            store_tail_columns(p, row + lane, ld_shared_v4(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)));
+    }
 }
 
 // kMx: MXFP4 operands (UE8M0 scales per 32 K-elements, scale_vec::2X), else NVFP4.
-// kEpi: the epilogue variant (epilogue.cuh).
-template <bool kMx, int kEpi>
+// kEpi: the epilogue variant (epilogue.cuh).  kFull: with a residual (if one is
+// given) and columns that end inside 16 bytes; its registers and code stay out
+// of the other instances (8192 x 4096 x 28672 without either: 286 us, 310 us
+// with the tail's code alone).
+template <bool kMx, int kEpi, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmSfb, const __grid_constant__ CUtensorMap tmOut,
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sf_full[s], 1);          // the scale producer
             mbar_init(&sf_empty[s], 4);         // the four scale warps
         }
-        if constexpr (kEpi != kEpiPlain)
+        if constexpr (kFull)
             for (int w = 0; w < kEpiWarps; ++w) mbar_init(&res_full[w], 1);
         fence_mbarrier_init();
         prefetch_tensormap(&tmA);
@@ -182,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bias_vec = (reinterpret_cast<uintptr_t>(p.bias) & 7) == 0;   // 8-byte loads of 4 columns
         const float alpha = p.alpha != nullptr ? __ldg(p.alpha) : 1.0f;
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
+        const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
         uint64_t *my_res = res_full + (warp - kEpiWarp0);
         uint32_t res_phase = 0;
@@ -213,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // another): it lands while the accumulator is still being computed.
             const int row0 = t.mb * kTileM + (int)rank * kRowsCta + q * 32;
             const int out_col = kEpi == kEpiGated ? col_base / 2 : col_base;
-            if constexpr (kEpi != kEpiPlain)
+            if constexpr (kFull)
                 if (p.residual != nullptr && n_cols > 0) {
                     request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res, out_col, row0,
                                      lane);
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // One output chunk: 64 columns of the warp's 128 accumulator
                 // columns, gate and up side by side in one thread's registers.
                 if (n_cols > 0) {                               // uniform across the warp
-                    if (p.residual != nullptr) {
+                    if (kFull && p.residual != nullptr) {
                         if (!__all_sync(~0u, mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns))) break;
                         res_phase ^= 1;
                         res_pending = false;
@@ -261,28 +269,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int ch = 0; ch < kEpiCols / 32; ++ch) {
-                        float o[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float b0 = 0.0f, b1 = 0.0f;
-                            if (use_bias) {
-                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + 2 * j);
-                                b0 = __uint_as_float(bw << 16);
-                                b1 = __uint_as_float(bw & 0xFFFF0000u);
+                        for (int g = 0; g < 2; ++g) {               // eight output columns each
+                            float v[16], o[8];
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                float b0 = 0.0f, b1 = 0.0f;
+                                if (use_bias) {
+                                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + g * 16 + j);
+                                    b0 = __uint_as_float(bw << 16);
+                                    b1 = __uint_as_float(bw & 0xFFFF0000u);
+                                }
+                                v[j] = __fmaf_rn(__uint_as_float(acc_regs[ch][g * 16 + j]), alpha, b0);
+                                v[j + 1] = __fmaf_rn(__uint_as_float(acc_regs[ch][g * 16 + j + 1]), alpha, b1);
                             }
-                            o[j] = apply_gate(__fmaf_rn(__uint_as_float(acc_regs[ch][2 * j]), alpha, b0),
-                                              __fmaf_rn(__uint_as_float(acc_regs[ch][2 * j + 1]), alpha, b1), p.act);
-                        }
-#pragma unroll
-                        for (int j4 = 0; j4 < 2; ++j4) {
-                            const uint32_t at = out_stage + lane * 128 + (((ch * 2 + j4) ^ (lane & 7)) << 4);
-                            float(&o8)[8] = *reinterpret_cast<float(*)[8]>(o + 8 * j4);
-                            if (p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
-                            st_shared_v4(at, bf16x2_rn(o8[0], o8[1]), bf16x2_rn(o8[2], o8[3]), bf16x2_rn(o8[4], o8[5]),
-                                         bf16x2_rn(o8[6], o8[7]));
+                            apply_gate(o, v, actp);
+                            const uint32_t at = out_stage + lane * 128 + (((ch * 2 + g) ^ (lane & 7)) << 4);
+                            if (kFull && p.residual != nullptr) add_residual8(o, ld_shared_v4(at));
+                            st_shared_v4(at, bf16x2_rn(o[0], o[1]), bf16x2_rn(o[2], o[3]), bf16x2_rn(o[4], o[5]),
+                                         bf16x2_rn(o[6], o[7]));
                         }
                     }
-                    store_chunk(p, &tmOut, out_stage, out_col, row0, lane, out_policy);
+                    store_chunk<kFull>(p, &tmOut, out_stage, out_col, row0, lane, out_policy);
                 }
                 __syncwarp();                                   // every lane has read the bias buffer
                 continue;
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kEpiCols / 64; ++c) {
                 if (c * 64 < n_cols) {                          // uniform across the warp
-                    if (kEpi == kEpiAct && p.residual != nullptr) {
+                    if (kFull && p.residual != nullptr) {
                         if (c > 0) {                            // (chunk 0 was requested before the accumulator's wait)
                             request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res,
                                              out_col + c * 64, row0, lane);
@@ -313,13 +321,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j4 = 0; j4 < 4; ++j4) {
                                 float o8[8];
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
+                                for (int e = 0; e < 8; e += 2) {
                                     const int j = j4 * 8 + e;
-                                    const float b = use_bias ? __uint_as_float((uint32_t)s_bias[ch * 32 + j] << 16) : 0.0f;
-                                    o8[e] = apply_act(__fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b), p.act);
+                                    float b0 = 0.0f, b1 = 0.0f;
+                                    if (use_bias) {
+                                        const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
+                                        b0 = __uint_as_float(bw << 16);
+                                        b1 = __uint_as_float(bw & 0xFFFF0000u);
+                                    }
+                                    o8[e] = __fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b0);
+                                    o8[e + 1] = __fmaf_rn(__uint_as_float(acc_regs[ch][j + 1]), alpha, b1);
                                 }
+                                apply_act(o8, actp);
                                 const uint32_t at = out_stage + lane * 128 + (((h * 4 + j4) ^ (lane & 7)) << 4);
-                                if (p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
+                                if (kFull && p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
                                 st_shared_v4(at, bf16x2_rn(o8[0], o8[1]), bf16x2_rn(o8[2], o8[3]),
                                              bf16x2_rn(o8[4], o8[5]), bf16x2_rn(o8[6], o8[7]));
                             }
@@ -344,13 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     }
-                    store_chunk(p, &tmOut, out_stage, out_col + c * 64, row0, lane, out_policy);
+                    store_chunk<kFull>(p, &tmOut, out_stage, out_col + c * 64, row0, lane, out_policy);
                 }
             }
             __syncwarp();                                       // every lane has read the bias buffer
             if (!res_ok) break;
         }
-        if constexpr (kEpi != kEpiPlain)                        // (after an expired wait) nothing may land after the exit
+        if constexpr (kFull)                                    // (after an expired wait) nothing may land after the exit
             if (res_pending) mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns);
         if (lane == 0) bulk_wait_group<0>();                    // all output written before the CTA exits
     } else if (warp >= kSfWarp0) {
@@ -559,10 +574,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                             const CUtensorMap, const GemmParams);
-constexpr PairKernel kPairKernels[6] = {                 // [epilogue variant * 2 + MXFP4]
-    gemm_nvf4_pair_kernel<false, kEpiPlain>, gemm_nvf4_pair_kernel<true, kEpiPlain>,
-    gemm_nvf4_pair_kernel<false, kEpiAct>,   gemm_nvf4_pair_kernel<true, kEpiAct>,
-    gemm_nvf4_pair_kernel<false, kEpiGated>, gemm_nvf4_pair_kernel<true, kEpiGated>};
+constexpr PairKernel kPairKernels[] = {                  // [instance * 2 + MXFP4]
+    gemm_nvf4_pair_kernel<false, kEpiPlain, false>, gemm_nvf4_pair_kernel<true, kEpiPlain, false>,
+    gemm_nvf4_pair_kernel<false, kEpiAct, false>,   gemm_nvf4_pair_kernel<true, kEpiAct, false>,
+    gemm_nvf4_pair_kernel<false, kEpiGated, false>, gemm_nvf4_pair_kernel<true, kEpiGated, false>,
+    gemm_nvf4_pair_kernel<false, kEpiAct, true>,    gemm_nvf4_pair_kernel<true, kEpiAct, true>,
+    gemm_nvf4_pair_kernel<false, kEpiGated, true>,  gemm_nvf4_pair_kernel<true, kEpiGated, true>};
+
+int pair_instance(const GemmParams &p)
+{
+    const int v = epilogue_variant(p);
+    return epilogue_full(p) ? v + 2 : v;                 // (v is kEpiAct or kEpiGated when full)
+}
 
 }  // namespace
 
@@ -627,7 +650,6 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         *why = "cuTensorMapEncodeTiled failed for the residual";
         return cudaErrorInvalidValue;
     }
-    const int epi = epilogue_variant(p);
     const int tiles = p.num_m_blk * p.num_n_blk;
     const int pairs = tiles < max_pairs ? tiles : max_pairs;
     cudaLaunchConfig_t cfg = {};
@@ -644,7 +666,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = dependent ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kPairKernels[epi * 2 + p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
+    return cudaLaunchKernelEx(&cfg, kPairKernels[pair_instance(p) * 2 + p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
 }
 
 }  // namespace nvfp4
