@@ -132,26 +132,18 @@ __device__ __forceinline__ Work work_of(int item, const GemmParams &p, int num_k
 // floats (256 columns, padded by 4 so that the 32 rows a warp writes at once
 // fall on different banks).
 constexpr int kPartLd = kBN + 4;
-// Residual columns [col, col + 8 kG) of `row`, eight per uint4 (zeros past m,
-// out_cols, or without a residual; col % 8 == 0 and rows start on 16 bytes).
-// One row per thread: 32 or 64 consecutive bytes of it, whole sectors.
+// Residual columns [col, col + 8 kG) of `row`, eight per uint4 (zeros past m or
+// without a residual; col % 8 == 0 and rows start on 16 bytes).  The last piece
+// of a row is read whole, up to 14 bytes past out_cols inside its aligned 16;
+// they only meet columns that are not stored.  One row per thread: 32 or 64
+// consecutive bytes of it, whole sectors.
 template <int kG>
 __device__ __forceinline__ void load_residual_row(const GemmParams &p, uint4 (&res)[kG], int64_t row, int col)
 {
-    const bool ok = p.residual != nullptr && row < p.m;
+    const int cols = p.residual != nullptr && row < p.m ? p.out_cols - col : 0;
     const uint16_t *src = p.residual + row * p.ldr + col;
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-        res[g] = make_uint4(0, 0, 0, 0);
-        if (ok && col + 8 * g + 8 <= p.out_cols) {
-            res[g] = ld_stream_v4(src + 8 * g);
-        } else if (ok && col + 8 * g < p.out_cols) {
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = col + 8 * g + e < p.out_cols ? src[8 * g + e] : 0u;
-            res[g] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-        }
-    }
+    for (int g = 0; g < kG; ++g) res[g] = 8 * g < cols ? ld_stream_v4(src + 8 * g) : make_uint4(0, 0, 0, 0);
 }
 
 // Up to this many rows below m in an epilogue warp's 32, the rows are written
@@ -213,11 +205,14 @@ __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &
                                                                      : 0.0f;
             v4[e] = __fmaf_rn(a[e], alpha, b);
         }
+        uint64_t v2[2] = {pack2(v4[0], v4[1]), pack2(v4[2], v4[3])};
         if constexpr (kEpi == kEpiGated) {
             // n_out is even, so a pair is inside or outside as a whole
             const int oc = gcol >> 1;
+            uint64_t g2[1];
+            apply_gate(g2, v2, actp);
             float o2[2];
-            apply_gate(o2, v4, actp);
+            unpack2(g2[0], o2[0], o2[1]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 if (oc + e < p.out_cols) {
@@ -227,7 +222,11 @@ __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &
                 }
         } else {
             uint32_t h[4];
-            if constexpr (kEpi == kEpiAct) apply_act(v4, actp);
+            if constexpr (kEpi == kEpiAct) {
+                apply_act(v2, actp);
+                unpack2(v2[0], v4[0], v4[1]);
+                unpack2(v2[1], v4[2], v4[3]);
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if constexpr (kEpi == kEpiAct) {
@@ -366,8 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(x_full + kStages);
 
     const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             // the activation and the weight producer (fused: the weight
@@ -401,11 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-
-    const int num_tiles = p.num_m_blk * p.num_n_blk * p.splits;     // work items
-    const int num_ks = (p.num_k64 + 3) / 4;
-    const int n_bands_w = (p.n_w + 127) / 128;
 
     // The next kernel on the stream, if launched as a programmatic dependent
     // (this library's quantizer or GEMM), may get resident now: it waits for
@@ -415,6 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Roles by warpgroup; each warpgroup first resizes its register file.
     if (warp >= kEpiWarp0) {
         setmaxnreg_inc<kRegsEpi>();
+        const int lane = role_value((int)(threadIdx.x & 31));
+        const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
+        const int num_ks = role_value((p.num_k64 + 3) / 4);
+        const uint32_t tmem = role_tmem(tmem_slot);
         // ------------------------------------------------------ epilogue --
         // Drain the finished 128 x 256 accumulator (this warp: TMEM lane
         // quarter warp % 4, one row per thread) into registers as packed bf16
@@ -509,30 +505,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // eight output columns at a time (sixteen accumulator columns when gated)
 #pragma unroll
                     for (int g = 0; g < kOutChunk / 8; ++g) {
-                        constexpr int kIn = kEpi == kEpiGated ? 16 : 8;
-                        float in[kIn], v[8];
-#pragma unroll
-                        for (int e = 0; e < kIn; e += 2) {
-                            const int j = kIn * g + e;
-                            float b0 = 0.0f, b1 = 0.0f;
-                            if (use_bias) {
-                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
-                                b0 = __uint_as_float(bw << 16);
-                                b1 = __uint_as_float(bw & 0xFFFF0000u);
-                            }
-                            in[e] = __fmaf_rn(__uint_as_float(cur[j]), alpha, b0);
-                            in[e + 1] = __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1);
-                        }
+                        const uint16_t *gb = use_bias ? s_bias + ch * 32 + g * (kEpi == kEpiGated ? 16 : 8) : nullptr;
+                        uint64_t v[4];
                         if constexpr (kEpi == kEpiGated) {
+                            uint64_t in[8];
+                            scale_bias(in, cur + g * 16, alpha, gb);
                             apply_gate(v, in, actp);
                         } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = in[e];
+                            scale_bias(v, cur + g * 8, alpha, gb);
                             if constexpr (kEpi == kEpiAct) apply_act(v, actp);
                         }
                         if constexpr (kEpi != kEpiPlain) add_residual8(v, res[g]);
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) packed[ch * (kOutChunk / 2) + g * 4 + e / 2] = bf16x2_rn(v[e], v[e + 1]);
+                        for (int e = 0; e < 4; ++e) packed[ch * (kOutChunk / 2) + g * 4 + e] = bf16x2_of(v[e]);
                     }
                 }
             }
@@ -607,6 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
+        const int lane = role_value((int)(threadIdx.x & 31));
+        const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
+        const int num_ks = role_value((p.num_k64 + 3) / 4);
+        const uint32_t tmem = role_tmem(tmem_slot);
         // ----------------------------------------------- scale staging --
         // When a stage lands, copy its scale tiles from shared memory into the
         // stage's TMEM columns with tcgen05.st (the tensor pipe's tcgen05.cp
@@ -661,6 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         setmaxnreg_dec<kRegsCtl>();
+        const int lane = role_value((int)(threadIdx.x & 31));
+        const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
+        const int num_ks = role_value((p.num_k64 + 3) / 4);
+        const uint32_t tmem = role_tmem(tmem_slot);
         if (kFused && warp == 0) {
             // the fused linear reads no A tensor: the epilogue warps quantize it
         } else if ((warp == 0 || warp == 3) && lane == 0 && !p.drill) {   // (a timeout drill issues no copies)
@@ -720,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++stage == kStages) { stage = 0; phase ^= 1; }
                 }
             }
-            (void)n_bands_w;
             // Every copy this thread issued has landed before the CTA may exit.
             for (int s = 0; s < kStages; ++s)
                 if (issued_mask & (1u << s)) {
@@ -820,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     if (p.splits > 1) cluster_wait_acquire();          // every peer has read this CTA's partials
-    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 1) tmem_dealloc(*tmem_slot, kTmemCols);
 }
 
 }  // namespace

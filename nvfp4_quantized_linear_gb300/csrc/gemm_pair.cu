@@ -47,13 +47,13 @@ constexpr int kWalkGroup = 32;                  // pair tiles per group of the t
 constexpr int kTileN = 256;
 constexpr int kRowsCta = 128;
 constexpr int kBKBytes = 128;                   // 256 FP4 elements of K per stage
-constexpr int kStages = 5;
 constexpr int kEpiColsBias = 128;                     // bias columns per epilogue warp
 constexpr uint32_t kABytes = kRowsCta * kBKBytes;     // 16 KB: this CTA's A rows
 constexpr uint32_t kBBytes = kRowsCta * kBKBytes;     // 16 KB: this CTA's half of B
 constexpr uint32_t kSfaBytes = 4 * 512;               // this CTA's A band, 4 K-steps
 constexpr uint32_t kSfbBytes = 2 * 4 * 512;           // both B bands of the tile
 constexpr uint32_t kOutChunkBytes = 32 * 64 * 2;      // output staging: 32 rows x 64 columns bf16 (4 KB)
+constexpr int kStages = 5;
 constexpr uint32_t kOffA = 0;
 constexpr uint32_t kOffB = kOffA + kStages * kABytes;
 constexpr uint32_t kOffSfa = kOffB + kStages * kBBytes;
@@ -80,17 +80,48 @@ static_assert(kOffOut % 1024 == 0, "128-byte-swizzled TMA store sources are 1024
 static_assert(kTmemSf + kStages * kSfColsPerStage <= kTmemCols, "TMEM budget");
 static_assert(128 * (kRegsCtl + kRegsSf + 2 * kRegsEpi) <= kThreads * 128, "register reallocation budget");
 
-// One warp requests a 32-row x 64-column chunk of the residual into its staging
-// buffer, once its previous store has read it; the copy completes on `bar`.
+// What every role of the kernel needs, read at the role's start (role_value).
+struct Role {
+    int lane, pair_id, num_pairs, num_tiles, num_ks;
+    uint32_t rank, tmem;
+    bool is_leader;
+};
+
+__device__ __forceinline__ Role enter_role(const GemmParams &p, const uint32_t *tmem_slot)
+{
+    Role r;
+    r.lane = role_value((int)(threadIdx.x & 31));
+    r.pair_id = role_value((int)(blockIdx.x >> 1));
+    r.num_pairs = role_value((int)(gridDim.x >> 1));
+    r.num_tiles = role_value(p.num_m_blk * p.num_n_blk);       // num_m_blk counts 256-row tiles here
+    r.num_ks = role_value((p.num_k64 + 3) / 4);
+    r.rank = cluster_ctarank();
+    r.is_leader = r.rank == 0;
+    r.tmem = role_tmem(tmem_slot);
+    return r;
+}
+
+// One warp requests a 32-row x 64-column chunk of the residual into its output
+// chunk, once the previous store has read it.
 __device__ __forceinline__ void request_residual(const CUtensorMap *map, uint8_t *stage, uint64_t *bar, int col, int row,
                                                  int lane)
 {
-    __syncwarp();                                  // every lane is done with the buffer
+    __syncwarp();                                  // every lane is done with the chunk
     if (lane == 0) {
         bulk_wait_group_read<0>();
         mbar_arrive_expect_tx(bar, kOutChunkBytes);
         tma_load_2d(stage, map, bar, col, row, l2_policy_evict_first());
     }
+}
+
+// Waits for a requested chunk; after an expired wait once more, so that the copy
+// does not land in shared memory that the CTA has left.
+__device__ __forceinline__ bool wait_residual(const GemmParams &p, uint64_t *bar, uint32_t &phase)
+{
+    const bool ok = mbar_wait(bar, phase, p.err_flag, kErrTimeout, p.wait_ns);
+    if (!ok) mbar_wait(bar, phase, p.err_flag, kErrTimeout, p.wait_ns);
+    phase ^= 1;
+    return __all_sync(~0u, ok);
 }
 
 // One warp stores its staged 32-row x 64-column output chunk (kTail: the
@@ -137,9 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_full + kEpiWarps);
 
     const int warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const bool is_leader = rank == 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -169,16 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync_all();                 // barrier inits and the TMEM allocation visible in both CTAs
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-
-    const int pair_id = blockIdx.x >> 1;
-    const int num_pairs = gridDim.x >> 1;
-    const int num_tiles = p.num_m_blk * p.num_n_blk;       // num_m_blk counts 256-row tiles here
-    const int num_ks = (p.num_k64 + 3) / 4;
-    const int a_bands = (p.m + 127) / 128;
-
     if (warp >= kEpiWarp0) {
         setmaxnreg_inc<kRegsEpi>();
+        const Role role = enter_role(p, tmem_slot);
+        const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
+        const uint32_t rank = role.rank, tmem = role.tmem;
         // ------------------------------------------------------ epilogue --
         const int q = warp & 3;
         const int hcol = ((warp - kEpiWarp0) >> 2) * kEpiCols;
@@ -191,11 +214,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
         const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
-        uint64_t *my_res = res_full + (warp - kEpiWarp0);
         uint32_t res_phase = 0;
-        bool res_pending = false;                               // a residual copy is in flight (all lanes agree)
         int it = 0;
-        for (int tile = pair_id; tile < num_tiles; tile += num_pairs, ++it) {
+        for (int tile = role.pair_id; tile < num_tiles; tile += num_pairs, ++it) {
             const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
             const int n_cols = min(kEpiCols, p.n_out - t.nb * kTileN - hcol);   // may be <= 0
             const int col_base = t.nb * kTileN + hcol;
@@ -216,17 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2 *>(s_bias + 4 * lane) = bw;
                 __syncwarp();
             }
-            // The residual of the tile's first output chunk is requested now,
-            // into the staging buffer itself (no shared memory is left for
-            // another): it lands while the accumulator is still being computed.
+            // The residual's first chunk is requested now, into the output chunk
+            // itself (no shared memory is left for another), and its second one
+            // into L2: both arrive while the accumulator is being computed.
             const int row0 = t.mb * kTileM + (int)rank * kRowsCta + q * 32;
             const int out_col = kEpi == kEpiGated ? col_base / 2 : col_base;
-            if constexpr (kFull)
-                if (p.residual != nullptr && n_cols > 0) {
-                    request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res, out_col, row0,
-                                     lane);
-                    res_pending = true;
-                }
+            uint8_t *const chunk = smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes;
+            uint64_t *const res_bar = res_full + (warp - kEpiWarp0);
+            const bool use_res = kFull && p.residual != nullptr;
+            if (use_res && n_cols > 0) {
+                request_residual(&tmRes, chunk, res_bar, out_col, row0, lane);
+                if (kEpi == kEpiAct && lane == 0 && n_cols > 64) tma_prefetch_2d(&tmRes, out_col + 64, row0);
+                if (!wait_residual(p, res_bar, res_phase)) break;
+            }
             if (!__all_sync(~0u, mbar_wait(tmem_full, acc_phase, p.err_flag, kErrTimeout, p.wait_ns))) break;
             tc_fence_after_sync();
             acc_phase ^= 1;
@@ -245,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (is_leader) mbar_arrive(tmem_empty);          // the leader's own barrier: local arrive
+                if (role.is_leader) mbar_arrive(tmem_empty);          // the leader's own barrier: local arrive
                 else mbar_arrive_remote(leader_tmem_empty);
             }
 
@@ -259,11 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // One output chunk: 64 columns of the warp's 128 accumulator
                 // columns, gate and up side by side in one thread's registers.
                 if (n_cols > 0) {                               // uniform across the warp
-                    if (kFull && p.residual != nullptr) {
-                        if (!__all_sync(~0u, mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns))) break;
-                        res_phase ^= 1;
-                        res_pending = false;
-                    } else {
+                    if (!use_res) {                             // (with a residual: waited for at its request)
                         if (lane == 0) bulk_wait_group_read<0>();
                         __syncwarp();
                     }
@@ -271,23 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int ch = 0; ch < kEpiCols / 32; ++ch) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {               // eight output columns each
-                            float v[16], o[8];
-#pragma unroll
-                            for (int j = 0; j < 16; j += 2) {
-                                float b0 = 0.0f, b1 = 0.0f;
-                                if (use_bias) {
-                                    const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + g * 16 + j);
-                                    b0 = __uint_as_float(bw << 16);
-                                    b1 = __uint_as_float(bw & 0xFFFF0000u);
-                                }
-                                v[j] = __fmaf_rn(__uint_as_float(acc_regs[ch][g * 16 + j]), alpha, b0);
-                                v[j + 1] = __fmaf_rn(__uint_as_float(acc_regs[ch][g * 16 + j + 1]), alpha, b1);
-                            }
+                            uint64_t v[8], o[4];
+                            scale_bias(v, acc_regs[ch] + g * 16, alpha, use_bias ? s_bias + ch * 32 + g * 16 : nullptr);
                             apply_gate(o, v, actp);
                             const uint32_t at = out_stage + lane * 128 + (((ch * 2 + g) ^ (lane & 7)) << 4);
-                            if (kFull && p.residual != nullptr) add_residual8(o, ld_shared_v4(at));
-                            st_shared_v4(at, bf16x2_rn(o[0], o[1]), bf16x2_rn(o[2], o[3]), bf16x2_rn(o[4], o[5]),
-                                         bf16x2_rn(o[6], o[7]));
+                            if (use_res) add_residual8(o, ld_shared_v4(at));
+                            const uint4 w = bf16x8_of(o);
+                            st_shared_v4(at, w.x, w.y, w.z, w.w);
                         }
                     }
                     store_chunk<kFull>(p, &tmOut, out_stage, out_col, row0, lane, out_policy);
@@ -299,18 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < kEpiCols / 64; ++c) {
                 if (c * 64 < n_cols) {                          // uniform across the warp
-                    if (kFull && p.residual != nullptr) {
-                        if (c > 0) {                            // (chunk 0 was requested before the accumulator's wait)
-                            request_residual(&tmRes, smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes, my_res,
-                                             out_col + c * 64, row0, lane);
-                            res_pending = true;
+                    if (use_res) {
+                        if (c > 0) {                            // (the first was waited for before the accumulator)
+                            request_residual(&tmRes, chunk, res_bar, out_col + c * 64, row0, lane);
+                            res_ok = wait_residual(p, res_bar, res_phase);
+                            if (!res_ok) break;
                         }
-                        res_ok = __all_sync(~0u, mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns));
-                        if (!res_ok) break;
-                        res_phase ^= 1;
-                        res_pending = false;
                     } else {
-                        if (lane == 0) bulk_wait_group_read<0>();   // the previous store has read the buffer
+                        if (lane == 0) bulk_wait_group_read<0>();   // the previous store has read the chunk
                         __syncwarp();
                     }
 #pragma unroll
@@ -319,24 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (kEpi == kEpiAct) {
 #pragma unroll
                             for (int j4 = 0; j4 < 4; ++j4) {
-                                float o8[8];
-#pragma unroll
-                                for (int e = 0; e < 8; e += 2) {
-                                    const int j = j4 * 8 + e;
-                                    float b0 = 0.0f, b1 = 0.0f;
-                                    if (use_bias) {
-                                        const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
-                                        b0 = __uint_as_float(bw << 16);
-                                        b1 = __uint_as_float(bw & 0xFFFF0000u);
-                                    }
-                                    o8[e] = __fmaf_rn(__uint_as_float(acc_regs[ch][j]), alpha, b0);
-                                    o8[e + 1] = __fmaf_rn(__uint_as_float(acc_regs[ch][j + 1]), alpha, b1);
-                                }
-                                apply_act(o8, actp);
+                                uint64_t o[4];
+                                scale_bias(o, acc_regs[ch] + j4 * 8, alpha, use_bias ? s_bias + ch * 32 + j4 * 8 : nullptr);
+                                apply_act(o, actp);
                                 const uint32_t at = out_stage + lane * 128 + (((h * 4 + j4) ^ (lane & 7)) << 4);
-                                if (kFull && p.residual != nullptr) add_residual8(o8, ld_shared_v4(at));
-                                st_shared_v4(at, bf16x2_rn(o8[0], o8[1]), bf16x2_rn(o8[2], o8[3]),
-                                             bf16x2_rn(o8[4], o8[5]), bf16x2_rn(o8[6], o8[7]));
+                                if (use_res) add_residual8(o, ld_shared_v4(at));
+                                const uint4 w = bf16x8_of(o);
+                                st_shared_v4(at, w.x, w.y, w.z, w.w);
                             }
                         } else {
                             uint32_t pk[16];
@@ -363,13 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();                                       // every lane has read the bias buffer
-            if (!res_ok) break;
+            if (kFull && !res_ok) break;
         }
-        if constexpr (kFull)                                    // (after an expired wait) nothing may land after the exit
-            if (res_pending) mbar_wait(my_res, res_phase, p.err_flag, kErrTimeout, p.wait_ns);
         if (lane == 0) bulk_wait_group<0>();                    // all output written before the CTA exits
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
+        const Role role = enter_role(p, tmem_slot);
+        const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
+        const uint32_t tmem = role.tmem;
         // ----------------------------------------------- scale staging --
         // tcgen05.cp 32x128b.warpx4 layout: lane 32q + i of quarter q gets
         // bytes [16i, 16i + 16) of each 512-byte scale tile.  A stage's TMEM
@@ -383,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int tile = pair_id; tile < num_tiles && ok; tile += num_pairs) {
-            for (int ks = 0; ks < num_ks; ++ks) {
+        for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
+            for (int ks = 0; ks < role.num_ks; ++ks) {
                 ok = __all_sync(~0u, mbar_wait(&sf_full[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
                 if (!ok) break;
                 constexpr int kT = kSfTilesPerStage<kMx>;
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 __syncwarp();
                 if (lane == 0) {
-                    if (is_leader) mbar_arrive(&sf_ready[stage]);      // the leader's own barrier: local arrive
+                    if (role.is_leader) mbar_arrive(&sf_ready[stage]);      // the leader's own barrier: local arrive
                     else mbar_arrive_remote(leader_sf_ready + stage * (uint32_t)sizeof(uint64_t));
                 }
                 if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -433,6 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         setmaxnreg_dec<kRegsCtl>();
+        const Role role = enter_role(p, tmem_slot);
+        const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
+        const uint32_t rank = role.rank, tmem = role.tmem;
         if ((warp == 0 || warp == 3) && lane == 0 && !p.drill) {   // (a timeout drill issues no copies)
             // ---------------------------------------------- operand producers --
             // Two threads per CTA fill the operand ring, each with its half of
@@ -447,10 +445,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             uint32_t issued_mask = 0, issued_phase = 0;
             bool ok = true;
-            for (int tile = pair_id; tile < num_tiles && ok; tile += num_pairs) {
+            for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
                 const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
                 const int band_a = t.mb * 2 + (int)rank;
-                for (int ks = 0; ks < num_ks; ++ks) {
+                for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
                         ok = false;
                         break;
@@ -489,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             uint32_t issued_mask = 0, issued_phase = 0;
             bool ok = true;
-            for (int tile = pair_id; tile < num_tiles && ok; tile += num_pairs) {
+            for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
                 const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
                 const int band_a = t.mb * 2 + (int)rank;
-                const bool a_here = band_a < a_bands;
-                for (int ks = 0; ks < num_ks; ++ks) {
+                const bool a_here = band_a < (p.m + 127) / 128;
+                for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&sf_empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
                         ok = false;
                         break;
@@ -513,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < kStages; ++s)
                 if (issued_mask & (1u << s))
                     mbar_wait(&sf_full[s], (issued_phase >> s) & 1u, p.err_flag, kErrTimeout, p.wait_ns);
-        } else if (warp == 1 && is_leader) {
+        } else if (warp == 1 && role.is_leader) {
             // ---------------------------------------------------- MMA (leader) --
             // The whole warp runs the loop (warp-uniform values); one elected
             // lane issues the MMAs and commits for both CTAs.
@@ -524,11 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t b_base = smem_u32(smem + kOffB);
             const uint32_t idesc = idesc_nvf4(kTileM, kTileN);
             bool ok = true;
-            for (int tile = pair_id; tile < num_tiles && ok; tile += num_pairs) {
+            for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
                 if (!__all_sync(~0u, mbar_wait(tmem_empty, acc_phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)))
                     break;
                 tc_fence_after_sync();
-                for (int ks = 0; ks < num_ks; ++ks) {
+                for (int ks = 0; ks < role.num_ks; ++ks) {
                     // the stage's scales in both CTAs' TMEM, its operands in both
                     // CTAs' shared memory
                     if (!__all_sync(~0u, mbar_wait(&sf_ready[stage], phase, p.err_flag, kErrTimeout, p.wait_ns))) {
@@ -569,22 +567,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();                       // reconverge the role lanes before the aligned cluster barrier
     cluster_sync_all();                 // no peer access to this CTA's smem or TMEM after this point
     tc_fence_after_sync();
-    if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+    if (warp == 1) tmem_dealloc_pair(*tmem_slot, kTmemCols);
 }
 
 using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
                             const CUtensorMap, const GemmParams);
-constexpr PairKernel kPairKernels[] = {                  // [instance * 2 + MXFP4]
-    gemm_nvf4_pair_kernel<false, kEpiPlain, false>, gemm_nvf4_pair_kernel<true, kEpiPlain, false>,
-    gemm_nvf4_pair_kernel<false, kEpiAct, false>,   gemm_nvf4_pair_kernel<true, kEpiAct, false>,
-    gemm_nvf4_pair_kernel<false, kEpiGated, false>, gemm_nvf4_pair_kernel<true, kEpiGated, false>,
-    gemm_nvf4_pair_kernel<false, kEpiAct, true>,    gemm_nvf4_pair_kernel<true, kEpiAct, true>,
-    gemm_nvf4_pair_kernel<false, kEpiGated, true>,  gemm_nvf4_pair_kernel<true, kEpiGated, true>};
 
-int pair_instance(const GemmParams &p)
+struct PairInstance {
+    PairKernel kernel[2];                                // [MXFP4]
+};
+
+template <int kEpi, bool kFull>
+constexpr PairInstance instance_of()
+{
+    return {{gemm_nvf4_pair_kernel<false, kEpi, kFull>, gemm_nvf4_pair_kernel<true, kEpi, kFull>}};
+}
+
+constexpr PairInstance kPairInstances[] = {instance_of<kEpiPlain, false>(), instance_of<kEpiAct, false>(),
+                                           instance_of<kEpiGated, false>(), instance_of<kEpiAct, true>(),
+                                           instance_of<kEpiGated, true>()};
+
+const PairInstance &pair_instance(const GemmParams &p)
 {
     const int v = epilogue_variant(p);
-    return epilogue_full(p) ? v + 2 : v;                 // (v is kEpiAct or kEpiGated when full)
+    return kPairInstances[epilogue_full(p) ? v + 2 : v]; // (v is kEpiAct or kEpiGated when full)
 }
 
 }  // namespace
@@ -597,10 +603,11 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        for (PairKernel k : kPairKernels) {
-            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-            if (e != cudaSuccess) return e;
-        }
+        for (const PairInstance &i : kPairInstances)
+            for (PairKernel k : i.kernel) {
+                cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                if (e != cudaSuccess) return e;
+            }
         cudaLaunchConfig_t probe = {};
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -613,7 +620,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         probe.attrs = &attr;
         probe.numAttrs = 1;
         int clusters = 0;
-        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kPairKernels[0], &probe);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kPairInstances[0].kernel[0], &probe);
         if (e != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             clusters = num_sms / 2;
@@ -666,7 +673,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = dependent ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kPairKernels[pair_instance(p) * 2 + p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
+    return cudaLaunchKernelEx(&cfg, pair_instance(p).kernel[p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
 }
 
 }  // namespace nvfp4
