@@ -140,22 +140,18 @@ __device__ __forceinline__ void apply_gate(uint64_t (&o)[N], const uint64_t (&v)
     }
 }
 
-// alpha * acc + bias of N pairs of consecutive columns; s_bias: the bf16 biases of
-// the first one on (nullptr: none).
-template <int N>
-__device__ __forceinline__ void scale_bias(uint64_t (&v)[N], const uint32_t *acc, float alpha, const uint16_t *s_bias)
+// alpha * acc + bias of eight consecutive columns; s_bias: their biases in shared
+// memory, 16-byte aligned (not read without use_bias).
+__device__ __forceinline__ void scale_bias8(uint64_t *v, const uint32_t *acc, float alpha, const uint16_t *s_bias,
+                                            bool use_bias)
 {
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (use_bias) b = *reinterpret_cast<const uint4 *>(s_bias);
+    const uint32_t w[4] = {b.x, b.y, b.z, b.w};
     const uint64_t al = pack2(alpha, alpha);
-    if (s_bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = fma2(pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1])), al,
-                        bf16x2_to_f32x2(reinterpret_cast<const uint32_t *>(s_bias)[i]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = mul2(pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1])), al);
-    }
+    for (int i = 0; i < 4; ++i)
+        v[i] = fma2(pack2(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1])), al, bf16x2_to_f32x2(w[i]));
 }
 
 // o[i] += the i-th of four bf16 pairs packed in `w`.

@@ -505,14 +505,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // eight output columns at a time (sixteen accumulator columns when gated)
 #pragma unroll
                     for (int g = 0; g < kOutChunk / 8; ++g) {
-                        const uint16_t *gb = use_bias ? s_bias + ch * 32 + g * (kEpi == kEpiGated ? 16 : 8) : nullptr;
+                        const uint16_t *gb = s_bias + ch * 32 + g * (kEpi == kEpiGated ? 16 : 8);
                         uint64_t v[4];
                         if constexpr (kEpi == kEpiGated) {
                             uint64_t in[8];
-                            scale_bias(in, cur + g * 16, alpha, gb);
+                            scale_bias8(in, cur + g * 16, alpha, gb, use_bias);
+                            scale_bias8(in + 4, cur + g * 16 + 8, alpha, gb + 8, use_bias);
                             apply_gate(v, in, actp);
                         } else {
-                            scale_bias(v, cur + g * 8, alpha, gb);
+                            scale_bias8(v, cur + g * 8, alpha, gb, use_bias);
                             if constexpr (kEpi == kEpiAct) apply_act(v, actp);
                         }
                         if constexpr (kEpi != kEpiPlain) add_residual8(v, res[g]);

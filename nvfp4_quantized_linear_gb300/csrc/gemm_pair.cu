@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {               // eight output columns each
                             uint64_t v[8], o[4];
-                            scale_bias(v, acc_regs[ch] + g * 16, alpha, use_bias ? s_bias + ch * 32 + g * 16 : nullptr);
+                            scale_bias8(v, acc_regs[ch] + g * 16, alpha, s_bias + ch * 32 + g * 16, use_bias);
+                            scale_bias8(v + 4, acc_regs[ch] + g * 16 + 8, alpha, s_bias + ch * 32 + g * 16 + 8, use_bias);
                             apply_gate(o, v, actp);
                             const uint32_t at = out_stage + lane * 128 + (((ch * 2 + g) ^ (lane & 7)) << 4);
                             if (use_res) add_residual8(o, ld_shared_v4(at));
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int j4 = 0; j4 < 4; ++j4) {
                                 uint64_t o[4];
-                                scale_bias(o, acc_regs[ch] + j4 * 8, alpha, use_bias ? s_bias + ch * 32 + j4 * 8 : nullptr);
+                                scale_bias8(o, acc_regs[ch] + j4 * 8, alpha, s_bias + ch * 32 + j4 * 8, use_bias);
                                 apply_act(o, actp);
                                 const uint32_t at = out_stage + lane * 128 + (((h * 4 + j4) ^ (lane & 7)) << 4);
                                 if (use_res) add_residual8(o, ld_shared_v4(at));
