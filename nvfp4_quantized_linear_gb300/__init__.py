@@ -116,6 +116,8 @@ def build(force: bool = False) -> str:
 def load_library():
     """Load ``libnvfp4_gb300.so`` (raises if it has not been built)."""
     global _lib
+    if _lib is not None:                 # every call passes here: no lock once loaded
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -138,17 +140,23 @@ def _check(status: int):
 
 def _ptr(t):
     """Device pointer of a tensor (None -> NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
 
+_current_stream = None                   # () -> handle of torch's current stream
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            # the handle itself where torch has the call: a Stream object per launch costs 2 us
+            _current_stream = (lambda: raw(dev())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
