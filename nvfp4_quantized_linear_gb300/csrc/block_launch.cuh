@@ -22,7 +22,12 @@ struct NormQuantParams {
     int32_t m, k, kp, nb, nbp, mp;           // as in QuantParams, nb in the format's blocks
     const float *gs;                         // device fp32 (NVFP4)
     uint8_t *q, *sf;
+    unsigned int *err_flag;                  // device error word (bounded waits)
 };
+
+// Shared memory of an SM that the norm's row rings may take, and rows of a ring.
+constexpr uint32_t kNormRingBytes = 200 * 1024;
+constexpr int kNormMaxStages = 4;
 
 cudaError_t launch_norm_quant(const NormQuantParams &p, int num_sms, cudaStream_t s);
 
