@@ -14,6 +14,7 @@
 
 #include "block_launch.cuh"
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "quant_core.cuh"
 #include "scale_math.cuh"
@@ -38,15 +39,33 @@ __device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float 
     return cvt_e4m3x2(b, a) | (cvt_e4m3x2(d, c) << 16);
 }
 
-// fp32 of the 16 bf16 at row[k0 ..], zero past k or without a row.
-__device__ __forceinline__ void load_row16(float (&v)[16], const uint16_t *row, int k0, int k, bool ok)
+// A thread's 16 values as eight fp32 pairs (packed arithmetic, epilogue.cuh).
+using Pairs = uint64_t[8];
+
+__device__ __forceinline__ void pairs_of(Pairs &v, const Raw16 &r)
 {
-    const Raw16 r = load16(row, k0, k, ok);
-    float a[8], b[8];
-    unpack8(r.a, a);
-    unpack8(r.b, b);
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { v[i] = a[i]; v[8 + i] = b[i]; }
+    for (int i = 0; i < 8; ++i) v[i] = bf16x2_to_f32x2(w[i]);
+}
+
+// h (+)= residual, and its sum of squares.
+__device__ __forceinline__ void add_pairs(Pairs &h, const Raw16 &r)
+{
+    Pairs v;
+    pairs_of(v, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = add2(h[i], v[i]);
+}
+
+__device__ __forceinline__ float sum_squares(const Pairs &h, float sum)
+{
+    uint64_t s = pack2(sum, 0.0f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fma2(h[i], h[i], s);
+    float lo, hi;
+    unpack2(s, lo, hi);
+    return lo + hi;
 }
 
 // Sum over the block of one value per thread, the same in every thread and in
@@ -57,14 +76,15 @@ __device__ __forceinline__ float block_sum(float v, float *part)
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    float total = 0.0f;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) total += part[w];
-    return total;
+    v = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
 }
 
 __device__ __forceinline__ float rstd_of(float sum, const NormQuantParams &p)
 {
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)p.k) + p.eps));
+    return __frsqrt_rn(__fdiv_rn(sum, (float)p.k) + p.eps);
 }
 
 __device__ __forceinline__ void zero_scale_row(const NormQuantParams &p, int row)
@@ -74,56 +94,58 @@ __device__ __forceinline__ void zero_scale_row(const NormQuantParams &p, int row
 }
 
 // The second half of a row's work for one thread's 16 elements at k0: h, then
-// y = h * rstd * gamma into codes and a scale.
+// y = (h * rstd) * gamma into codes and a scale.
 template <int kFmt>
-__device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int k0, const float (&h)[16], float rstd,
-                                         const float (&g)[16], float gs)
+__device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int k0, const Pairs &h, float rstd,
+                                         const Raw16 &gamma, float gs)
 {
     if (p.h != nullptr && k0 < p.k) {
         uint16_t *o = p.h + (int64_t)row * p.ldh + k0;
-        if (k0 + 16 <= p.k) {
+        uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<uint4 *>(o + 8 * i) =
-                    make_uint4(bf16x2_rn(h[8 * i], h[8 * i + 1]), bf16x2_rn(h[8 * i + 2], h[8 * i + 3]),
-                               bf16x2_rn(h[8 * i + 4], h[8 * i + 5]), bf16x2_rn(h[8 * i + 6], h[8 * i + 7]));
+        for (int i = 0; i < 8; ++i) w[i] = bf16x2_of(h[i]);
+        if (k0 + 16 <= p.k) {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (k0 + i < p.k) o[i] = (uint16_t)bf16x2_rn(h[i], 0.0f);
+                if (k0 + i < p.k) o[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
         }
     }
-    float y0[8], y1[8];
+    Pairs y;
+    pairs_of(y, gamma);
+    const uint64_t rs = pack2(rstd, rstd);
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y0[i] = h[i] * rstd * g[i];
-        y1[i] = h[8 + i] * rstd * g[8 + i];
-        amax = max_abs3(amax, y0[i], y1[i]);
+        y[i] = mul2(mul2(h[i], rs), y[i]);
+        float lo, hi;
+        unpack2(y[i], lo, hi);
+        amax = max_abs3(amax, lo, hi);
     }
     uint32_t code;
+    float mul;                                            // y * mul is rounded to the element format
     if constexpr (kFmt == kFmtNvfp4) {
         code = cvt_e4m3x2(0.0f, div6_rn(__fmul_rn(amax, gs))) & 0x7Fu;
         const float d = e4m3_to_f32(code);
-        const float inv = d == 0.0f ? 0.0f : __fdiv_rn(gs, d);
-        if (k0 < p.kp)
-            *reinterpret_cast<uint2 *>(p.q + (int64_t)row * (p.kp / 2) + k0 / 2) =
-                make_uint2(quant8(y0, inv), quant8(y1, inv));
+        mul = d == 0.0f ? 0.0f : __fdiv_rn(gs, d);
     } else {
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));      // the block's other half
         code = kFmt == kFmtMxfp8 ? mx8_scale_code(amax) : mx_scale_code(amax);
-        const float mul = mx_scale_mul(code);
-        if (k0 < p.kp) {
-            if constexpr (kFmt == kFmtMxfp8) {
+        mul = mx_scale_mul(code);
+    }
+    if (k0 < p.kp) {
+        float v[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) { y0[i] *= mul; y1[i] *= mul; }
-                *reinterpret_cast<uint4 *>(p.q + (int64_t)row * p.kp + k0) =
-                    make_uint4(cvt_e4m3x4(y0[0], y0[1], y0[2], y0[3]), cvt_e4m3x4(y0[4], y0[5], y0[6], y0[7]),
-                               cvt_e4m3x4(y1[0], y1[1], y1[2], y1[3]), cvt_e4m3x4(y1[4], y1[5], y1[6], y1[7]));
-            } else {
-                *reinterpret_cast<uint2 *>(p.q + (int64_t)row * (p.kp / 2) + k0 / 2) =
-                    make_uint2(quant8(y0, mul), quant8(y1, mul));
-            }
+        for (int i = 0; i < 8; ++i) unpack2(mul2(y[i], pack2(mul, mul)), v[2 * i], v[2 * i + 1]);
+        if constexpr (kFmt == kFmtMxfp8) {
+            *reinterpret_cast<uint4 *>(p.q + (int64_t)row * p.kp + k0) =
+                make_uint4(cvt_e4m3x4(v[0], v[1], v[2], v[3]), cvt_e4m3x4(v[4], v[5], v[6], v[7]),
+                           cvt_e4m3x4(v[8], v[9], v[10], v[11]), cvt_e4m3x4(v[12], v[13], v[14], v[15]));
+        } else {
+            *reinterpret_cast<uint2 *>(p.q + (int64_t)row * (p.kp / 2) + k0 / 2) =
+                make_uint2(cvt_e2m1x8(*reinterpret_cast<float(*)[8]>(v)), cvt_e2m1x8(*reinterpret_cast<float(*)[8]>(v + 8)));
         }
     }
     // four consecutive scale codes as one word: the blocks of 4 lanes
@@ -153,30 +175,43 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantParams 
     }
     const uint16_t *x = p.x + (int64_t)row * p.ldx;
     const uint16_t *res = p.residual != nullptr ? p.residual + (int64_t)row * p.ldr : nullptr;
-    float h[U][16];
+    Pairs h[U];
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        load_row16(h[u], x, k0, p.k, k0 < p.k);
-        if (res != nullptr) {
-            float r[16];
-            load_row16(r, res, k0, p.k, k0 < p.k);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) h[u][i] += r[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum = __fmaf_rn(h[u][i], h[u][i], sum);
+        pairs_of(h[u], load16(x, k0, p.k, k0 < p.k));
+        if (res != nullptr) add_pairs(h[u], load16(res, k0, p.k, k0 < p.k));
+        sum = sum_squares(h[u], sum);
     }
     const float gs = kFmt == kFmtNvfp4 ? __ldg(p.gs) : 1.0f;
     const float rstd = rstd_of(block_sum(sum, s_part), p);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        float g[16];
-        load_row16(g, p.gamma, k0, p.k, k0 < p.k);
-        finish16<kFmt>(p, row, k0, h[u], rstd, g, gs);
+        finish16<kFmt>(p, row, k0, h[u], rstd, load16(p.gamma, k0, p.k, k0 < p.k), gs);
     }
+}
+
+// The 16 bf16 of a copied row at k0; a row's last 16-byte piece holds bytes past k.
+__device__ __forceinline__ Raw16 ring16(const uint8_t *row, int k0, int k)
+{
+    Raw16 r;
+    r.a = r.b = make_uint4(0, 0, 0, 0);
+    if (k0 + 16 <= k) {
+        r.a = *reinterpret_cast<const uint4 *>(row + 2 * k0);
+        r.b = *reinterpret_cast<const uint4 *>(row + 2 * k0 + 16);
+    } else if (k0 < k) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t v = k0 + 2 * i < k ? *reinterpret_cast<const uint32_t *>(row + 2 * k0 + 4 * i) : 0u;
+            w[i] = k0 + 2 * i + 1 < k ? v : v & 0xFFFFu;
+        }
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return r;
 }
 
 // Persistent CTAs over the rows, the next rows' x and residual arriving in a ring
@@ -210,12 +245,11 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
     const int step = gridDim.x;
     if (tid == 0)
         for (int s = 0; s < stages && (int)blockIdx.x + s * step < p.m; ++s) request(blockIdx.x + s * step, s);
-    uint4 gamma[U][2];
+    Raw16 gamma[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const Raw16 g = load16(p.gamma, (u * blockDim.x + tid) * 16, p.k, (int)(u * blockDim.x + tid) * 16 < p.k);
-        gamma[u][0] = g.a;
-        gamma[u][1] = g.b;
+        const int k0 = (u * blockDim.x + tid) * 16;
+        gamma[u] = load16(p.gamma, k0, p.k, k0 < p.k);
     }
     const float gs = kFmt == kFmtNvfp4 ? __ldg(p.gs) : 1.0f;
     for (int row = p.m + blockIdx.x; row < p.mp; row += step) zero_scale_row(p, row);
@@ -232,49 +266,21 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
             return;
         }
         const uint8_t *xs = ring + s * stage_bytes;
-        float h[U][16];
+        Pairs h[U];
         float sum = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k0 = (u * blockDim.x + tid) * 16;
-            float v[8];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int c = k0 + 8 * half;
-                if (c < p.k) {
-                    unpack8(*reinterpret_cast<const uint4 *>(xs + 2 * c), v);
-                    if (use_res) {
-                        float r[8];
-                        unpack8(*reinterpret_cast<const uint4 *>(xs + row_bytes + 2 * c), r);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] += r[i];
-                    }
-                    if (c + 8 > p.k)                     // the row's last piece holds bytes past k
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c + i >= p.k) v[i] = 0.0f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    h[u][8 * half + i] = v[i];
-                    sum = __fmaf_rn(v[i], v[i], sum);
-                }
-            }
+            pairs_of(h[u], ring16(xs, k0, p.k));
+            if (use_res) add_pairs(h[u], ring16(xs + row_bytes, k0, p.k));
+            sum = sum_squares(h[u], sum);
         }
         // after the sum's barrier every thread has read the stage: refill it
         const float rstd = rstd_of(block_sum(sum, s_part[it & 1]), p);
         if (tid == 0 && row + stages * step < p.m) request(row + stages * step, s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float g[16], a[8], b[8];
-            unpack8(gamma[u][0], a);
-            unpack8(gamma[u][1], b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) { g[i] = a[i]; g[8 + i] = b[i]; }
-            finish16<kFmt>(p, row, (u * blockDim.x + tid) * 16, h[u], rstd, g, gs);
+            finish16<kFmt>(p, row, (u * blockDim.x + tid) * 16, h[u], rstd, gamma[u], gs);
         }
         if (++s == stages) { s = 0; phase ^= 1; }
     }
