@@ -13,6 +13,7 @@
 
 #include "block_launch.cuh"
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "quant_core.cuh"
 #include "scale_math.cuh"
@@ -21,6 +22,8 @@ namespace nvfp4 {
 namespace {
 
 using namespace quant_core;
+
+constexpr int kAloneTiles = 2;      // up to here one block sorts alone
 
 // ------------------------------------------------------------------- sort ----
 // A stable counting sort.  Block b owns a range of whole 1024-assignment tiles.
@@ -42,7 +45,9 @@ template <typename Id>
 __global__ void __launch_bounds__(kMoeSortTile) moe_count_kernel(const MoeSortParams p, int tiles_per_block)
 {
     __shared__ int s_count[kMoeMaxExperts];
+    griddep_launch_dependents();
     for (int e = threadIdx.x; e < p.experts; e += kMoeSortTile) s_count[e] = 0;
+    griddep_wait();
     __syncthreads();
     for (int t = 0; t < tiles_per_block; ++t) {
         const int64_t i = ((int64_t)blockIdx.x * tiles_per_block + t) * kMoeSortTile + threadIdx.x;
@@ -53,21 +58,48 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_count_kernel(const MoeSortPa
     for (int e = threadIdx.x; e < p.experts; e += kMoeSortTile) p.hist[(int64_t)blockIdx.x * p.experts + e] = s_count[e];
 }
 
-template <typename Id>
+// kAlone: one block sorts everything, and counts for itself (few assignments: one
+// launch instead of two).
+template <typename Id, bool kAlone>
 __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortParams p, int tiles_per_block)
 {
     extern __shared__ uint16_t s_warp[];                 // [32 warps][experts] counts of a tile
     __shared__ int s_next[kMoeMaxExperts];               // next row of each expert for this block
+    __shared__ int s_total[kMoeMaxExperts];
     __shared__ int s_scan[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int experts = p.experts;
-    int before = 0, total = 0;                           // expert tid: rows of earlier blocks, of all
-    if (tid < experts)
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-            const int c = p.hist[(int64_t)b * experts + tid];
-            if (b < (int)blockIdx.x) before += c;
-            total += c;
+    griddep_launch_dependents();
+    for (int e = tid; e < experts; e += kMoeSortTile) s_next[e] = s_total[e] = 0;
+    const int64_t first = (int64_t)blockIdx.x * tiles_per_block * kMoeSortTile;
+    griddep_wait();
+    int id0 = load_id<Id>(p.ids, first + tid, p.n, experts);      // the first tile's, with the counts in flight
+    __syncthreads();
+    if constexpr (kAlone) {
+        if (id0 >= 0) atomicAdd(&s_total[id0], 1);
+        for (int t = 1; t < tiles_per_block; ++t) {
+            const int id = load_id<Id>(p.ids, first + t * kMoeSortTile + tid, p.n, experts);
+            if (id >= 0) atomicAdd(&s_total[id], 1);
         }
+    } else {
+        // column sums of hist: `groups` threads per expert, each a share of the
+        // blocks (integer adds: their order does not matter)
+        const int width = (experts + 31) / 32 * 32, groups = kMoeSortTile / width;
+        const int e = tid % width, g = tid / width;
+        if (e < experts && g < groups) {
+            int before = 0, total = 0;
+#pragma unroll 8
+            for (int b = g; b < (int)gridDim.x; b += groups) {
+                const int c = p.hist[(int64_t)b * experts + e];
+                before += b < (int)blockIdx.x ? c : 0;
+                total += c;
+            }
+            if (total) atomicAdd(&s_total[e], total);
+            if (before) atomicAdd(&s_next[e], before);
+        }
+    }
+    __syncthreads();
+    const int total = tid < experts ? s_total[tid] : 0;
     const int padded = (total + 127) / 128 * 128;
     int incl = padded;
 #pragma unroll
@@ -77,11 +109,12 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortPa
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += s_scan[w];
+    int base = lane < warp ? s_scan[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(kFull, base, o);
     const int offset = base + incl - padded;
     if (tid < experts) {
-        s_next[tid] = offset + before;
+        s_next[tid] += offset;
         if (blockIdx.x == 0) {
             p.offsets[tid] = offset;
             p.counts[tid] = total;
@@ -89,27 +122,27 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortPa
         }
     }
     for (int t = 0; t < tiles_per_block; ++t) {
-        const int64_t i = ((int64_t)blockIdx.x * tiles_per_block + t) * kMoeSortTile + tid;
-        for (int j = tid; j < 32 * experts; j += kMoeSortTile) s_warp[j] = 0;
+        const int64_t i = first + t * kMoeSortTile + tid;
+        for (int j = tid; j < 16 * experts; j += kMoeSortTile) reinterpret_cast<uint32_t *>(s_warp)[j] = 0;
         __syncthreads();
-        const int id = load_id<Id>(p.ids, i, p.n, experts);
+        const int id = t == 0 ? id0 : load_id<Id>(p.ids, i, p.n, experts);
         const unsigned peers = __match_any_sync(kFull, id);
         const int rank = __popc(peers & ((1u << lane) - 1));
         if (id >= 0 && rank == 0) s_warp[warp * experts + id] = (uint16_t)__popc(peers);
         __syncthreads();
-        if (tid < experts) {                             // exclusive prefix over the warps; advance the expert
-            int run = 0;
+        int run = 0;
+        if (tid < experts) {                             // exclusive prefix over the warps
+#pragma unroll 8
             for (int w = 0; w < 32; ++w) {
                 const int c = s_warp[w * experts + tid];
                 s_warp[w * experts + tid] = (uint16_t)run;
                 run += c;
             }
-            total = run;
         }
         __syncthreads();
         if (i < p.n) p.dest[i] = id < 0 ? -1 : s_next[id] + s_warp[warp * experts + id] + rank;
         __syncthreads();
-        if (tid < experts) s_next[tid] += total;
+        if (tid < experts) s_next[tid] += run;           // advance the experts past the tile
     }
 }
 
@@ -142,31 +175,50 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int h, const uint4 
 // p.rows rows does not hold).
 __device__ __forceinline__ int row_of(const MoeRowsParams &p, int64_t assignment)
 {
-    const int d = __ldg(p.dest + assignment);
+    const int d = p.dest[assignment];
     return d < p.rows ? d : -1;
 }
 
-__device__ __forceinline__ void zero_padding_rows(const MoeRowsParams &p, int e)
+// Zeros into a share of the padding rows (fewer than 128) of a group: item
+// e * kPadSlices + j takes rows j, j + kPadSlices, ... of group e's.
+constexpr int kPadSlices = 16;
+
+__device__ __forceinline__ void zero_padding_rows(const MoeRowsParams &p, int item)
 {
+    const int e = item / kPadSlices;
     const int first = max(0, p.offsets[e] + p.counts[e]), end = min(p.offsets[e + 1], p.rows);
-    for (int r = first; r < end; ++r)
+    for (int r = first + item % kPadSlices; r < end; r += kPadSlices)
         for (int c = threadIdx.x * 8; c < p.h; c += blockDim.x * 8)
             store8(p.out + (int64_t)r * p.ldo, c, p.h, make_uint4(0, 0, 0, 0));
 }
 
+// The rows of up to 8 assignments from `first` on, by lane (< 8; -1 past `count`).
+__device__ __forceinline__ int rows_by_lane(const MoeRowsParams &p, int64_t first, int count)
+{
+    const int lane = threadIdx.x & 31;
+    return lane < min(count, 8) ? row_of(p, first + lane) : -1;
+}
+
 __global__ void __launch_bounds__(256) moe_dispatch_kernel(const MoeRowsParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     if ((int)blockIdx.x >= p.tokens) {
         zero_padding_rows(p, blockIdx.x - p.tokens);
         return;
     }
     const int64_t first = (int64_t)blockIdx.x * p.topk;     // the token's assignments
     const uint16_t *x = p.x + (int64_t)blockIdx.x * p.ldx;
-    for (int c = threadIdx.x * 8; c < p.h; c += blockDim.x * 8) {
-        const uint4 v = load8(x, c, p.h);
-        for (int k = 0; k < p.topk; ++k) {
-            const int d = row_of(p, first + k);
-            if (d >= 0) store8(p.out + (int64_t)d * p.ldo, c, p.h, v);
+    for (int kb = 0; kb < p.topk; kb += 8) {
+        const int mine = rows_by_lane(p, first + kb, p.topk - kb);
+        for (int c0 = 0; c0 < p.h; c0 += blockDim.x * 8) {
+            const int c = c0 + threadIdx.x * 8;
+            const uint4 v = c < p.h ? load8(x, c, p.h) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int d = __shfl_sync(kFull, mine, k);
+                if (d >= 0 && c < p.h) store8(p.out + (int64_t)d * p.ldo, c, p.h, v);
+            }
         }
     }
 }
@@ -177,12 +229,14 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 {
     const int64_t first = (int64_t)blockIdx.x * p.topk;     // the token's assignments
     const uint16_t *x = p.x + (int64_t)blockIdx.x * p.ldx;
-    const float gs = __ldg(p.gs);
+    griddep_launch_dependents();
+    griddep_wait();
+    const float gs = *p.gs;
     const int steps = (p.nbp + blockDim.x - 1) / blockDim.x;
     for (int u = 0; u < steps; ++u) {
         const int blk = u * blockDim.x + threadIdx.x;
         const int k0 = blk * 16;
-        const Raw16 raw = load16(x, k0, p.h, k0 < p.h);
+        const Raw16 raw = load16_coherent(x, k0, p.h);
         float v0[8], v1[8];
         unpack8(raw.a, v0);
         unpack8(raw.b, v1);
@@ -208,88 +262,153 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 }
 
 // ---------------------------------------------------------------- combine ----
+// A block takes a token's columns, eight per thread; the rows of eight
+// assignments are requested before the first is added, so that a thread has up
+// to 128 bytes in flight.
 __global__ void __launch_bounds__(256) moe_combine_kernel(const MoeRowsParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t t = blockIdx.x;
-    for (int c = threadIdx.x * 8; c < p.h; c += blockDim.x * 8) {
-        float acc[8] = {};
-        for (int k = 0; k < p.topk; ++k) {
-            const int r = row_of(p, t * p.topk + k);
-            if (r < 0) continue;
-            float v[8];
-            unpack8(load8(p.x + (int64_t)r * p.ldx, c, p.h), v);
-            const float w = p.weights != nullptr ? p.weights[t * p.topk + k] : 1.0f;
+    const int lane = threadIdx.x & 31;
+    const int c0 = blockIdx.y * blockDim.x * 8;
+    const int c = c0 + threadIdx.x * 8;
+    const bool here = c < p.h;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (p.residual != nullptr && here) res = load8(p.residual + t * p.ldr, c, p.h);
+    uint64_t acc[4] = {0, 0, 0, 0};
+    for (int kb = 0; kb < p.topk; kb += 8) {
+        const int mine = rows_by_lane(p, t * p.topk + kb, p.topk - kb);
+        const float my_w = mine >= 0 && p.weights != nullptr ? p.weights[t * p.topk + kb + lane] : 1.0f;
+        uint4 v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(w, v[i], acc[i]);
+        for (int k = 0; k < 8; ++k) {
+            const int r = __shfl_sync(kFull, mine, k);
+            v[k] = r >= 0 && here ? load8(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
         }
-        if (p.residual != nullptr) {
-            float v[8];
-            unpack8(load8(p.residual + t * p.ldr, c, p.h), v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += v[i];
+        for (int k = 0; k < 8; ++k) {
+            const float w = __shfl_sync(kFull, my_w, k);     // (1 with zeros for a dropped assignment)
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = fma2(bf16x2_to_f32x2(u[i]), pack2(w, w), acc[i]);
         }
-        store8(p.out + t * p.ldo, c, p.h, make_uint4(bf16x2_rn(acc[0], acc[1]), bf16x2_rn(acc[2], acc[3]),
-                                                     bf16x2_rn(acc[4], acc[5]), bf16x2_rn(acc[6], acc[7])));
     }
+    if (p.residual != nullptr) add_residual8(acc, res);
+    if (here) store8(p.out + t * p.ldo, c, p.h, bf16x8_of(acc));
 }
 
-// Blocks as in moe_dispatch_kernel.  Each assignment in turn: its dot product
-// (fp32; lanes, then warps, in a fixed order) and its gradient row.
+// Blocks as in moe_dispatch_kernel.  Eight assignments at a time: their rows are
+// requested together, each thread keeps eight partial dot products, and one
+// reduction per eight (lanes, then warps, in a fixed order) ends them.
 __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const MoeRowsParams p)
 {
+    griddep_launch_dependents();
+    griddep_wait();
     if ((int)blockIdx.x >= p.tokens) {
         zero_padding_rows(p, blockIdx.x - p.tokens);
         return;
     }
-    __shared__ float s_dot[8];
+    __shared__ float s_dot[8][8];                        // [warp][assignment]
     const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *g = p.g + t * p.ldg;
-    for (int k = 0; k < p.topk; ++k) {
-        const int r = row_of(p, t * p.topk + k);
-        float dot = 0.0f;
-        if (r >= 0) {
-            const float w = p.weights[t * p.topk + k];
-            for (int c = threadIdx.x * 8; c < p.h; c += blockDim.x * 8) {
-                float a[8], y[8];
-                unpack8(load8(g, c, p.h), a);
-                unpack8(load8(p.x + (int64_t)r * p.ldx, c, p.h), y);
+    for (int kb = 0; kb < p.topk; kb += 8) {
+        const int mine = rows_by_lane(p, t * p.topk + kb, p.topk - kb);
+        const float my_w = mine >= 0 ? p.weights[t * p.topk + kb + lane] : 0.0f;
+        uint64_t dot[8] = {};
+        for (int c0 = 0; c0 < p.h; c0 += blockDim.x * 8) {
+            const int c = c0 + threadIdx.x * 8;
+            const bool here = c < p.h;
+            uint4 v[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot = __fmaf_rn(a[i], y[i], dot);
-                    a[i] *= w;
+            for (int k = 0; k < 8; ++k) {
+                const int r = __shfl_sync(kFull, mine, k);
+                v[k] = r >= 0 && here ? load8(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
+            }
+            const uint4 gv = here ? load8(g, c, p.h) : make_uint4(0, 0, 0, 0);
+            const uint64_t a[4] = {bf16x2_to_f32x2(gv.x), bf16x2_to_f32x2(gv.y), bf16x2_to_f32x2(gv.z),
+                                   bf16x2_to_f32x2(gv.w)};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = __shfl_sync(kFull, mine, k);
+                const float w = __shfl_sync(kFull, my_w, k);
+                const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                uint64_t d[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dot[k] = fma2(a[i], bf16x2_to_f32x2(u[i]), dot[k]);
+                    d[i] = mul2(a[i], pack2(w, w));
                 }
-                store8(p.out + (int64_t)r * p.ldo, c, p.h, make_uint4(bf16x2_rn(a[0], a[1]), bf16x2_rn(a[2], a[3]),
-                                                                      bf16x2_rn(a[4], a[5]), bf16x2_rn(a[6], a[7])));
+                if (r >= 0 && here) store8(p.out + (int64_t)r * p.ldo, c, p.h, bf16x8_of(d));
             }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-        if ((threadIdx.x & 31) == 0) s_dot[threadIdx.x >> 5] = dot;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float sum = 0.0f;
-            for (int w = 0; w < 8; ++w) sum += s_dot[w];
-            p.dw[t * p.topk + k] = sum;
+        for (int k = 0; k < 8; ++k) {
+            float lo, hi;
+            unpack2(dot[k], lo, hi);
+            float v = lo + hi;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+            if (lane == k) s_dot[warp][k] = v;
         }
         __syncthreads();
+        if (threadIdx.x < 8 && kb + (int)threadIdx.x < p.topk) {
+            float sum = 0.0f;
+            for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += s_dot[w][threadIdx.x];
+            p.dw[t * p.topk + kb + threadIdx.x] = mine >= 0 ? sum : 0.0f;   // (lane k holds row k)
+        }
+        if (kb + 8 < p.topk) __syncthreads();
     }
+}
+
+// Every kernel here is launched as a programmatic dependent and waits for the
+// kernel before it (griddepcontrol.wait) before it reads or writes memory.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), int64_t grid, int threads, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename Id, bool kAlone>
+cudaError_t launch_place(const MoeSortParams &p, int blocks, int per_block, cudaStream_t s)
+{
+    static int configured_device = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel<Id, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             32 * kMoeMaxExperts * (int)sizeof(uint16_t));
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    return launch_dependent(moe_place_kernel<Id, kAlone>, blocks, kMoeSortTile, (size_t)32 * p.experts * sizeof(uint16_t),
+                            s, p, per_block);
 }
 
 template <typename Id>
 cudaError_t launch_sort(const MoeSortParams &p, int num_sms, cudaStream_t s)
 {
     const int tiles = p.n > 0 ? (p.n + kMoeSortTile - 1) / kMoeSortTile : 1;   // (no tokens: the offsets are still written)
+    if (tiles <= kAloneTiles) return launch_place<Id, true>(p, 1, tiles, s);
     const int per_block = (tiles + num_sms - 1) / num_sms;
     const int blocks = (tiles + per_block - 1) / per_block;
-    const size_t smem = (size_t)32 * p.experts * sizeof(uint16_t);
-    if (smem > 48 * 1024 - sizeof(int) * (kMoeMaxExperts + 32)) {
-        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel<Id>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    moe_count_kernel<Id><<<blocks, kMoeSortTile, 0, s>>>(p, per_block);
-    moe_place_kernel<Id><<<blocks, kMoeSortTile, smem, s>>>(p, per_block);
-    return cudaGetLastError();
+    const cudaError_t e = launch_dependent(moe_count_kernel<Id>, blocks, kMoeSortTile, 0, s, p, per_block);
+    return e != cudaSuccess ? e : launch_place<Id, false>(p, blocks, per_block, s);
 }
+
+// Threads for rows of h elements, eight per thread, and column parts of a row.
+int row_threads(int h) { return h >= 2048 ? 256 : ((h + 7) / 8 + 31) / 32 * 32; }
 
 }  // namespace
 
@@ -301,29 +420,38 @@ cudaError_t launch_moe_sort(const MoeSortParams &p, int num_sms, cudaStream_t s)
 cudaError_t launch_moe_dispatch(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    moe_dispatch_kernel<<<(unsigned)(p.tokens + p.experts), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(moe_dispatch_kernel, (int64_t)p.tokens + (int64_t)p.experts * kPadSlices, row_threads(p.h), 0,
+                            s, p);
 }
 
 cudaError_t launch_moe_dispatch_quant(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    moe_dispatch_quant_kernel<<<(unsigned)p.tokens, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const int threads = p.nbp >= 256 ? 256 : (p.nbp + 31) / 32 * 32;
+    return launch_dependent(moe_dispatch_quant_kernel, p.tokens, threads, 0, s, p);
 }
 
 cudaError_t launch_moe_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    moe_combine_kernel<<<(unsigned)p.tokens, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const int threads = row_threads(p.h), parts = (p.h + threads * 8 - 1) / (threads * 8);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)parts, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, moe_combine_kernel, p);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    moe_combine_backward_kernel<<<(unsigned)(p.tokens + p.experts), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(moe_combine_backward_kernel, (int64_t)p.tokens + (int64_t)p.experts * kPadSlices,
+                            row_threads(p.h), 0, s, p);
 }
 
 }  // namespace nvfp4

@@ -180,16 +180,16 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantParams 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        pairs_of(h[u], load16(x, k0, p.k, k0 < p.k));
-        if (res != nullptr) add_pairs(h[u], load16(res, k0, p.k, k0 < p.k));
+        pairs_of(h[u], load16_coherent(x, k0, p.k));
+        if (res != nullptr) add_pairs(h[u], load16_coherent(res, k0, p.k));
         sum = sum_squares(h[u], sum);
     }
-    const float gs = kFmt == kFmtNvfp4 ? __ldg(p.gs) : 1.0f;
+    const float gs = kFmt == kFmtNvfp4 ? *p.gs : 1.0f;
     const float rstd = rstd_of(block_sum(sum, s_part), p);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        finish16<kFmt>(p, row, k0, h[u], rstd, load16(p.gamma, k0, p.k, k0 < p.k), gs);
+        finish16<kFmt>(p, row, k0, h[u], rstd, load16_coherent(p.gamma, k0, p.k), gs);
     }
 }
 
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        gamma[u] = load16(p.gamma, k0, p.k, k0 < p.k);
+        gamma[u] = load16_coherent(p.gamma, k0, p.k);
     }
-    const float gs = kFmt == kFmtNvfp4 ? __ldg(p.gs) : 1.0f;
+    const float gs = kFmt == kFmtNvfp4 ? *p.gs : 1.0f;
     for (int row = p.m + blockIdx.x; row < p.mp; row += step) zero_scale_row(p, row);
     int s = 0;
     uint32_t phase = 0;

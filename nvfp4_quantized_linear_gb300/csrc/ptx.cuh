@@ -585,6 +585,17 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p)
     return r;
 }
 
+// A coherent 16-byte load that leaves nothing in L1.
+__device__ __forceinline__ uint4 ld_global_v4(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
 // The same with an L2 eviction policy (e.g. evict-first for data read once).
 __device__ __forceinline__ uint4 ld_stream_v4(const void *p, uint64_t l2_policy)
 {

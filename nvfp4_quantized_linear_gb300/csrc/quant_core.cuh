@@ -123,6 +123,31 @@ __device__ __forceinline__ Raw16 load16(const uint16_t *row, int k0, int k, bool
     return r;
 }
 
+// The 16 bf16 at row[k0 ..], zero past k, by coherent loads: for kernels that are
+// launched as programmatic dependents of the kernel that writes them and so
+// may start before it ends (a non-coherent load promises data that is constant
+// from the kernel's start).
+__device__ __forceinline__ Raw16 load16_coherent(const uint16_t *row, int k0, int k)
+{
+    Raw16 r;
+    r.a = r.b = make_uint4(0, 0, 0, 0);
+    if (k0 + 16 <= k) {
+        r.a = ld_global_v4(row + k0);
+        r.b = ld_global_v4(row + k0 + 8);
+    } else if (k0 < k) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t lo = k0 + 2 * i < k ? row[k0 + 2 * i] : 0u;
+            const uint32_t hi = k0 + 2 * i + 1 < k ? row[k0 + 2 * i + 1] : 0u;
+            w[i] = lo | (hi << 16);
+        }
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    return r;
+}
+
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8])
 {
     v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
