@@ -155,7 +155,7 @@ __device__ __forceinline__ void scale_bias8(uint64_t *v, const uint32_t *acc, fl
 }
 
 // o[i] += the i-th of four bf16 pairs packed in `w`.
-__device__ __forceinline__ void add_residual8(uint64_t (&o)[4], const uint4 &w)
+__device__ __forceinline__ void add_residual8(uint64_t *o, const uint4 &w)
 {
     o[0] = add2(o[0], bf16x2_to_f32x2(w.x));
     o[1] = add2(o[1], bf16x2_to_f32x2(w.y));
@@ -170,7 +170,7 @@ __device__ __forceinline__ uint32_t bf16x2_of(uint64_t v)
     return bf16x2_rn(lo, hi);
 }
 
-__device__ __forceinline__ uint4 bf16x8_of(const uint64_t (&o)[4])
+__device__ __forceinline__ uint4 bf16x8_of(const uint64_t *o)
 {
     return make_uint4(bf16x2_of(o[0]), bf16x2_of(o[1]), bf16x2_of(o[2]), bf16x2_of(o[3]));
 }

@@ -86,8 +86,8 @@ constexpr int kEpiWarp0 = 8;                  // warps 8..15: epilogue, lane qua
 constexpr int kEpiWarps = 8;                  // columns [128 h, 128 h + 128) for h = (warp - 8) / 4
 constexpr int kEpiCols = kBN / 2;
 // Registers per thread after the reallocation at kernel start (launched with
-// 65536 / 512 = 128): 128 x (56 + 96 + 2 x 176) = 64512 <= 512 x 128 = 65536.
-constexpr uint32_t kRegsCtl = 56, kRegsSf = 96, kRegsEpi = 176;
+// 65536 / 512 = 128): 128 x (56 + 88 + 2 x 184) = 65536 = 512 x 128.
+constexpr uint32_t kRegsCtl = 56, kRegsSf = 88, kRegsEpi = 184;
 static_assert(128 * (kRegsCtl + kRegsSf + 2 * kRegsEpi) <= kThreads * 128, "register reallocation budget");
 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -149,6 +149,19 @@ __device__ __forceinline__ void load_residual_row(const GemmParams &p, uint4 (&r
 // Up to this many rows below m in an epilogue warp's 32, the rows are written
 // straight from registers instead of through the staging buffer and the TMA.
 constexpr int kDirectStoreRows = 16;
+// Columns [col, col + 8) of an output row (col % 8 == 0), those below `cols`.
+__device__ __forceinline__ void store_columns8(uint16_t *row, int col, int cols, const uint4 &v)
+{
+    if (col + 8 <= cols) {
+        *reinterpret_cast<uint4 *>(row + col) = v;
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (col + e < cols) row[col + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
 static_assert((uint32_t)kBM * kPartLd * 4 <= kOffSfa, "the partials fit in the idle operand ring");
 
 // Cluster split-K finish, by the 256 epilogue threads of CTA `rank` of the
@@ -456,126 +469,197 @@ __global__ void __launch_bounds__(kThreads, 1)
             // columns of this warp's slice that hold output, 0 when all of
             // its 32 rows are at or past m (small m: most warps)
             const int cols_here = p.m > row0 ? n_cols : 0;
-            uint32_t r0[32], r1[32];
+            if constexpr (kEpi == kEpiPlain) {
+                uint32_t r0[32], r1[32];
 
-            if (p.splits > 1) {
-                // split-K: raw fp32 sums of this K range for rows < m, into this
-                // CTA's shared memory (the operand ring: every stage of the
-                // CTA's one work item has been consumed)
-                const uint32_t dst = smem_u32(smem) + (uint32_t)((row - t.mb * kBM) * kPartLd + hcol) * 4;
+                if (p.splits > 1) {
+                    // split-K: raw fp32 sums of this K range for rows < m, into this
+                    // CTA's shared memory (the operand ring: every stage of the
+                    // CTA's one work item has been consumed)
+                    const uint32_t dst = smem_u32(smem) + (uint32_t)((row - t.mb * kBM) * kPartLd + hcol) * 4;
+                    if (cols_here > 0) tmem_ld_32cols(acc, r0);
+#pragma unroll
+                    for (int ch = 0; ch < kEpiCols / 32; ++ch) {
+                        uint32_t(&cur)[32] = (ch & 1) ? r1 : r0;
+                        uint32_t(&nxt)[32] = (ch & 1) ? r0 : r1;
+                        if (ch * 32 < cols_here) {                  // uniform across the warp
+                            tmem_ld_wait_regs(cur);
+                            if (ch + 1 < kEpiCols / 32 && (ch + 1) * 32 < cols_here)
+                                tmem_ld_32cols(acc + (ch + 1) * 32, nxt);
+                            if (row < p.m) {
+#pragma unroll
+                                for (int v = 0; v < 8; ++v)
+                                    st_shared_v4(dst + (uint32_t)(ch * 32 + 4 * v) * 4, cur[4 * v], cur[4 * v + 1],
+                                                 cur[4 * v + 2], cur[4 * v + 3]);
+                            }
+                        }
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(tmem_empty);
+                    continue;
+                }
+
+                uint32_t packed[kEpiCols / 2];
                 if (cols_here > 0) tmem_ld_32cols(acc, r0);
 #pragma unroll
                 for (int ch = 0; ch < kEpiCols / 32; ++ch) {
                     uint32_t(&cur)[32] = (ch & 1) ? r1 : r0;
                     uint32_t(&nxt)[32] = (ch & 1) ? r0 : r1;
-                    if (ch * 32 < cols_here) {                  // uniform across the warp
+                    if (ch * 32 < cols_here) {                      // uniform across the warp
                         tmem_ld_wait_regs(cur);
-                        if (ch + 1 < kEpiCols / 32 && (ch + 1) * 32 < cols_here)
-                            tmem_ld_32cols(acc + (ch + 1) * 32, nxt);
-                        if (row < p.m) {
+                        if (ch + 1 < kEpiCols / 32 && (ch + 1) * 32 < cols_here) tmem_ld_32cols(acc + (ch + 1) * 32, nxt);
 #pragma unroll
-                            for (int v = 0; v < 8; ++v)
-                                st_shared_v4(dst + (uint32_t)(ch * 32 + 4 * v) * 4, cur[4 * v], cur[4 * v + 1],
-                                             cur[4 * v + 2], cur[4 * v + 3]);
+                        for (int j = 0; j < 32; j += 2) {
+                            float b0 = 0.0f, b1 = 0.0f;
+                            if (use_bias) {
+                                const uint32_t bw = *reinterpret_cast<const uint32_t *>(s_bias + ch * 32 + j);
+                                b0 = __uint_as_float(bw << 16);
+                                b1 = __uint_as_float(bw & 0xFFFF0000u);
+                            }
+                            packed[ch * 16 + j / 2] = bf16x2_rn(__fmaf_rn(__uint_as_float(cur[j]), alpha, b0),
+                                                                __fmaf_rn(__uint_as_float(cur[j + 1]), alpha, b1));
                         }
                     }
                 }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(tmem_empty);
-                continue;
-            }
+                if (lane == 0) {
+                    mbar_arrive(tmem_empty);
+                    if (use_bias) mbar_arrive(&bias_empty[it & 1]);
+                }
 
-            constexpr int kOutCols = kEpi == kEpiGated ? kEpiCols / 2 : kEpiCols;
-            constexpr int kOutChunk = kEpi == kEpiGated ? 16 : 32;   // output columns of 32 accumulator columns
-            const int out_col_base = kEpi == kEpiGated ? col_base / 2 : col_base;
-            const int out_cols_here = kEpi == kEpiGated ? cols_here / 2 : cols_here;
-            uint32_t packed[kOutCols / 2];
-            if (cols_here > 0) tmem_ld_32cols(acc, r0);
+                // A few rows (small m): each of their lanes writes its row from
+                // registers, 16 bytes at a time (rows start on 16 bytes, col_base
+                // % 128 == 0); no round trips through the staging buffer.
+                const int rows_here = min(32, p.m - row0);
+                if (cols_here > 0 && rows_here <= kDirectStoreRows) {
+                    if (lane < rows_here) {
+                        uint16_t *o = p.out + (int64_t)(row0 + lane) * p.ldo + col_base;
 #pragma unroll
-            for (int ch = 0; ch < kEpiCols / 32; ++ch) {
-                uint32_t(&cur)[32] = (ch & 1) ? r1 : r0;
-                uint32_t(&nxt)[32] = (ch & 1) ? r0 : r1;
-                if (ch * 32 < cols_here) {                      // uniform across the warp
-                    uint4 res[kOutChunk / 8];
-                    if constexpr (kEpi != kEpiPlain)
-                        load_residual_row(p, res, row, out_col_base + ch * kOutChunk);
-                    tmem_ld_wait_regs(cur);
-                    if (ch + 1 < kEpiCols / 32 && (ch + 1) * 32 < cols_here) tmem_ld_32cols(acc + (ch + 1) * 32, nxt);
-                    // eight output columns at a time (sixteen accumulator columns when gated)
+                        for (int g = 0; g < kEpiCols / 8; ++g) {
+                            if (8 * g + 8 <= cols_here) {
+                                *reinterpret_cast<uint4 *>(o + 8 * g) =
+                                    make_uint4(packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
+                            } else if (8 * g < cols_here) {
 #pragma unroll
-                    for (int g = 0; g < kOutChunk / 8; ++g) {
-                        const uint16_t *gb = s_bias + ch * 32 + g * (kEpi == kEpiGated ? 16 : 8);
-                        uint64_t v[4];
+                                for (int e = 0; e < 8; ++e)
+                                    if (8 * g + e < cols_here)
+                                        o[8 * g + e] = (uint16_t)(packed[4 * g + e / 2] >> (16 * (e & 1)));
+                            }
+                        }
+                    }
+                    continue;
+                }
+
+                // Store through shared memory and the TMA: 16-column chunks of this
+                // warp's 32 rows x 128 columns; the TMA clips rows >= m and
+                // columns >= n_out.  (Thread-per-row global stores would touch 32
+                // rows per instruction and congest the SM's memory pipeline that
+                // the MMA thread's barrier and issue traffic also uses.)
+#pragma unroll
+                for (int c = 0; c < kEpiCols / 16; ++c) {
+                    if (c * 16 < cols_here) {                       // uniform across the warp
+                        if (lane == 0) bulk_wait_group_read<0>();   // the previous chunk's store has read the buffer
+                        __syncwarp();
+                        st_shared_v4(out_stage + lane * 32, packed[c * 8], packed[c * 8 + 1], packed[c * 8 + 2],
+                                     packed[c * 8 + 3]);
+                        st_shared_v4(out_stage + lane * 32 + 16, packed[c * 8 + 4], packed[c * 8 + 5],
+                                     packed[c * 8 + 6], packed[c * 8 + 7]);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&tmOut, out_stage, col_base + c * 16, row0, out_policy);
+                            bulk_commit_group();
+                        }
+                    }
+                }
+            } else {
+                // Load this warp's 128 accumulator columns with all four loads in
+                // flight and hand the accumulator back at once: the next tile's
+                // MMAs overlap the arithmetic and stores below.
+                uint32_t acc_regs[kEpiCols / 32][32];
+                if (cols_here > 0) {                                // uniform across the warp
+#pragma unroll
+                    for (int ch = 0; ch < kEpiCols / 32; ++ch) tmem_ld_32cols(acc + ch * 32, acc_regs[ch]);
+#pragma unroll
+                    for (int ch = 0; ch < kEpiCols / 32; ++ch) tmem_ld_wait_regs(acc_regs[ch]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tmem_empty);
+
+                if (p.splits > 1) {
+                    // split-K: raw fp32 sums of this K range for rows < m, into this
+                    // CTA's shared memory (the operand ring: every stage of the
+                    // CTA's one work item has been consumed)
+                    const uint32_t dst = smem_u32(smem) + (uint32_t)((row - t.mb * kBM) * kPartLd + hcol) * 4;
+                    if (row < p.m) {
+#pragma unroll
+                        for (int ch = 0; ch < kEpiCols / 32; ++ch)
+                            if (ch * 32 < cols_here) {
+                                uint32_t(&cur)[32] = acc_regs[ch];
+#pragma unroll
+                                for (int v = 0; v < 8; ++v)
+                                    st_shared_v4(dst + (uint32_t)(ch * 32 + 4 * v) * 4, cur[4 * v], cur[4 * v + 1],
+                                                 cur[4 * v + 2], cur[4 * v + 3]);
+                            }
+                    }
+                    continue;
+                }
+
+                // Sixteen output columns at a time: this row's values into the
+                // warp's staging chunk (16-byte piece j of row r at piece
+                // j ^ (r / 4 % 2), free of bank conflicts), then two lanes per row
+                // to memory, whole 32-byte sectors.  (With a TMA store per chunk,
+                // each waiting for the one before to have read the one chunk
+                // there is room for, the 32-expert SWIGLU GEMM of 256 rows each,
+                // 1536 x 2048, takes 25.7 us instead of 24.2.)
+                constexpr int kChunks = (kEpi == kEpiGated ? kEpiCols / 2 : kEpiCols) / 16;
+                const int out_col_base = kEpi == kEpiGated ? col_base / 2 : col_base;
+                uint4 res[2] = {};
+                if constexpr (kEpi != kEpiPlain) load_residual_row(p, res, row, out_col_base);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int col = out_col_base + c * 16;
+                    if (c * (kEpi == kEpiGated ? 32 : 16) < cols_here) {   // uniform across the warp
+                        uint64_t v[8];
                         if constexpr (kEpi == kEpiGated) {
-                            uint64_t in[8];
-                            scale_bias8(in, cur + g * 16, alpha, gb, use_bias);
-                            scale_bias8(in + 4, cur + g * 16 + 8, alpha, gb + 8, use_bias);
+                            uint64_t in[16];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                scale_bias8(in + 4 * g, acc_regs[c] + 8 * g, alpha, s_bias + c * 32 + 8 * g, use_bias);
                             apply_gate(v, in, actp);
                         } else {
-                            scale_bias8(v, cur + g * 8, alpha, gb, use_bias);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g)
+                                scale_bias8(v + 4 * g, acc_regs[c / 2] + (c & 1) * 16 + 8 * g, alpha,
+                                            s_bias + c * 16 + 8 * g, use_bias);
                             if constexpr (kEpi == kEpiAct) apply_act(v, actp);
                         }
-                        if constexpr (kEpi != kEpiPlain) add_residual8(v, res[g]);
+                        if constexpr (kEpi != kEpiPlain) {
+                            add_residual8(v, res[0]);
+                            add_residual8(v + 4, res[1]);
+                            if (c + 1 < kChunks) load_residual_row(p, res, row, col + 16);
+                        }
+                        __syncwarp();                           // the previous chunk has been read
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) packed[ch * (kOutChunk / 2) + g * 4 + e] = bf16x2_of(v[e]);
-                    }
-                }
-            }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(tmem_empty);
-                if (use_bias) mbar_arrive(&bias_empty[it & 1]);
-            }
-
-            // A few rows (small m): each of their lanes writes its row from
-            // registers, 16 bytes at a time (rows start on 16 bytes, out_col_base
-            // % 64 == 0); no round trips through the staging buffer.
-            const int rows_here = min(32, p.m - row0);
-            if (cols_here > 0 && rows_here <= kDirectStoreRows) {
-                if (lane < rows_here) {
-                    uint16_t *o = p.out + (int64_t)(row0 + lane) * p.ldo + out_col_base;
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 w = bf16x8_of(v + 4 * j);
+                            st_shared_v4(out_stage + lane * 32 + ((j ^ ((lane >> 2) & 1)) << 4), w.x, w.y, w.z, w.w);
+                        }
+                        __syncwarp();
 #pragma unroll
-                    for (int g = 0; g < kOutCols / 8; ++g) {
-                        if (8 * g + 8 <= out_cols_here) {
-                            *reinterpret_cast<uint4 *>(o + 8 * g) =
-                                make_uint4(packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
-                        } else if (8 * g < out_cols_here) {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (8 * g + e < out_cols_here)
-                                    o[8 * g + e] = (uint16_t)(packed[4 * g + e / 2] >> (16 * (e & 1)));
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = i * 16 + (lane >> 1), j = lane & 1;
+                            const uint4 w = ld_shared_v4(out_stage + r * 32 + ((j ^ ((r >> 2) & 1)) << 4));
+                            if (row0 + r < p.m)
+                                store_columns8(p.out + (int64_t)(row0 + r) * p.ldo, col + 8 * j, p.out_cols, w);
                         }
                     }
                 }
-                continue;
-            }
-
-            // Store through shared memory and the TMA: 16-column chunks of this
-            // warp's 32 rows x 128 columns; the TMA clips rows >= m and
-            // columns past the last whole 16 bytes, the rest is stored by the row's lane.  (Thread-per-row global stores would touch 32
-            // rows per instruction and congest the SM's memory pipeline that
-            // the MMA thread's barrier and issue traffic also uses.)
-#pragma unroll
-            for (int c = 0; c < kOutCols / 16; ++c) {
-                if (c * 16 < out_cols_here) {                       // uniform across the warp
-                    if (lane == 0) bulk_wait_group_read<0>();   // the previous chunk's store has read the buffer
-                    __syncwarp();
-                    st_shared_v4(out_stage + lane * 32, packed[c * 8], packed[c * 8 + 1], packed[c * 8 + 2],
-                                 packed[c * 8 + 3]);
-                    st_shared_v4(out_stage + lane * 32 + 16, packed[c * 8 + 4], packed[c * 8 + 5],
-                                 packed[c * 8 + 6], packed[c * 8 + 7]);
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    const int col = out_col_base + c * 16, whole = tma_cols(p.out_cols);
-                    if (lane == 0 && (kEpi == kEpiPlain || col < whole)) {
-                        tma_store_2d(&tmOut, out_stage, col, row0, out_policy);
-                        bulk_commit_group();
-                    }
-                    if (kEpi != kEpiPlain && whole < p.out_cols && whole >= col && whole < col + 16 && row < p.m)
-                        store_tail_columns(p, row, ld_shared_v4(out_stage + lane * 32 + (whole - col) * 2));
-                }
+                __syncwarp();
+                if (use_bias && lane == 0) mbar_arrive(&bias_empty[it & 1]);
             }
         }
         if (lane == 0) bulk_wait_group<0>();                    // all output written before the CTA exits
