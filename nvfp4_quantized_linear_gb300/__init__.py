@@ -429,6 +429,10 @@ def mxfp4_linear(x, w_fp4, w_sf, k: int, n_out: int, bias=None, out=None, worksp
     if workspace is None:
         workspace = torch.empty(max(nvfp4_mxfp4_linear_workspace_bytes(m, k, n_w), 1), dtype=torch.uint8,
                                 device=x.device)
+    if act == "none" and residual is None:
+        nvfp4_mxfp4_linear(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, out, _ld(out, "out"), workspace,
+                           workspace.numel(), stream)
+        return out
     nvfp4_mxfp4_linear_act(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, ACTIVATIONS[act], residual,
                            _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,
                            workspace.numel(), stream)
@@ -458,6 +462,10 @@ def linear(x, w_fp4, w_sf, k: int, n_out: int, gs, alpha, bias=None, transform=N
     need = nvfp4_linear_workspace_bytes(m, k, n_w)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
+    if act == "none" and residual is None:
+        nvfp4_linear(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
+                     alpha, bias, out, _ld(out, "out"), workspace, workspace.numel(), stream)
+        return out
     nvfp4_linear_act(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
                      alpha, bias, ACTIVATIONS[act], residual,
                      _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,

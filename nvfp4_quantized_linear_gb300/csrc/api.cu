@@ -248,6 +248,7 @@ nvfp4::GemmParams gemm_params(const uint8_t *a_sf, int64_t m, const uint8_t *w_s
     g.act = epi.act;
     g.residual = static_cast<const uint16_t *>(epi.residual);
     g.ldr = epi.ldr;
+    g.wait_all = 0;
     g.kp = (int32_t)nvfp4::padded_k(k);
     const int64_t nbp = scale_cols_of(k, mx);
     g.num_k64 = (int32_t)((g.kp + 63) / 64);
@@ -335,7 +336,9 @@ nvfp4_status run_gemm(const uint8_t *a, const uint8_t *a_sf, int64_t m, const ui
     nvfp4::GemmParams g = gemm_params(a_sf, m, w_sf, n_w, n_out, k, alpha, bias, out, ldo, err, mx, epi);
     if (wait_ns != 0) g.wait_ns = wait_ns;
     g.drill = drill;
-    if (allow_split && !(kernel == kGemmPair || (kernel == kGemmAuto && m > 128))) {
+    const char *why = nullptr;
+    const bool pair = kernel == kGemmPair || (kernel == kGemmAuto && m > 128);
+    if (allow_split && !pair) {
         int sps = 0;
         const int splits = split_k_plan(g, num_sms, &sps);
         if (splits > 1) {
@@ -343,14 +346,13 @@ nvfp4_status run_gemm(const uint8_t *a, const uint8_t *a_sf, int64_t m, const ui
             g.stages_per_split = sps;
         }
     }
-    const char *why = nullptr;
-    const bool pair = kernel == kGemmPair || (kernel == kGemmAuto && m > 128);
     if (fuse_quant != nullptr) {                     // the fused small-m linear: quantizer inside the GEMM
         g.quant = *fuse_quant;
         e = nvfp4::launch_linear_fused(g, w, num_sms, s, &why);
     } else {
-        e = pair ? nvfp4::launch_gemm_pair(g, a, w, num_sms, s, &why, after_quant)
-                 : nvfp4::launch_gemm(g, a, w, num_sms, s, &why, after_quant);
+        g.wait_all = after_quant ? 0 : 1;
+        e = pair ? nvfp4::launch_gemm_pair(g, a, w, num_sms, s, &why, true)
+                 : nvfp4::launch_gemm(g, a, w, num_sms, s, &why, true);
     }
     if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
     return launch_status(e, fuse_quant ? "fused linear kernel" : "GEMM kernel");
@@ -558,7 +560,8 @@ nvfp4_status grouped_gemm_impl(const uint8_t *a_fp4, const uint8_t *a_sf, int64_
     g.num_groups = num_groups;
     g.group_n = (int32_t)n_acc;
     const char *why = nullptr;
-    e = nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, reinterpret_cast<cudaStream_t>(stream), &why, false);
+    g.wait_all = 1;
+    e = nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, reinterpret_cast<cudaStream_t>(stream), &why, true);
     if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
     return launch_status(e, "grouped GEMM kernel");
 }
@@ -829,8 +832,8 @@ nvfp4_status nvfp4_mxfp4_linear_act(const void *x_bf16, int64_t m, int64_t k, in
                                     const void *residual_bf16, int64_t ldr, void *out_bf16, int64_t ldo,
                                     void *workspace, size_t workspace_bytes, nvfp4_stream_t stream)
 {
-    return mxfp4_linear_impl(x_bf16, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias_bf16, {act, residual_bf16, ldr}, out_bf16,
-                             ldo, workspace, workspace_bytes, stream);
+    return mxfp4_linear_impl(x_bf16, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias_bf16, {act, residual_bf16, ldr},
+                             out_bf16, ldo, workspace, workspace_bytes, stream);
 }
 
 nvfp4_status nvfp4_grouped_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,

@@ -82,6 +82,11 @@ struct GemmParams {
     int32_t out_cols;
     const uint16_t *residual;        // bf16 bits [m, ldr] or nullptr
     int64_t ldr;
+    // 1: launched as a programmatic dependent of an arbitrary kernel, whose
+    // completion every role waits for before it reads memory (the prologue
+    // overlaps that kernel's end); 0: launched normally, or as the dependent of
+    // the quantizer of its activation, which only the activation side waits for.
+    int32_t wait_all;
     uint64_t wait_ns;                // bound of every pipeline barrier wait (ns of %globaltimer)
     int32_t drill;                   // 1: timeout drill, the producers issue no copies (test hook)
     // Fused small-m linear (one-CTA kernel): the activation the kernel
@@ -95,8 +100,9 @@ constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // two seconds
 cudaError_t launch_quant(const QuantParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_quant_transform(const QuantParams &p, int num_sms, cudaStream_t s, const char **why);
 // dependent = true launches the GEMM as a programmatic dependent of the
-// preceding kernel, which must be the quantizer of its activation operand:
-// the GEMM's weight-side loads then start before that kernel has finished.
+// preceding kernel.  Without p.wait_all that kernel must be the quantizer of its
+// activation operand: the GEMM's weight-side loads then start before it has
+// finished.
 cudaError_t launch_gemm(const GemmParams &p, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,
                         const char **why, bool dependent = false);
 // The fused small-m linear (m <= 16, NVFP4, no transform): p.quant describes

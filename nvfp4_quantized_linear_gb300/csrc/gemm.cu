@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Roles by warpgroup; each warpgroup first resizes its register file.
     if (warp >= kEpiWarp0) {
         setmaxnreg_inc<kRegsEpi>();
+        if (p.wait_all) griddep_wait();
         const int lane = role_value((int)(threadIdx.x & 31));
         const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
         const int num_ks = role_value((p.num_k64 + 3) / 4);
@@ -458,6 +459,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n_cols = min(kEpiCols, p.n_out - t.nb * kBN - hcol);   // may be <= 0
             const int col_base = t.nb * kBN + hcol;
             const uint16_t *s_bias = reinterpret_cast<const uint16_t *>(smem + kOffBias) + (it & 1) * kBN + hcol;
+            // the warp's residual into L2 while the accumulator is being computed
+            if (kEpi != kEpiPlain && p.residual != nullptr && p.splits == 1) {
+                const int64_t r = (int64_t)t.mb * kBM + q * 32 + lane;
+                const int c = kEpi == kEpiGated ? col_base / 2 : col_base;
+#pragma unroll
+                for (int i = 0; i < (kEpi == kEpiGated ? 1 : 2); ++i)
+                    if (r < p.m && c + 64 * i < p.out_cols) prefetch_l2(p.residual + r * p.ldr + c + 64 * i);
+            }
             if (use_bias &&
                 !__all_sync(~0u, mbar_wait(&bias_full[it & 1], (it >> 1) & 1, p.err_flag, kErrTimeout, p.wait_ns)))
                 break;
@@ -677,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
+        if (p.wait_all) griddep_wait();
         const int lane = role_value((int)(threadIdx.x & 31));
         const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
         const int num_ks = role_value((p.num_k64 + 3) / 4);
@@ -735,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         setmaxnreg_dec<kRegsCtl>();
+        if (p.wait_all) griddep_wait();
         const int lane = role_value((int)(threadIdx.x & 31));
         const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
         const int num_ks = role_value((p.num_k64 + 3) / 4);

@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     if (warp >= kEpiWarp0) {
         setmaxnreg_inc<kRegsEpi>();
+        if (p.wait_all) griddep_wait();
         const Role role = enter_role(p, tmem_slot);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t rank = role.rank, tmem = role.tmem;
@@ -363,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bulk_wait_group<0>();                    // all output written before the CTA exits
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
+        if (p.wait_all) griddep_wait();
         const Role role = enter_role(p, tmem_slot);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t tmem = role.tmem;
@@ -429,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         setmaxnreg_dec<kRegsCtl>();
+        if (p.wait_all) griddep_wait();
         const Role role = enter_role(p, tmem_slot);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t rank = role.rank, tmem = role.tmem;

@@ -150,18 +150,22 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortPa
 // Blocks [0, tokens): a token's row to its assignments' rows, read once.
 // Blocks past them, one per expert: zeros into the group's padding rows.
 
+// Eight columns of a row; kWhole: h % 8 == 0, so they are all inside (the other
+// case's code and registers stay out of that instance).
+template <bool kWhole>
 __device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int h)
 {
-    if (c + 8 <= h) return *reinterpret_cast<const uint4 *>(row + c);
+    if (kWhole || c + 8 <= h) return *reinterpret_cast<const uint4 *>(row + c);
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = c + i < h ? row[c + i] : 0u;
     return make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
 }
 
+template <bool kWhole>
 __device__ __forceinline__ void store8(uint16_t *row, int c, int h, const uint4 &v)
 {
-    if (c + 8 <= h) {
+    if (kWhole || c + 8 <= h) {
         *reinterpret_cast<uint4 *>(row + c) = v;
         return;
     }
@@ -183,13 +187,14 @@ __device__ __forceinline__ int row_of(const MoeRowsParams &p, int64_t assignment
 // e * kPadSlices + j takes rows j, j + kPadSlices, ... of group e's.
 constexpr int kPadSlices = 16;
 
+template <bool kWhole>
 __device__ __forceinline__ void zero_padding_rows(const MoeRowsParams &p, int item)
 {
     const int e = item / kPadSlices;
     const int first = max(0, p.offsets[e] + p.counts[e]), end = min(p.offsets[e + 1], p.rows);
     for (int r = first + item % kPadSlices; r < end; r += kPadSlices)
         for (int c = threadIdx.x * 8; c < p.h; c += blockDim.x * 8)
-            store8(p.out + (int64_t)r * p.ldo, c, p.h, make_uint4(0, 0, 0, 0));
+            store8<kWhole>(p.out + (int64_t)r * p.ldo, c, p.h, make_uint4(0, 0, 0, 0));
 }
 
 // The rows of up to 8 assignments from `first` on, by lane (< 8; -1 past `count`).
@@ -199,12 +204,13 @@ __device__ __forceinline__ int rows_by_lane(const MoeRowsParams &p, int64_t firs
     return lane < min(count, 8) ? row_of(p, first + lane) : -1;
 }
 
+template <bool kWhole>
 __global__ void __launch_bounds__(256) moe_dispatch_kernel(const MoeRowsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
     if ((int)blockIdx.x >= p.tokens) {
-        zero_padding_rows(p, blockIdx.x - p.tokens);
+        zero_padding_rows<kWhole>(p, blockIdx.x - p.tokens);
         return;
     }
     const int64_t first = (int64_t)blockIdx.x * p.topk;     // the token's assignments
@@ -213,11 +219,11 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const MoeRowsParams p
         const int mine = rows_by_lane(p, first + kb, p.topk - kb);
         for (int c0 = 0; c0 < p.h; c0 += blockDim.x * 8) {
             const int c = c0 + threadIdx.x * 8;
-            const uint4 v = c < p.h ? load8(x, c, p.h) : make_uint4(0, 0, 0, 0);
+            const uint4 v = c < p.h ? load8<kWhole>(x, c, p.h) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int d = __shfl_sync(kFull, mine, k);
-                if (d >= 0 && c < p.h) store8(p.out + (int64_t)d * p.ldo, c, p.h, v);
+                if (d >= 0 && c < p.h) store8<kWhole>(p.out + (int64_t)d * p.ldo, c, p.h, v);
             }
         }
     }
@@ -262,51 +268,74 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 }
 
 // ---------------------------------------------------------------- combine ----
-// A block takes a token's columns, eight per thread; the rows of eight
-// assignments are requested before the first is added, so that a thread has up
-// to 128 bytes in flight.
-__global__ void __launch_bounds__(256) moe_combine_kernel(const MoeRowsParams p)
+// A block takes its columns (eight per thread; blockIdx.y) of every gridDim.x-th
+// token: a token's rows, up to eight 16-byte loads per thread, are requested
+// together, with the next token's row numbers and weights behind them, so that
+// one memory latency passes per token instead of two and a block start.
+template <bool kWhole>
+__global__ void __launch_bounds__(256, 4) moe_combine_kernel(const MoeRowsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 31;
-    const int c0 = blockIdx.y * blockDim.x * 8;
-    const int c = c0 + threadIdx.x * 8;
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
     const bool here = c < p.h;
-    uint4 res = make_uint4(0, 0, 0, 0);
-    if (p.residual != nullptr && here) res = load8(p.residual + t * p.ldr, c, p.h);
-    uint64_t acc[4] = {0, 0, 0, 0};
-    for (int kb = 0; kb < p.topk; kb += 8) {
-        const int mine = rows_by_lane(p, t * p.topk + kb, p.topk - kb);
-        const float my_w = mine >= 0 && p.weights != nullptr ? p.weights[t * p.topk + kb + lane] : 1.0f;
-        uint4 v[8];
+    auto weight_of = [&](int row, int64_t first) {
+        return row >= 0 && p.weights != nullptr ? p.weights[first + lane] : 1.0f;
+    };
+    int mine = rows_by_lane(p, (int64_t)blockIdx.x * p.topk, p.topk);
+    float my_w = weight_of(mine, (int64_t)blockIdx.x * p.topk);
+    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+        uint64_t acc[4] = {0, 0, 0, 0};
+        uint4 res = make_uint4(0, 0, 0, 0);
+        int next_mine = -1;
+        float next_w = 1.0f;
+        for (int kb = 0; kb < p.topk; kb += 8) {
+            const int64_t first = (int64_t)t * p.topk + kb;
+            if (kb > 0) {
+                mine = rows_by_lane(p, first, p.topk - kb);
+                my_w = weight_of(mine, first);
+            }
+            uint4 v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = __shfl_sync(kFull, mine, k);
-            v[k] = r >= 0 && here ? load8(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 8; ++k) {
+                const int r = __shfl_sync(kFull, mine, k);
+                v[k] = r >= 0 && here ? load8<kWhole>(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
+            }
+            if (kb == 0 && p.residual != nullptr && here) res = load8<kWhole>(p.residual + (int64_t)t * p.ldr, c, p.h);
+            if (kb == 0 && p.tokens - t > (int)gridDim.x) {
+                const int64_t next = (int64_t)(t + gridDim.x) * p.topk;
+                next_mine = rows_by_lane(p, next, p.topk);
+                next_w = weight_of(next_mine, next);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float w = __shfl_sync(kFull, my_w, k); // (1 with zeros for a dropped assignment)
+                acc[0] = fma2(bf16x2_to_f32x2(v[k].x), pack2(w, w), acc[0]);
+                acc[1] = fma2(bf16x2_to_f32x2(v[k].y), pack2(w, w), acc[1]);
+                acc[2] = fma2(bf16x2_to_f32x2(v[k].z), pack2(w, w), acc[2]);
+                acc[3] = fma2(bf16x2_to_f32x2(v[k].w), pack2(w, w), acc[3]);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float w = __shfl_sync(kFull, my_w, k);     // (1 with zeros for a dropped assignment)
-            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = fma2(bf16x2_to_f32x2(u[i]), pack2(w, w), acc[i]);
+        if (here) {
+            if (p.residual != nullptr) add_residual8(acc, res);
+            store8<kWhole>(p.out + (int64_t)t * p.ldo, c, p.h, bf16x8_of(acc));
         }
+        mine = next_mine;
+        my_w = next_w;
     }
-    if (p.residual != nullptr) add_residual8(acc, res);
-    if (here) store8(p.out + t * p.ldo, c, p.h, bf16x8_of(acc));
 }
 
 // Blocks as in moe_dispatch_kernel.  Eight assignments at a time: their rows are
 // requested together, each thread keeps eight partial dot products, and one
 // reduction per eight (lanes, then warps, in a fixed order) ends them.
-__global__ void __launch_bounds__(256) moe_combine_backward_kernel(const MoeRowsParams p)
+template <bool kWhole>
+__global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeRowsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
     if ((int)blockIdx.x >= p.tokens) {
-        zero_padding_rows(p, blockIdx.x - p.tokens);
+        zero_padding_rows<kWhole>(p, blockIdx.x - p.tokens);
         return;
     }
     __shared__ float s_dot[8][8];                        // [warp][assignment]
@@ -324,9 +353,9 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const MoeRows
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int r = __shfl_sync(kFull, mine, k);
-                v[k] = r >= 0 && here ? load8(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
+                v[k] = r >= 0 && here ? load8<kWhole>(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
             }
-            const uint4 gv = here ? load8(g, c, p.h) : make_uint4(0, 0, 0, 0);
+            const uint4 gv = here ? load8<kWhole>(g, c, p.h) : make_uint4(0, 0, 0, 0);
             const uint64_t a[4] = {bf16x2_to_f32x2(gv.x), bf16x2_to_f32x2(gv.y), bf16x2_to_f32x2(gv.z),
                                    bf16x2_to_f32x2(gv.w)};
 #pragma unroll
@@ -340,7 +369,7 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const MoeRows
                     dot[k] = fma2(a[i], bf16x2_to_f32x2(u[i]), dot[k]);
                     d[i] = mul2(a[i], pack2(w, w));
                 }
-                if (r >= 0 && here) store8(p.out + (int64_t)r * p.ldo, c, p.h, bf16x8_of(d));
+                if (r >= 0 && here) store8<kWhole>(p.out + (int64_t)r * p.ldo, c, p.h, bf16x8_of(d));
             }
         }
 #pragma unroll
@@ -365,13 +394,13 @@ __global__ void __launch_bounds__(256) moe_combine_backward_kernel(const MoeRows
 // Every kernel here is launched as a programmatic dependent and waits for the
 // kernel before it (griddepcontrol.wait) before it reads or writes memory.
 template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), int64_t grid, int threads, size_t smem, cudaStream_t s, Args... args)
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -420,7 +449,7 @@ cudaError_t launch_moe_sort(const MoeSortParams &p, int num_sms, cudaStream_t s)
 cudaError_t launch_moe_dispatch(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    return launch_dependent(moe_dispatch_kernel, (int64_t)p.tokens + (int64_t)p.experts * kPadSlices, row_threads(p.h), 0,
+    return launch_dependent(p.h % 8 == 0 ? moe_dispatch_kernel<true> : moe_dispatch_kernel<false>, (unsigned)(p.tokens + p.experts * kPadSlices), row_threads(p.h), 0,
                             s, p);
 }
 
@@ -433,24 +462,18 @@ cudaError_t launch_moe_dispatch_quant(const MoeRowsParams &p, int num_sms, cudaS
 
 cudaError_t launch_moe_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
-    (void)num_sms;
     const int threads = row_threads(p.h), parts = (p.h + threads * 8 - 1) / (threads * 8);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)p.tokens, (unsigned)parts, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_combine_kernel, p);
+    // 64 registers a thread: 1024 threads per SM
+    int64_t blocks = ((int64_t)num_sms * (1024 / threads) + parts - 1) / parts;
+    if (blocks > p.tokens) blocks = p.tokens;
+    return launch_dependent(p.h % 8 == 0 ? moe_combine_kernel<true> : moe_combine_kernel<false>,
+                            dim3((unsigned)blocks, (unsigned)parts, 1), threads, 0, s, p);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    return launch_dependent(moe_combine_backward_kernel, (int64_t)p.tokens + (int64_t)p.experts * kPadSlices,
+    return launch_dependent(p.h % 8 == 0 ? moe_combine_backward_kernel<true> : moe_combine_backward_kernel<false>, (unsigned)(p.tokens + p.experts * kPadSlices),
                             row_threads(p.h), 0, s, p);
 }
 

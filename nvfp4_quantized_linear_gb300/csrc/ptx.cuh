@@ -585,6 +585,11 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void *p)
     return r;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // A coherent 16-byte load that leaves nothing in L1.
 __device__ __forceinline__ uint4 ld_global_v4(const void *p)
 {

@@ -142,6 +142,15 @@ def test_mxfp4(m, act):
     c.gemm()
 
 
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("m,k,n", [(129, 2080, 520), (333, 4104, 328), (640, 2304, 200), (1000, 608, 96)])
+def test_few_tiles_over_several_row_bands(m, k, n, act):
+    """m > 128 with fewer output tiles than CTA pairs, in both formats."""
+    Case(m, k, n, act, True, True, seed=m).linear()
+    if act == "gelu":
+        Case(m, k, n, act, True, True, seed=m, mx=True).linear()
+
+
 @pytest.mark.parametrize("act", ["relu", "swiglu"])
 def test_weight_rows_past_the_output_are_ignored(act):
     for m in (4, 150):
@@ -207,7 +216,7 @@ def test_large_arguments_saturate():
 
 def test_transform_path():
     """The transform quantizer feeds the same epilogue: equal to the GEMM entry
-    point on the transform quantizer's own codes, bit for bit (no split at this m)."""
+    point on the transform quantizer's own codes, bit for bit."""
     m, k, n, bs = 300, 512, 256, 32
     x = syn.bf16_outlier_channels(m, k, 3).cuda()
     t = syn.random_hadamard_transform(bs, 4).cuda()
