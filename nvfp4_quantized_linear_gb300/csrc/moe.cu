@@ -268,69 +268,89 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 }
 
 // ---------------------------------------------------------------- combine ----
-// A block takes its columns (eight per thread; blockIdx.y) of every gridDim.x-th
-// token: a token's rows, up to eight 16-byte loads per thread, are requested
-// together, with the next token's row numbers and weights behind them, so that
-// one memory latency passes per token instead of two and a block start.
-template <bool kWhole>
-__global__ void __launch_bounds__(256, 4) moe_combine_kernel(const MoeRowsParams p)
+// A block takes its columns (eight per thread; blockIdx.y) of kT consecutive
+// tokens at a time: the kT x kK rows of a step, up to eight 16-byte loads per
+// thread, are requested together, with the next step's row numbers and weights
+// behind them, so that one memory latency passes per step instead of two and a
+// block start.  Small topk takes more tokens per step: with one row in flight
+// per thread 16384 tokens of topk 1 moved 1.6 TB/s.  topk > kK (= 8) goes round.
+template <bool kWhole, int kK, int kT>
+__global__ void __launch_bounds__(128, 8) moe_combine_kernel(const MoeRowsParams p)
 {
+    static_assert(kK * kT <= 8, "rows by lane");
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int c = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
     const bool here = c < p.h;
-    auto weight_of = [&](int row, int64_t first) {
-        return row >= 0 && p.weights != nullptr ? p.weights[first + lane] : 1.0f;
+    // lane l < 8: assignment kb + l % kK of token t0 + l / kK
+    auto row_at = [&](int t0, int kb) {
+        const int t = t0 + lane / kK, k = kb + lane % kK;
+        return lane < kK * kT && t < p.tokens && k < p.topk ? row_of(p, (int64_t)t * p.topk + k) : -1;
     };
-    int mine = rows_by_lane(p, (int64_t)blockIdx.x * p.topk, p.topk);
-    float my_w = weight_of(mine, (int64_t)blockIdx.x * p.topk);
-    for (int t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-        uint64_t acc[4] = {0, 0, 0, 0};
-        uint4 res = make_uint4(0, 0, 0, 0);
+    auto weight_at = [&](int row, int t0, int kb) {
+        return row >= 0 && p.weights != nullptr ? p.weights[(int64_t)(t0 + lane / kK) * p.topk + kb + lane % kK] : 1.0f;
+    };
+    const int step = gridDim.x * kT;
+    int mine = row_at(blockIdx.x * kT, 0);
+    float my_w = weight_at(mine, blockIdx.x * kT, 0);
+    for (int t0 = blockIdx.x * kT; t0 < p.tokens; t0 += step) {
+        uint64_t acc[kT][4] = {};
+        uint4 res[kT] = {};
         int next_mine = -1;
         float next_w = 1.0f;
-        for (int kb = 0; kb < p.topk; kb += 8) {
-            const int64_t first = (int64_t)t * p.topk + kb;
+        for (int kb = 0; kb < p.topk; kb += kK) {
             if (kb > 0) {
-                mine = rows_by_lane(p, first, p.topk - kb);
-                my_w = weight_of(mine, first);
+                mine = row_at(t0, kb);
+                my_w = weight_at(mine, t0, kb);
             }
-            uint4 v[8];
+            uint4 v[kT][kK];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = __shfl_sync(kFull, mine, k);
-                v[k] = r >= 0 && here ? load8<kWhole>(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < kT * kK; ++i) {
+                const int r = __shfl_sync(kFull, mine, i);
+                v[i / kK][i % kK] =
+                    r >= 0 && here ? load8<kWhole>(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
             }
-            if (kb == 0 && p.residual != nullptr && here) res = load8<kWhole>(p.residual + (int64_t)t * p.ldr, c, p.h);
-            if (kb == 0 && p.tokens - t > (int)gridDim.x) {
-                const int64_t next = (int64_t)(t + gridDim.x) * p.topk;
-                next_mine = rows_by_lane(p, next, p.topk);
-                next_w = weight_of(next_mine, next);
+            if (kb == 0) {
+                if (p.residual != nullptr && here)
+#pragma unroll
+                    for (int i = 0; i < kT; ++i)
+                        if (t0 + i < p.tokens) res[i] = load8<kWhole>(p.residual + (int64_t)(t0 + i) * p.ldr, c, p.h);
+                if (p.tokens - t0 > step) {
+                    next_mine = row_at(t0 + step, 0);
+                    next_w = weight_at(next_mine, t0 + step, 0);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float w = __shfl_sync(kFull, my_w, k); // (1 with zeros for a dropped assignment)
-                acc[0] = fma2(bf16x2_to_f32x2(v[k].x), pack2(w, w), acc[0]);
-                acc[1] = fma2(bf16x2_to_f32x2(v[k].y), pack2(w, w), acc[1]);
-                acc[2] = fma2(bf16x2_to_f32x2(v[k].z), pack2(w, w), acc[2]);
-                acc[3] = fma2(bf16x2_to_f32x2(v[k].w), pack2(w, w), acc[3]);
+            for (int i = 0; i < kT * kK; ++i) {
+                const float w = __shfl_sync(kFull, my_w, i); // (1 with zeros for a dropped assignment)
+                const uint4 &u = v[i / kK][i % kK];
+                uint64_t(&a)[4] = acc[i / kK];
+                a[0] = fma2(bf16x2_to_f32x2(u.x), pack2(w, w), a[0]);
+                a[1] = fma2(bf16x2_to_f32x2(u.y), pack2(w, w), a[1]);
+                a[2] = fma2(bf16x2_to_f32x2(u.z), pack2(w, w), a[2]);
+                a[3] = fma2(bf16x2_to_f32x2(u.w), pack2(w, w), a[3]);
             }
         }
-        if (here) {
-            if (p.residual != nullptr) add_residual8(acc, res);
-            store8<kWhole>(p.out + (int64_t)t * p.ldo, c, p.h, bf16x8_of(acc));
-        }
+        if (here)
+#pragma unroll
+            for (int i = 0; i < kT; ++i)
+                if (t0 + i < p.tokens) {
+                    if (p.residual != nullptr) add_residual8(acc[i], res[i]);
+                    store8<kWhole>(p.out + (int64_t)(t0 + i) * p.ldo, c, p.h, bf16x8_of(acc[i]));
+                }
         mine = next_mine;
         my_w = next_w;
     }
 }
 
-// Blocks as in moe_dispatch_kernel.  Eight assignments at a time: their rows are
-// requested together, each thread keeps eight partial dot products, and one
-// reduction per eight (lanes, then warps, in a fixed order) ends them.
-template <bool kWhole>
-__global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeRowsParams p)
+// Blocks as in moe_dispatch_kernel.  kK assignments at a time: their rows are
+// requested together, each thread keeps kK partial dot products, and one
+// reduction per kK (lanes, then warps, in a fixed order) ends them.  The
+// instances for small topk hold fewer registers, so more tokens are in flight
+// per SM.
+template <bool kWhole, int kK>
+__global__ void __launch_bounds__(256, kK == 8 ? 4 : kK == 4 ? 5 : 8) moe_combine_backward_kernel(const MoeRowsParams p)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -338,20 +358,20 @@ __global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeR
         zero_padding_rows<kWhole>(p, blockIdx.x - p.tokens);
         return;
     }
-    __shared__ float s_dot[8][8];                        // [warp][assignment]
+    __shared__ float s_dot[8][kK];                       // [warp][assignment]
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *g = p.g + t * p.ldg;
-    for (int kb = 0; kb < p.topk; kb += 8) {
-        const int mine = rows_by_lane(p, t * p.topk + kb, p.topk - kb);
+    for (int kb = 0; kb < p.topk; kb += kK) {
+        const int mine = lane < min(kK, p.topk - kb) ? row_of(p, t * p.topk + kb + lane) : -1;
         const float my_w = mine >= 0 ? p.weights[t * p.topk + kb + lane] : 0.0f;
-        uint64_t dot[8] = {};
+        uint64_t dot[kK] = {};
         for (int c0 = 0; c0 < p.h; c0 += blockDim.x * 8) {
             const int c = c0 + threadIdx.x * 8;
             const bool here = c < p.h;
-            uint4 v[8];
+            uint4 v[kK];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kK; ++k) {
                 const int r = __shfl_sync(kFull, mine, k);
                 v[k] = r >= 0 && here ? load8<kWhole>(p.x + (int64_t)r * p.ldx, c, p.h) : make_uint4(0, 0, 0, 0);
             }
@@ -359,7 +379,7 @@ __global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeR
             const uint64_t a[4] = {bf16x2_to_f32x2(gv.x), bf16x2_to_f32x2(gv.y), bf16x2_to_f32x2(gv.z),
                                    bf16x2_to_f32x2(gv.w)};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kK; ++k) {
                 const int r = __shfl_sync(kFull, mine, k);
                 const float w = __shfl_sync(kFull, my_w, k);
                 const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -373,7 +393,7 @@ __global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeR
             }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kK; ++k) {
             float lo, hi;
             unpack2(dot[k], lo, hi);
             float v = lo + hi;
@@ -382,12 +402,12 @@ __global__ void __launch_bounds__(256, 4) moe_combine_backward_kernel(const MoeR
             if (lane == k) s_dot[warp][k] = v;
         }
         __syncthreads();
-        if (threadIdx.x < 8 && kb + (int)threadIdx.x < p.topk) {
+        if (threadIdx.x < kK && kb + (int)threadIdx.x < p.topk) {
             float sum = 0.0f;
             for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += s_dot[w][threadIdx.x];
             p.dw[t * p.topk + kb + threadIdx.x] = mine >= 0 ? sum : 0.0f;   // (lane k holds row k)
         }
-        if (kb + 8 < p.topk) __syncthreads();
+        if (kb + kK < p.topk) __syncthreads();
     }
 }
 
@@ -460,21 +480,52 @@ cudaError_t launch_moe_dispatch_quant(const MoeRowsParams &p, int num_sms, cudaS
     return launch_dependent(moe_dispatch_quant_kernel, p.tokens, threads, 0, s, p);
 }
 
+namespace {
+
+template <bool kWhole, int kK, int kT>
+cudaError_t launch_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
+{
+    // 128 threads (fewer for short rows) of 64 registers: 1024 threads per SM
+    const int threads = p.h >= 1024 ? 128 : ((p.h + 7) / 8 + 31) / 32 * 32, parts = (p.h + threads * 8 - 1) / (threads * 8);
+    const int64_t resident = ((int64_t)num_sms * (1024 / threads) + parts - 1) / parts, steps = (p.tokens + kT - 1) / kT;
+    // Persistent blocks from six rounds on (16384 tokens, topk 8, 2048 columns:
+    // 87 us, 93 us with a block per step); below, whole rounds are too coarse
+    // (1003 tokens, topk 6, 5120 columns: 15.5 us persistent, 13.5 us not).
+    const int64_t blocks = steps < 6 * resident ? steps : resident;
+    return launch_dependent(moe_combine_kernel<kWhole, kK, kT>, dim3((unsigned)blocks, (unsigned)parts, 1), threads, 0, s,
+                            p);
+}
+
+template <bool kWhole>
+cudaError_t launch_combine_topk(const MoeRowsParams &p, int num_sms, cudaStream_t s)
+{
+    return p.topk == 1   ? launch_combine<kWhole, 1, 2>(p, num_sms, s)
+           : p.topk == 2 ? launch_combine<kWhole, 2, 2>(p, num_sms, s)
+           : p.topk <= 4 ? launch_combine<kWhole, 4, 1>(p, num_sms, s)
+                         : launch_combine<kWhole, 8, 1>(p, num_sms, s);
+}
+
+template <bool kWhole>
+cudaError_t launch_combine_backward_topk(const MoeRowsParams &p, cudaStream_t s)
+{
+    void (*kernel)(MoeRowsParams) = p.topk == 1   ? moe_combine_backward_kernel<kWhole, 1>
+                                    : p.topk == 2 ? moe_combine_backward_kernel<kWhole, 2>
+                                    : p.topk <= 4 ? moe_combine_backward_kernel<kWhole, 4>
+                                                  : moe_combine_backward_kernel<kWhole, 8>;
+    return launch_dependent(kernel, (unsigned)(p.tokens + p.experts * kPadSlices), row_threads(p.h), 0, s, p);
+}
+
+}  // namespace
+
 cudaError_t launch_moe_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
-    const int threads = row_threads(p.h), parts = (p.h + threads * 8 - 1) / (threads * 8);
-    // 64 registers a thread: 1024 threads per SM
-    int64_t blocks = ((int64_t)num_sms * (1024 / threads) + parts - 1) / parts;
-    if (blocks > p.tokens) blocks = p.tokens;
-    return launch_dependent(p.h % 8 == 0 ? moe_combine_kernel<true> : moe_combine_kernel<false>,
-                            dim3((unsigned)blocks, (unsigned)parts, 1), threads, 0, s, p);
+    return p.h % 8 == 0 ? launch_combine_topk<true>(p, num_sms, s) : launch_combine_topk<false>(p, num_sms, s);
 }
 
 cudaError_t launch_moe_combine_backward(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    return launch_dependent(p.h % 8 == 0 ? moe_combine_backward_kernel<true> : moe_combine_backward_kernel<false>, (unsigned)(p.tokens + p.experts * kPadSlices),
-                            row_threads(p.h), 0, s, p);
+    return p.h % 8 == 0 ? launch_combine_backward_topk<true>(p, s) : launch_combine_backward_topk<false>(p, s);
 }
 
 }  // namespace nvfp4
