@@ -103,8 +103,6 @@ nvfp4_status nvfp4_add_rmsnorm_quant(const void *x_bf16, int64_t ldx, const void
     p.gs = gs_dev;
     p.q = x_q;
     p.sf = x_sf;
-    cudaError_t e = nvfp4::device_error_word(&p.err_flag);
-    if (e != cudaSuccess) return launch_status(e, "norm-quantize kernel (error word)");
     return launch_status(nvfp4::launch_norm_quant(p, num_sms, reinterpret_cast<cudaStream_t>(stream)),
                          "norm-quantize kernel");
 }

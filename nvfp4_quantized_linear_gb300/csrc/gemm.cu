@@ -80,6 +80,7 @@ constexpr int kXSliceRows = 16;                             // rows of the fused
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSf = 256;
 constexpr uint32_t kSfColsPerStage = 48;
+constexpr int kPrefetchStages = 4;            // weight stages prefetched into L2 before the wait for the kernel before
 constexpr int kThreads = 512;                 // four warpgroups
 constexpr int kSfWarp0 = 4;                   // warps 4..7: scale staging, lane quarter warp % 4
 constexpr int kEpiWarp0 = 8;                  // warps 8..15: epilogue, lane quarter warp % 4,
@@ -745,7 +746,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         setmaxnreg_dec<kRegsCtl>();
-        if (p.wait_all) griddep_wait();
+        if (p.wait_all) {
+            // While the kernel before this one ends: the first stages' weights
+            // into L2.  (A prefetch is a hint to L2, where later writes land
+            // too: nothing is read before the wait.  A group's weights depend
+            // on offsets that kernel may write.)
+            if (warp == 3 && (threadIdx.x & 31) == 0 && !p.drill && p.group_offsets == nullptr) {
+                const Work wk = work_of(blockIdx.x, p, (p.num_k64 + 3) / 4);
+                for (int ks = wk.ks0; ks < min(wk.ks1, wk.ks0 + kPrefetchStages); ++ks)
+                    tma_prefetch_2d(&tmB, ks * kBKBytes, wk.t.nb * kBN);
+            }
+            griddep_wait();
+        }
         const int lane = role_value((int)(threadIdx.x & 31));
         const int num_tiles = role_value(p.num_m_blk * p.num_n_blk * p.splits);     // work items
         const int num_ks = role_value((p.num_k64 + 3) / 4);

@@ -273,9 +273,10 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 // thread, are requested together, with the next step's row numbers and weights
 // behind them, so that one memory latency passes per step instead of two and a
 // block start.  Small topk takes more tokens per step: with one row in flight
-// per thread 16384 tokens of topk 1 moved 1.6 TB/s.  topk > kK (= 8) goes round.
+// per thread 16384 tokens of topk 1 moved 1.6 TB/s, with four 5.4 TB/s (at 85
+// registers).  topk > kK (= 8) goes round.
 template <bool kWhole, int kK, int kT>
-__global__ void __launch_bounds__(128, 8) moe_combine_kernel(const MoeRowsParams p)
+__global__ void __launch_bounds__(128, kK == 1 ? 6 : 8) moe_combine_kernel(const MoeRowsParams p)
 {
     static_assert(kK * kT <= 8, "rows by lane");
     griddep_launch_dependents();
@@ -488,10 +489,10 @@ cudaError_t launch_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
     // 128 threads (fewer for short rows) of 64 registers: 1024 threads per SM
     const int threads = p.h >= 1024 ? 128 : ((p.h + 7) / 8 + 31) / 32 * 32, parts = (p.h + threads * 8 - 1) / (threads * 8);
     const int64_t resident = ((int64_t)num_sms * (1024 / threads) + parts - 1) / parts, steps = (p.tokens + kT - 1) / kT;
-    // Persistent blocks from six rounds on (16384 tokens, topk 8, 2048 columns:
+    // Persistent blocks from six rounds on, but for topk 1 (16384 tokens, topk 8, 2048 columns:
     // 87 us, 93 us with a block per step); below, whole rounds are too coarse
     // (1003 tokens, topk 6, 5120 columns: 15.5 us persistent, 13.5 us not).
-    const int64_t blocks = steps < 6 * resident ? steps : resident;
+    const int64_t blocks = kK == 1 || steps < 6 * resident ? steps : resident;
     return launch_dependent(moe_combine_kernel<kWhole, kK, kT>, dim3((unsigned)blocks, (unsigned)parts, 1), threads, 0, s,
                             p);
 }
@@ -499,7 +500,7 @@ cudaError_t launch_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 template <bool kWhole>
 cudaError_t launch_combine_topk(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
-    return p.topk == 1   ? launch_combine<kWhole, 1, 2>(p, num_sms, s)
+    return p.topk == 1   ? launch_combine<kWhole, 1, 4>(p, num_sms, s)
            : p.topk == 2 ? launch_combine<kWhole, 2, 2>(p, num_sms, s)
            : p.topk <= 4 ? launch_combine<kWhole, 4, 1>(p, num_sms, s)
                          : launch_combine<kWhole, 8, 1>(p, num_sms, s);

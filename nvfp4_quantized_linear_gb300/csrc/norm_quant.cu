@@ -357,10 +357,13 @@ cudaError_t launch_norm_quant(const NormQuantParams &p, int num_sms, cudaStream_
     int stages = (int)(kNormRingBytes / ctas / stage_bytes);
     if (stages > kNormMaxStages) stages = kNormMaxStages;
     if (u <= 2 && stages >= 2 && p.m > ctas * num_sms) {
+        NormQuantParams q = p;
+        const cudaError_t e = device_error_word(&q.err_flag);
+        if (e != cudaSuccess) return e;
         const size_t smem = (size_t)stages * stage_bytes;
         const unsigned grid = (unsigned)(ctas * num_sms);
-        return u == 1 ? launch_ring<1>(p, threads, grid, stages, row_bytes, smem, s)
-                      : launch_ring<2>(p, threads, grid, stages, row_bytes, smem, s);
+        return u == 1 ? launch_ring<1>(q, threads, grid, stages, row_bytes, smem, s)
+                      : launch_ring<2>(q, threads, grid, stages, row_bytes, smem, s);
     }
     return u == 1 ? launch_rows<1>(p, threads, s) : u == 2 ? launch_rows<2>(p, threads, s) : launch_rows<4>(p, threads, s);
 }
