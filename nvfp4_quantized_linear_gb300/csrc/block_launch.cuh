@@ -25,8 +25,9 @@ struct NormQuantParams {
     unsigned int *err_flag;                  // device error word (bounded waits)
 };
 
-// Shared memory of an SM that the norm's row rings may take, and rows of a ring.
-constexpr uint32_t kNormRingBytes = 200 * 1024;
+// Shared memory of an SM that the norm's CTAs may take, what a CTA takes beside
+// its ring of rows, and rows of a ring.
+constexpr uint32_t kNormRingBytes = 224 * 1024, kNormCtaBytes = 1536;
 constexpr int kNormMaxStages = 4;
 
 cudaError_t launch_norm_quant(const NormQuantParams &p, int num_sms, cudaStream_t s);

@@ -10,6 +10,8 @@
 // packed codes need no shared memory; the row's fp32 values stay in registers
 // between the sum of squares and the quantization, so each input byte is read
 // once.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "block_launch.cuh"
@@ -104,7 +106,9 @@ __device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int 
         uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = bf16x2_of(h[i]);
-        if (k0 + 16 <= p.k) {
+        if (k0 + 16 <= p.k && (reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+            st_global_v8(o, w);                           // two 16-byte stores would each fill half of 32 sectors
+        } else if (k0 + 16 <= p.k) {
             *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
@@ -350,12 +354,10 @@ cudaError_t launch_norm_quant(const NormQuantParams &p, int num_sms, cudaStream_
     // least.
     const uint32_t row_bytes = (uint32_t)((p.k + 7) / 8 * 16);
     const uint32_t stage_bytes = p.residual != nullptr ? 2 * row_bytes : row_bytes;
-    int ctas = (u == 1 ? 1024 : 512) / threads;
-    if (ctas > 16) ctas = 16;
-    if (ctas < 1) ctas = 1;
-    while (ctas > 1 && kNormRingBytes / ctas / stage_bytes < 2) --ctas;
-    int stages = (int)(kNormRingBytes / ctas / stage_bytes);
-    if (stages > kNormMaxStages) stages = kNormMaxStages;
+    int ctas = std::max(1, std::min(32, (u == 1 ? 1024 : 512) / threads));
+    auto fitting = [&](int n) { return (int)((kNormRingBytes - n * kNormCtaBytes) / n / stage_bytes); };
+    while (ctas > 1 && fitting(ctas) < 2) --ctas;
+    const int stages = std::min(fitting(ctas), kNormMaxStages);
     if (u <= 2 && stages >= 2 && p.m > ctas * num_sms) {
         NormQuantParams q = p;
         const cudaError_t e = device_error_word(&q.err_flag);
