@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col_base = t.nb * kBN + hcol;
             const uint16_t *s_bias = reinterpret_cast<const uint16_t *>(smem + kOffBias) + (it & 1) * kBN + hcol;
             // the warp's residual into L2 while the accumulator is being computed
-            if (kEpi != kEpiPlain && p.residual != nullptr && p.splits == 1) {
+            if (kEpi != kEpiPlain && p.residual != nullptr) {
                 const int64_t r = (int64_t)t.mb * kBM + q * 32 + lane;
                 const int c = kEpi == kEpiGated ? col_base / 2 : col_base;
 #pragma unroll

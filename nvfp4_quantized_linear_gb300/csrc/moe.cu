@@ -233,36 +233,39 @@ __global__ void __launch_bounds__(256) moe_dispatch_kernel(const MoeRowsParams p
 // 16-element block, four neighbours' scale codes stored as one word.
 __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsParams p)
 {
-    const int64_t first = (int64_t)blockIdx.x * p.topk;     // the token's assignments
-    const uint16_t *x = p.x + (int64_t)blockIdx.x * p.ldx;
     griddep_launch_dependents();
     griddep_wait();
+    const int64_t first = (int64_t)blockIdx.x * p.topk;     // the token's assignments
+    const uint16_t *x = p.x + (int64_t)blockIdx.x * p.ldx;
     const float gs = *p.gs;
     const int steps = (p.nbp + blockDim.x - 1) / blockDim.x;
-    for (int u = 0; u < steps; ++u) {
-        const int blk = u * blockDim.x + threadIdx.x;
-        const int k0 = blk * 16;
-        const Raw16 raw = load16_coherent(x, k0, p.h);
-        float v0[8], v1[8];
-        unpack8(raw.a, v0);
-        unpack8(raw.b, v1);
-        float amax = 0.0f;
+    for (int kb = 0; kb < p.topk; kb += 8) {                // (topk > 8 quantizes the row again per eight)
+        const int mine = rows_by_lane(p, first + kb, p.topk - kb);
+        for (int u = 0; u < steps; ++u) {
+            const int blk = u * blockDim.x + threadIdx.x;
+            const int k0 = blk * 16;
+            const Raw16 raw = load16_coherent(x, k0, p.h);
+            float v0[8], v1[8];
+            unpack8(raw.a, v0);
+            unpack8(raw.b, v1);
+            float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = max_abs3(amax, v0[i], v1[i]);
-        const uint32_t code = cvt_e4m3x2(0.0f, div6_rn(__fmul_rn(amax, gs))) & 0x7Fu;
-        const float d = e4m3_to_f32(code);
-        const float inv = d == 0.0f ? 0.0f : __fdiv_rn(gs, d);
-        const uint2 q = make_uint2(quant8(v0, inv), quant8(v1, inv));
-        const uint32_t c1 = __shfl_down_sync(kFull, code, 1);
-        const uint32_t c2 = __shfl_down_sync(kFull, code, 2);
-        const uint32_t c3 = __shfl_down_sync(kFull, code, 3);
-        const uint32_t word = code | (c1 << 8) | (c2 << 16) | (c3 << 24);
-        for (int k = 0; k < p.topk; ++k) {
-            const int r = row_of(p, first + k);
-            if (r < 0) continue;
-            if (blk < p.nb) *reinterpret_cast<uint2 *>(p.q + (int64_t)r * (p.kp / 2) + k0 / 2) = q;
-            if ((threadIdx.x & 3) == 0 && blk < p.nb)
-                *reinterpret_cast<uint32_t *>(p.sf + sf_offset(r, blk, p.nbp)) = word;
+            for (int i = 0; i < 8; ++i) amax = max_abs3(amax, v0[i], v1[i]);
+            const uint32_t code = cvt_e4m3x2(0.0f, div6_rn(__fmul_rn(amax, gs))) & 0x7Fu;
+            const float d = e4m3_to_f32(code);
+            const float inv = d == 0.0f ? 0.0f : __fdiv_rn(gs, d);
+            const uint2 q = make_uint2(quant8(v0, inv), quant8(v1, inv));
+            const uint32_t c1 = __shfl_down_sync(kFull, code, 1);
+            const uint32_t c2 = __shfl_down_sync(kFull, code, 2);
+            const uint32_t c3 = __shfl_down_sync(kFull, code, 3);
+            const uint32_t word = code | (c1 << 8) | (c2 << 16) | (c3 << 24);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = __shfl_sync(kFull, mine, k);
+                if (r < 0 || blk >= p.nb) continue;
+                *reinterpret_cast<uint2 *>(p.q + (int64_t)r * (p.kp / 2) + k0 / 2) = q;
+                if ((threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t *>(p.sf + sf_offset(r, blk, p.nbp)) = word;
+            }
         }
     }
 }
