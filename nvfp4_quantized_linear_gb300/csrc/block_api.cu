@@ -23,7 +23,8 @@ nvfp4_status check_moe(int64_t tokens, int topk)
 {
     if (topk < 1 || topk > nvfp4::kMoeMaxTopk)
         return fail(NVFP4_ERR_INVALID_ARG, "topk must be in [1, %d] (got %d)", nvfp4::kMoeMaxTopk, topk);
-    if (tokens < 0 || tokens > kMaxDim / topk)
+    // (a grid of one block per token and 16 per expert stays below 2^31)
+    if (tokens < 0 || tokens > (kMaxDim - 16 * nvfp4::kMoeMaxExperts) / topk)
         return fail(NVFP4_ERR_INVALID_ARG, "tokens out of range: %lld", (long long)tokens);
     return NVFP4_OK;
 }
