@@ -82,6 +82,26 @@ __device__ __forceinline__ void store_tail_columns(const GemmParams &p, int64_t 
         if (e < n) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
 }
 
+// One warp stores its staged 32-row x 64-column output chunk (128-byte rows with
+// the TMA's 128-byte swizzle; kTail: the output's last columns may end inside 16
+// bytes).
+template <bool kTail>
+__device__ __forceinline__ void store_chunk(const GemmParams &p, const CUtensorMap *map, uint32_t stage, int col, int row,
+                                            int lane, uint64_t policy)
+{
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0 && (!kTail || col < tma_cols(p.out_cols))) {
+        tma_store_2d(map, stage, col, row, policy);
+        bulk_commit_group();
+    }
+    if (kTail && (p.out_cols & 7) != 0) {           // uniform: the chunk that holds the last columns
+        const int piece = (tma_cols(p.out_cols) - col) >> 3;
+        if (piece >= 0 && piece < 8 && row + lane < p.m)
+            store_tail_columns(p, row + lane, ld_shared_v4(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)));
+    }
+}
+
 // The epilogue variant a launch needs, and whether it needs the parts that the
 // kernels' kFull instances add: a residual, or output columns that end inside
 // 16 bytes.

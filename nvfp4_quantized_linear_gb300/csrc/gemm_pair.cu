@@ -124,25 +124,6 @@ __device__ __forceinline__ bool wait_residual(const GemmParams &p, uint64_t *bar
     return __all_sync(~0u, ok);
 }
 
-// One warp stores its staged 32-row x 64-column output chunk (kTail: the
-// output's last columns may end inside 16 bytes).
-template <bool kTail>
-__device__ __forceinline__ void store_chunk(const GemmParams &p, const CUtensorMap *map, uint32_t stage, int col, int row,
-                                            int lane, uint64_t policy)
-{
-    fence_proxy_async_shared();
-    __syncwarp();
-    if (lane == 0 && (!kTail || col < tma_cols(p.out_cols))) {
-        tma_store_2d(map, stage, col, row, policy);
-        bulk_commit_group();
-    }
-    if (kTail && (p.out_cols & 7) != 0) {           // uniform: the chunk that holds the last columns
-        const int piece = (tma_cols(p.out_cols) - col) >> 3;
-        if (piece >= 0 && piece < 8 && row + lane < p.m)
-            store_tail_columns(p, row + lane, ld_shared_v4(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)));
-    }
-}
-
 // kMx: MXFP4 operands (UE8M0 scales per 32 K-elements, scale_vec::2X), else NVFP4.
 // kEpi: the epilogue variant (epilogue.cuh).  kFull: with a residual (if one is
 // given) and columns that end inside 16 bytes; its registers and code stay out

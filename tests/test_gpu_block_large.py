@@ -1,0 +1,102 @@
+"""Offsets past 2^31 elements and graph capture of the operators around the linear."""
+import os
+import sys
+
+import pytest
+import torch
+
+from _helpers import dev_scalar, nv, require_library, syn
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+import ffn_block  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    return require_library()
+
+
+def _spread(rows, stride, make):
+    """A [len(rows), cols] tensor's rows written `stride` elements apart, as a strided view."""
+    src = make
+    full = torch.empty((src.shape[0] - 1) * stride + src.shape[1], dtype=torch.bfloat16, device="cuda")
+    view = full.as_strided(src.shape, (stride, 1))
+    view.copy_(src)
+    return view
+
+
+def test_norm_rows_past_2_31_elements():
+    x = syn.bf16_outlier_channels(3, 4096, 1).cuda()
+    r = syn.bf16_outlier_channels(3, 4096, 2).cuda()
+    gamma = torch.ones(4096, dtype=torch.bfloat16, device="cuda")
+    a = nv.add_rmsnorm_quant(x, gamma, 1e-6, residual=r, fmt=nv.NVFP4_FORMAT_MXFP8)
+    far = _spread(3, 1 << 30, x)
+    b = nv.add_rmsnorm_quant(far, gamma, 1e-6, residual=r, fmt=nv.NVFP4_FORMAT_MXFP8)
+    torch.cuda.synchronize()
+    assert all(torch.equal(i, j) for i, j in zip(a, b))
+
+
+def test_moe_rows_past_2_31_elements():
+    tokens, topk, e, h, ld = 40, 2, 3, 64, 1 << 23
+    ids = torch.randint(0, e, (tokens, topk), generator=torch.Generator().manual_seed(3)).int().cuda()
+    offsets, counts, dest = nv.moe_sort(ids, e)
+    rows = nv.nvfp4_moe_rows(tokens, topk, e)
+    assert rows * ld > 1 << 31
+    x = syn.bf16_normal((tokens, h), 1.0, 4).cuda()
+    w = torch.rand((tokens, topk), device="cuda")
+    near = torch.zeros((rows, h), dtype=torch.bfloat16, device="cuda")
+    far = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda").as_strided((rows, h), (ld, 1))
+    far.zero_()
+    nv.moe_dispatch(x, dest, offsets, counts, out=near)
+    nv.moe_dispatch(x, dest, offsets, counts, out=far)
+    torch.cuda.synchronize()
+    assert torch.equal(near, far)
+    assert torch.equal(nv.moe_combine(near, dest, w), nv.moe_combine(far, dest, w))
+    g = nv.moe_combine_backward(x, far, w, dest, offsets, counts, dy=far.clone())
+    n = nv.moe_combine_backward(x, near, w, dest, offsets, counts, dy=near.clone())
+    torch.cuda.synchronize()
+    assert torch.equal(g[1], n[1]) and torch.equal(g[0], n[0])
+
+
+@pytest.mark.parametrize("m", [3, 150])
+def test_residual_and_output_rows_past_2_31_elements(m):
+    k, n = 256, 136
+    stride = (1 << 31) // (m - 1) // 8 * 8 + 64
+    x = syn.bf16_outlier_channels(m, k, 5).cuda()
+    w = syn.bf16_normal((n, k), 0.05, 6)
+    gw = syn.global_scale(w)
+    w_fp4, w_sf = nv.prepare_weight(w.cuda(), dev_scalar(gw))
+    res = syn.bf16_normal((m, n), 1.0, 7).cuda()
+    args = (w_fp4, w_sf, k, n, dev_scalar(20.0), dev_scalar(syn.alpha_of(20.0, gw)))
+    a = nv.linear(x, *args, act="silu", residual=res)
+    out = torch.empty((m - 1) * stride + n, dtype=torch.bfloat16, device="cuda").as_strided((m, n), (stride, 1))
+    nv.linear(x, *args, act="silu", residual=_spread(m, stride, res), out=out)
+    torch.cuda.synchronize()
+    nv.nvfp4_device_error()
+    assert torch.equal(a, out)
+
+
+def test_graph_capture_of_both_ffn_blocks():
+    """Captured once, replayed on new inputs: equal to the eager calls."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)  # noqa: E731
+    k, f, e, m = 256, 384, 8, 40
+    dense = ffn_block.DenseFFN(1 + rnd(k, std=0.1), rnd(f, k, std=0.05), rnd(f, k, std=0.05), rnd(k, f, std=0.05))
+    moe = ffn_block.MoEFFN(rnd(e, k, std=0.1), rnd(e, f, k, std=0.05), rnd(e, f, k, std=0.05), rnd(e, k, f, std=0.05), 2)
+    x, r = rnd(m, k), rnd(m, k)
+    dense.calibrate(x, r)
+    moe.calibrate(x)
+    for _ in range(2):
+        dense(x, r), moe(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a, b = dense(x, r), moe(x)
+    for _ in range(2):
+        x.copy_(rnd(m, k))
+        r.copy_(rnd(m, k))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, dense(x, r)) and torch.equal(b, moe(x))

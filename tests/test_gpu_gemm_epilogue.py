@@ -233,10 +233,12 @@ def test_transform_path():
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
 
 
+@pytest.mark.parametrize("k", [264, 4104])
 @pytest.mark.parametrize("act", ["none", "relu", "swiglu"])
-def test_grouped(act):
-    """Each group against its own expert, bias included; bands past the groups untouched."""
-    group_m, k, n = [130, 0, 1, 128], 264, 192 if act == "swiglu" else 384
+def test_grouped(act, k):
+    """Each group against its own expert, bias included; bands past the groups
+    untouched.  Both shared-memory layouts (short and long K)."""
+    group_m, n = [130, 0, 1, 128], 192 if act == "swiglu" else 384
     nw = 384
     offsets = np.concatenate([[0], np.cumsum([(g + 127) // 128 * 128 for g in group_m])]).astype(np.int32)
     rows = int(offsets[-1]) + 128
