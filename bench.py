@@ -167,7 +167,7 @@ def gemm_source_hash() -> str:
     """Fingerprint of the headline's dominant kernel (the CTA-pair GEMM): its
     translation unit and the headers it includes."""
     h = hashlib.sha256()
-    for name in ("gemm_pair.cu", "gemm_common.cuh", "ptx.cuh", "common.cuh"):
+    for name in ("gemm_pair.cu", "gemm_common.cuh", "epilogue.cuh", "ptx.cuh", "common.cuh"):
         with open(os.path.join(ROOT, "nvfp4_quantized_linear_gb300", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]

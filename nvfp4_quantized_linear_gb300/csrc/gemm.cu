@@ -24,7 +24,11 @@
 //   warps 8..15 epilogue, two per TMEM lane quarter (128 columns each):
 //               tcgen05.ld of finished accumulators, fma with alpha and bias, bf16 round into
 //               registers, release of the TMEM tile, then masked stores
-//               (rows < m, cols < n_out) that overlap the next tile's MMAs.
+//               (rows < m, cols < n_out) that overlap the next tile's MMAs;
+//               with an activation, gate or residual the raw accumulator goes
+//               to registers and the arithmetic overlaps too.
+// Grouped GEMMs (mixture of experts) run here: a tile's row band names its group,
+// and with it the weight rows, alpha and bias.
 // Split-K (small m): the K ranges of a tile run as the CTAs of one thread-block
 // cluster, one range each; the drain writes the raw fp32 sums into the CTA's
 // own shared memory, and after a cluster barrier every CTA sums its share of

@@ -24,8 +24,9 @@
 //               completes once both CTAs hold the stage's operands and scales;
 //   warps 8..15 epilogue, two per TMEM lane quarter: load this CTA's whole
 //               accumulator into registers (four loads in flight), hand it
-//               back to the MMA warp, then apply alpha and bias, round to bf16
-//               and TMA-store the rows.
+//               back to the MMA warp, then apply alpha and bias, in the other
+//               instances also an activation, a gate and a residual, round to
+//               bf16 and TMA-store the rows.
 // Per SM and stage this moves 38 KB into shared memory instead of 54 KB, so
 // five stages fit where the one-CTA kernel holds four.  Every mbarrier wait is
 // bounded; all threads meet at one final cluster barrier before the TMEM is
