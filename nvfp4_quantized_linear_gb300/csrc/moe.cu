@@ -259,8 +259,7 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
             const uint32_t c2 = __shfl_down_sync(kFull, code, 2);
             const uint32_t c3 = __shfl_down_sync(kFull, code, 3);
             const uint32_t word = code | (c1 << 8) | (c2 << 16) | (c3 << 24);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < min(8, p.topk - kb); ++k) {
                 const int r = __shfl_sync(kFull, mine, k);
                 if (r < 0 || blk >= p.nb) continue;
                 *reinterpret_cast<uint2 *>(p.q + (int64_t)r * (p.kp / 2) + k0 / 2) = q;
