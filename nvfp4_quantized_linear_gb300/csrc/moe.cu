@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortPa
         const int e = tid % width, g = tid / width;
         if (e < experts && g < groups) {
             int before = 0, total = 0;
-#pragma unroll 8
+#pragma unroll 16
             for (int b = g; b < (int)gridDim.x; b += groups) {
                 const int c = p.hist[(int64_t)b * experts + e];
                 before += b < (int)blockIdx.x ? c : 0;

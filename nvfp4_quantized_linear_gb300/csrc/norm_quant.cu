@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantParams 
     griddep_launch_dependents();
     griddep_wait();
     if (row >= p.m) {                                    // padding rows of the last scale band
-        zero_scale_row(p, row);
+        for (int r = row; r < p.mp; r += gridDim.x - p.m) zero_scale_row(p, r);
         return;
     }
     const uint16_t *x = p.x + (int64_t)row * p.ldx;
@@ -312,7 +312,9 @@ cudaError_t launch_rows(const NormQuantParams &p, int threads, cudaStream_t s)
     void (*kernel)(NormQuantParams) = p.fmt == kFmtNvfp4   ? norm_quant_kernel<kFmtNvfp4, U>
                                       : p.fmt == kFmtMxfp4 ? norm_quant_kernel<kFmtMxfp4, U>
                                                            : norm_quant_kernel<kFmtMxfp8, U>;
-    return launch_dependent(kernel, (unsigned)p.mp, threads, 0, s, p);
+    // a block per row and up to 16 for the padding rows: a dependent GEMM starts
+    // on the SMs that no block occupies
+    return launch_dependent(kernel, (unsigned)(p.m + std::min(16, p.mp - p.m)), threads, 0, s, p);
 }
 
 template <int kFmt, int U>
