@@ -94,6 +94,8 @@ nvfp4_status nvfp4_add_rmsnorm_quant(const void *x_bf16, int64_t ldx, const void
     p.ldh = ldh;
     p.h = static_cast<uint16_t *>(h_bf16);
     p.eps = eps;
+    p.inv_k = (float)(1.0 / (double)k);
+    p.inv_k_lo = (float)(1.0 / (double)k - (double)p.inv_k);
     p.fmt = format;
     p.m = (int32_t)m;
     p.k = (int32_t)k;

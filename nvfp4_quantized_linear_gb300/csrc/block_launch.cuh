@@ -18,6 +18,7 @@ struct NormQuantParams {
     int64_t ldx, ldr, ldh;
     uint16_t *h;                             // [m, ldh] bf16 or nullptr
     float eps;
+    float inv_k, inv_k_lo;                   // 1 / k as hi + lo
     int32_t fmt;
     int32_t m, k, kp, nb, nbp, mp;           // as in QuantParams, nb in the format's blocks
     const float *gs;                         // device fp32 (NVFP4)

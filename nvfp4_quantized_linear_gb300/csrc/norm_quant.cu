@@ -70,23 +70,47 @@ __device__ __forceinline__ float sum_squares(const Pairs &h, float sum)
     return lo + hi;
 }
 
-// Sum over the block of one value per thread, the same in every thread and in
-// a fixed order.  `part` holds 32 floats that no thread still reads.
+// Sum over the block (kWarps warps at most) of one value per thread, the same in
+// every thread and in a fixed order.  `part` holds kWarps floats that no thread
+// still reads, zeros past the block's warps.  Every thread adds the warps' sums
+// itself: one shared-memory latency where a second round of shuffles takes five.
+template <int kWarps>
 __device__ __forceinline__ float block_sum(float v, float *part)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.0f;
+    uint64_t a = 0, b = 0;                               // (two floats each)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
+    for (int i = 0; i < kWarps / 4; ++i) {
+        const ulonglong2 w = reinterpret_cast<const ulonglong2 *>(part)[i];
+        a = add2(a, w.x);
+        b = add2(b, w.y);
+    }
+    float s0, s1;
+    unpack2(add2(a, b), s0, s1);
+    return s0 + s1;
 }
 
+// 1 / sqrt(sum / k + eps): the approximate root r of the rounded mean + eps, and
+// one Newton step whose residual 1 - a r^2 has the remainders of the product with
+// 1 / k, of the sum with eps and of the square in it, so that only the last
+// addition rounds.  A row's codes share this error: the IEEE quotient and root
+// instead, each rounded by itself, put 81 codes of 4096 x 4096 on the wrong side of
+// a threshold (an exact form's codes taken as right), this 42, and it is shorter:
+// 16384 x 5120 without a residual takes 47.4 us instead of 49.7.
 __device__ __forceinline__ float rstd_of(float sum, const NormQuantParams &p)
 {
-    return __frsqrt_rn(__fdiv_rn(sum, (float)p.k) + p.eps);
+    const float mean = __fmul_rn(sum, p.inv_k);
+    const float mean_lo = __fmaf_rn(sum, p.inv_k, -mean) + sum * p.inv_k_lo;
+    const float a = __fadd_rn(mean, p.eps);
+    const float added = __fsub_rn(a, mean);              // what the sum took of eps, and of the mean
+    const float a_lo = __fadd_rn(__fsub_rn(mean, __fsub_rn(a, added)), __fsub_rn(p.eps, added)) + mean_lo;
+    const float r = rsqrtf(a);
+    const float rr = __fmul_rn(r, r);
+    const float e = __fmaf_rn(-a, rr, 1.0f) - a * __fmaf_rn(r, r, -rr) - a_lo * rr;
+    return fabsf(e) < 1.0f ? __fmaf_rn(0.5f * r, e, r) : r;   // (an infinite or zero mean has no residual)
 }
 
 __device__ __forceinline__ void zero_scale_row(const NormQuantParams &p, int row)
@@ -96,7 +120,7 @@ __device__ __forceinline__ void zero_scale_row(const NormQuantParams &p, int row
 }
 
 // The second half of a row's work for one thread's 16 elements at k0: h, then
-// y = (h * rstd) * gamma into codes and a scale.
+// y = (h * gamma) * rstd into codes and a scale.
 template <int kFmt>
 __device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int k0, const Pairs &h, float rstd,
                                          const Raw16 &gamma, float gs)
@@ -123,7 +147,7 @@ __device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int 
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y[i] = mul2(mul2(h[i], rs), y[i]);
+        y[i] = mul2(mul2(h[i], y[i]), rs);                // h gamma is exact in most cases: 8 bits by few more
         float lo, hi;
         unpack2(y[i], lo, hi);
         amax = max_abs3(amax, lo, hi);
@@ -168,9 +192,10 @@ __device__ __forceinline__ void finish16(const NormQuantParams &p, int row, int 
 template <int kFmt, int U>
 __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantParams p)
 {
-    __shared__ float s_part[32];
+    __shared__ __align__(16) float s_part[32];
     const int tid = threadIdx.x;
     const int row = blockIdx.x;
+    if (tid < 32 && tid >= blockDim.x / 32) s_part[tid] = 0.0f;
     griddep_launch_dependents();
     griddep_wait();
     if (row >= p.m) {                                    // padding rows of the last scale band
@@ -189,11 +214,13 @@ __global__ void __launch_bounds__(1024) norm_quant_kernel(const NormQuantParams 
         sum = sum_squares(h[u], sum);
     }
     const float gs = kFmt == kFmtNvfp4 ? *p.gs : 1.0f;
-    const float rstd = rstd_of(block_sum(sum, s_part), p);
+    Raw16 gamma = load16_coherent(p.gamma, tid * 16, p.k);       // the first step's, before the sum's barrier
+    const float rstd = rstd_of(block_sum<32>(sum, s_part), p);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int k0 = (u * blockDim.x + tid) * 16;
-        finish16<kFmt>(p, row, k0, h[u], rstd, load16_coherent(p.gamma, k0, p.k), gs);
+        if (u > 0) gamma = load16_coherent(p.gamma, k0, p.k);
+        finish16<kFmt>(p, row, k0, h[u], rstd, gamma, gs);
     }
 }
 
@@ -228,8 +255,9 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
 {
     extern __shared__ __align__(128) uint8_t ring[];      // [stages][x row, residual row]
     __shared__ uint64_t full[kNormMaxStages];
-    __shared__ float s_part[2][32];
+    __shared__ __align__(16) float s_part[2][16];
     const int tid = threadIdx.x;
+    if (tid < 32 && tid % 16 >= blockDim.x / 32) s_part[tid / 16][tid % 16] = 0.0f;
     const bool use_res = p.residual != nullptr;
     const uint32_t stage_bytes = use_res ? 2 * row_bytes : row_bytes;
     griddep_launch_dependents();
@@ -280,7 +308,7 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
             sum = sum_squares(h[u], sum);
         }
         // after the sum's barrier every thread has read the stage: refill it
-        const float rstd = rstd_of(block_sum(sum, s_part[it & 1]), p);
+        const float rstd = rstd_of(block_sum<16>(sum, s_part[it & 1]), p);
         if (tid == 0 && row + stages * step < p.m) request(row + stages * step, s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
