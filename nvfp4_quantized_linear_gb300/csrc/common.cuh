@@ -64,7 +64,7 @@ struct GemmParams {
     // rounding.  splits == 1: no split.
     int32_t splits;                  // 1 .. kMaxSplits
     int32_t stages_per_split;
-    // Grouped GEMM (one-CTA kernel only): group_offsets [num_groups + 1] are
+    // Grouped GEMM: group_offsets [num_groups + 1] are
     // ascending row offsets, multiples of 128; the 128-row band of A at row r
     // belongs to the group g with offsets[g] <= r < offsets[g + 1] and is
     // multiplied by weight rows [g * group_n, (g + 1) * group_n) (stacked
@@ -115,7 +115,10 @@ cudaError_t launch_linear_fused(const GemmParams &p, const uint8_t *w, int num_s
 // Clusters of `splits` one-CTA GEMM blocks that can be resident at once (the
 // split-K plan's wave count).
 int gemm_split_clusters(int splits, int num_sms);
-// CTA-pair variant for m > 128 (tiles of 256 x 256 on two SMs).
+// CTA-pair variant for m > 128 (tiles of 256 x 256 on two SMs), grouped GEMMs that
+// grouped_on_pairs() names among them.
+constexpr int kPairMaxGroups = 256;
+bool grouped_on_pairs(const GemmParams &p);
 cudaError_t launch_gemm_pair(const GemmParams &p, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,
                              const char **why, bool dependent = false);
 

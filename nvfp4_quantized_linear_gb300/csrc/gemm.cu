@@ -27,7 +27,7 @@
 //               (rows < m, cols < n_out) that overlap the next tile's MMAs;
 //               with an activation, gate or residual the raw accumulator goes
 //               to registers and the arithmetic overlaps too.
-// Grouped GEMMs (mixture of experts) run here: a tile's row band names its group,
+// Grouped GEMMs (mixture of experts) of small groups run here: a tile's row band names its group,
 // and with it the weight rows, alpha and bias.
 // Split-K (small m): the K ranges of a tile run as the CTAs of one thread-block
 // cluster, one range each; the drain writes the raw fp32 sums into the CTA's
@@ -1021,9 +1021,11 @@ constexpr OneCtaKernel kGroupedKernels[3] = {            // [epilogue variant]
 // Whether a grouped GEMM takes the wide layout: where a tile's K is short, its
 // epilogue, which the wide staging makes two to four times as fast, outlasts the
 // next tile's MMAs; where it is long, the fourth operand stage counts for more.
-// Measured (narrow / wide, us; 256 rows per expert): plain at K = 768 20.5 / 16.9,
-// 1024 21.6 / 21.2, 1280 22.9 / 23.1; SWIGLU at 1024 25.8 / 21.3, 2048 23.8 / 23.8,
-// 3584 23.0 / 24.5; SILU at 2048 30.3 / 25.9, 3584 26.5 / 26.1, 5120 32.4 / 33.6.
+// Measured (narrow / wide, us; 64 experts of 128 and 256 rows in turn, 2048 weight
+// rows each): plain at K = 768 27.9 / 24.0, 1024 29.8 / 29.7, 1280 32.4 / 33.2;
+// SWIGLU at 1280 37.2 / 31.6, 2048 40.8 / 41.5, 3584 61.8 / 66.2 (32 of 128 rows:
+// 1280 18.1 / 15.7, 2048 21.0 / 21.2); SILU at 2048 53.6 / 45.2, 3584 69.2 / 70.9
+// (33.5 / 32.6), 5120 94.3 / 97.6.
 bool grouped_wide(const GemmParams &p)
 {
     constexpr int kMaxStages[3] = {4, 14, 8};            // 256-element K stages, by epilogue variant

@@ -1,4 +1,5 @@
-// Block-scaled FP4 GEMM on CTA pairs (tcgen05 cta_group::2), for m > 128.
+// Block-scaled FP4 GEMM on CTA pairs (tcgen05 cta_group::2), for m > 128, and
+// grouped GEMMs of large groups.
 //
 // Same operation as gemm.cu (page "TorchNvFp4LinearKernel", vLLM PR #53319,
 // section 关键源码片段: _scaled_mm, * alpha, slice, + bias), with each output
@@ -31,6 +32,8 @@
 // five stages fit where the one-CTA kernel holds four.  Every mbarrier wait is
 // bounded; all threads meet at one final cluster barrier before the TMEM is
 // released.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -62,7 +65,9 @@ constexpr uint32_t kOffSfb = kOffSfa + kStages * kSfaBytes;
 constexpr uint32_t kOffBias = kOffSfb + kStages * kSfbBytes;  // per epilogue warp: its 128 bias columns (bf16)
 constexpr uint32_t kOffOut = (kOffBias + 8 * kEpiColsBias * 2 + 1023) / 1024 * 1024;   // one chunk per epilogue warp
 constexpr uint32_t kOffBar = kOffOut + 8 * kOutChunkBytes;
+constexpr uint32_t kOffGroups = kOffBar + 512;                // grouped: the pair tiles before each group
 constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;         // barriers + alignment slack
+constexpr uint32_t kSmemBytesGrouped = kSmemBytes + (kPairMaxGroups + 4) * 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSf = 256;
 constexpr uint32_t kSfColsPerStage = 48;
@@ -76,7 +81,7 @@ constexpr uint16_t kBothCtas = 0x3;
 // accumulator slice (128 registers) at once
 constexpr uint32_t kRegsCtl = 56, kRegsSf = 88, kRegsEpi = 184;
 
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kSmemBytesGrouped <= 232448, "shared memory budget");
 static_assert(kOffOut % 1024 == 0, "128-byte-swizzled TMA store sources are 1024-byte aligned");
 static_assert(kTmemSf + kStages * kSfColsPerStage <= kTmemCols, "TMEM budget");
 static_assert(128 * (kRegsCtl + kRegsSf + 2 * kRegsEpi) <= kThreads * 128, "register reallocation budget");
@@ -88,18 +93,90 @@ struct Role {
     bool is_leader;
 };
 
-__device__ __forceinline__ Role enter_role(const GemmParams &p, const uint32_t *tmem_slot)
+template <bool kGrouped>
+__device__ __forceinline__ Role enter_role(const GemmParams &p, const uint32_t *tmem_slot, const int32_t *tiles_before)
 {
     Role r;
     r.lane = role_value((int)(threadIdx.x & 31));
     r.pair_id = role_value((int)(blockIdx.x >> 1));
     r.num_pairs = role_value((int)(gridDim.x >> 1));
-    r.num_tiles = role_value(p.num_m_blk * p.num_n_blk);       // num_m_blk counts 256-row tiles here
+    r.num_tiles = role_value((kGrouped ? tiles_before[p.num_groups] : p.num_m_blk) * p.num_n_blk);   // 256-row tiles
     r.num_ks = role_value((p.num_k64 + 3) / 4);
     r.rank = cluster_ctarank();
     r.is_leader = r.rank == 0;
     r.tmem = role_tmem(tmem_slot);
     return r;
+}
+
+// A tile of the walk as the roles see it: this CTA's 128-row band of A, whether
+// the tile has that band, the first of its weight rows and, within the group's
+// output columns, its column block.
+struct PairTile {
+    int band, nb, w_row, group;
+    bool here;
+};
+
+// Grouped GEMMs: a group's bands in pair tiles of two (the last one's second band
+// is missing where their number is odd: that CTA copies no rows and stores none),
+// the groups in order, row tiles fastest within a group, so that the pairs share
+// the tiles evenly whatever the groups' sizes.  A role's tiles ascend, so its
+// place among the groups only moves on.  Four operand stages and two output chunks
+// per warp instead of five and one: slower (32 groups of 256 rows, 4096 x 4096:
+// 69.3 us against 66.4; 2048 x 768: 16.2 against 16.0).
+struct GroupWalk {
+    int g, before, next, first, end;                // the group, pair tiles before it and up to its end, its bands
+};
+
+__device__ __forceinline__ int first_band(const GemmParams &p, int g)
+{
+    const int bands = (p.m + kRowsCta - 1) / kRowsCta;
+    return min(max((p.group_offsets[g] + kRowsCta - 1) / kRowsCta, 0), bands);
+}
+
+// One warp: tiles_before[g] for g in [0, num_groups], eight groups per lane.
+__device__ __forceinline__ void count_group_tiles(const GemmParams &p, int32_t *tiles_before, int lane)
+{
+    constexpr int kPerLane = kPairMaxGroups / 32;
+    int at[kPerLane + 1], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= kPerLane; ++i) at[i] = first_band(p, min(lane * kPerLane + i, p.num_groups));
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) sum += (max(at[i + 1] - at[i], 0) + 1) / 2;
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += v;
+    }
+    before -= sum;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        if (lane * kPerLane + i <= p.num_groups) tiles_before[lane * kPerLane + i] = before;
+        before += (max(at[i + 1] - at[i], 0) + 1) / 2;
+    }
+    if (lane == 31 && p.num_groups == kPairMaxGroups) tiles_before[kPairMaxGroups] = before;
+}
+
+template <bool kGrouped>
+__device__ __forceinline__ PairTile pair_tile(int tile, const GemmParams &p, uint32_t rank, const int32_t *tiles_before,
+                                              GroupWalk &walk)
+{
+    if constexpr (kGrouped) {
+        if (tile >= walk.next * p.num_n_blk) {
+            do walk.next = tiles_before[++walk.g + 1];
+            while (tile >= walk.next * p.num_n_blk);
+            walk.before = tiles_before[walk.g];
+            walk.first = first_band(p, walk.g);
+            walk.end = first_band(p, walk.g + 1);
+        }
+        const int within = tile - walk.before * p.num_n_blk, rows = walk.next - walk.before;
+        const int nb = within / rows, band = walk.first + 2 * (within - nb * rows) + (int)rank;
+        return {band, nb, walk.g * p.group_n + nb * kTileN, walk.g, band < walk.end};
+    } else {
+        const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
+        const int band = t.mb * 2 + (int)rank;
+        return {band, t.nb, t.nb * kTileN, 0, band < (p.m + kRowsCta - 1) / kRowsCta};
+    }
 }
 
 // One warp requests a 32-row x 64-column chunk of the residual into its output
@@ -129,8 +206,8 @@ __device__ __forceinline__ bool wait_residual(const GemmParams &p, uint64_t *bar
 // kEpi: the epilogue variant (epilogue.cuh).  kFull: with a residual (if one is
 // given) and columns that end inside 16 bytes; its registers and code stay out
 // of the other instances (8192 x 4096 x 28672 without either: 286 us, 310 us
-// with the tail's code alone).
-template <bool kMx, int kEpi, bool kFull>
+// with the tail's code alone).  kGrouped: a grouped GEMM (NVFP4, no residual).
+template <bool kMx, int kEpi, bool kFull, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmSfb, const __grid_constant__ CUtensorMap tmOut,
@@ -148,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *sf_empty = sf_full + kStages;                           // the scale warps have read them
     uint64_t *res_full = sf_empty + kStages;                          // [kEpiWarps] a residual chunk landed
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_full + kEpiWarps);
+    int32_t *const tiles_before = reinterpret_cast<int32_t *>(smem + kOffGroups);
 
     const int warp = threadIdx.x >> 5;
 
@@ -175,6 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc_pair(tmem_slot, kTmemCols);
         tmem_relinquish_pair();
     }
+    if (kGrouped && warp == 2) {
+        griddep_wait();                 // the kernel before may write the offsets
+        count_group_tiles(p, tiles_before, threadIdx.x & 31);
+    }
     tc_fence_before_sync();
     __syncwarp();
     cluster_sync_all();                 // barrier inits and the TMEM allocation visible in both CTAs
@@ -182,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kEpiWarp0) {
         setmaxnreg_inc<kRegsEpi>();
         if (p.wait_all) griddep_wait();
-        const Role role = enter_role(p, tmem_slot);
+        const Role role = enter_role<kGrouped>(p, tmem_slot, tiles_before);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t rank = role.rank, tmem = role.tmem;
         // ------------------------------------------------------ epilogue --
@@ -193,28 +275,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t leader_tmem_empty = mapa_shared(tmem_empty, 0);
         const bool use_bias = p.bias != nullptr;
         const bool bias_vec = (reinterpret_cast<uintptr_t>(p.bias) & 7) == 0;   // 8-byte loads of 4 columns
-        const float alpha = p.alpha != nullptr ? __ldg(p.alpha) : 1.0f;
+        float alpha = p.alpha != nullptr && !kGrouped ? __ldg(p.alpha) : 1.0f;
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
         const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
         uint32_t res_phase = 0;
-        int it = 0;
-        for (int tile = role.pair_id; tile < num_tiles; tile += num_pairs, ++it) {
-            const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
-            const int n_cols = min(kEpiCols, p.n_out - t.nb * kTileN - hcol);   // may be <= 0
+        GroupWalk walk = {-1, 0, 0, 0, 0};
+        for (int tile = role.pair_id; tile < num_tiles; tile += num_pairs) {
+            const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
+            const int n_cols = kGrouped && !t.here ? 0 : min(kEpiCols, p.n_out - t.nb * kTileN - hcol);   // may be <= 0
             const int col_base = t.nb * kTileN + hcol;
+            if constexpr (kGrouped) alpha = p.alpha[t.group];
             // this warp's 128 bias columns into its own buffer (four per lane)
             // while the accumulator is still being computed
             uint16_t *s_bias = reinterpret_cast<uint16_t *>(smem + kOffBias) + (warp - kEpiWarp0) * kEpiColsBias;
             if (use_bias) {
                 const int c0 = col_base + 4 * lane;
                 uint2 bw = make_uint2(0u, 0u);
+                const uint16_t *const bias = kGrouped ? p.bias + (int64_t)t.group * p.group_n : p.bias;
                 if (bias_vec && c0 + 4 <= p.n_out) {
-                    bw = __ldg(reinterpret_cast<const uint2 *>(p.bias + c0));
+                    bw = __ldg(reinterpret_cast<const uint2 *>(bias + c0));
                 } else {
                     uint16_t e[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) e[i] = (c0 + i < p.n_out) ? p.bias[c0 + i] : (uint16_t)0;
+                    for (int i = 0; i < 4; ++i) e[i] = (c0 + i < p.n_out) ? bias[c0 + i] : (uint16_t)0;
                     bw = make_uint2(e[0] | ((uint32_t)e[1] << 16), e[2] | ((uint32_t)e[3] << 16));
                 }
                 *reinterpret_cast<uint2 *>(s_bias + 4 * lane) = bw;
@@ -223,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The residual's first chunk is requested now, into the output chunk
             // itself (no shared memory is left for another), and its second one
             // into L2: both arrive while the accumulator is being computed.
-            const int row0 = t.mb * kTileM + (int)rank * kRowsCta + q * 32;
+            const int row0 = t.band * kRowsCta + q * 32;
             const int out_col = kEpi == kEpiGated ? col_base / 2 : col_base;
             uint8_t *const chunk = smem + kOffOut + (warp - kEpiWarp0) * kOutChunkBytes;
             uint64_t *const res_bar = res_full + (warp - kEpiWarp0);
@@ -347,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kSfWarp0) {
         setmaxnreg_dec<kRegsSf>();
         if (p.wait_all) griddep_wait();
-        const Role role = enter_role(p, tmem_slot);
+        const Role role = enter_role<kGrouped>(p, tmem_slot, tiles_before);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t tmem = role.tmem;
         // ----------------------------------------------- scale staging --
@@ -414,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         setmaxnreg_dec<kRegsCtl>();
         if (p.wait_all) griddep_wait();
-        const Role role = enter_role(p, tmem_slot);
+        const Role role = enter_role<kGrouped>(p, tmem_slot, tiles_before);
         const int lane = role.lane, num_pairs = role.num_pairs, num_tiles = role.num_tiles;
         const uint32_t rank = role.rank, tmem = role.tmem;
         if ((warp == 0 || warp == 3) && lane == 0 && !p.drill) {   // (a timeout drill issues no copies)
@@ -431,9 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             uint32_t issued_mask = 0, issued_phase = 0;
             bool ok = true;
+            GroupWalk walk = {-1, 0, 0, 0, 0};
             for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
-                const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
-                const int band_a = t.mb * 2 + (int)rank;
+                const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
                 for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
                         ok = false;
@@ -441,13 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // (a box past the last row is zero-filled and still counts
                     // its full bytes)
-                    mbar_arrive_expect_tx(&full[stage], act_side ? kABytes : kBBytes);
-                    if (act_side)
-                        tma_load_2d(smem + kOffA + stage * kABytes, &tmA, &full[stage], ks * kBKBytes,
-                                    band_a * kRowsCta, pol);
-                    else
+                    const bool no_rows = kGrouped && act_side && !t.here;    // (the stage keeps stale rows)
+                    mbar_arrive_expect_tx(&full[stage], no_rows ? 0 : act_side ? kABytes : kBBytes);
+                    if (!act_side)
                         tma_load_2d(smem + kOffB + stage * kBBytes, &tmB, &full[stage], ks * kBKBytes,
-                                    t.nb * kTileN + (int)rank * kRowsCta, pol);
+                                    t.w_row + (int)rank * kRowsCta, pol);
+                    else if (!no_rows)
+                        tma_load_2d(smem + kOffA + stage * kABytes, &tmA, &full[stage], ks * kBKBytes,
+                                    t.band * kRowsCta, pol);
                     issued_mask |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -473,10 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             uint32_t issued_mask = 0, issued_phase = 0;
             bool ok = true;
+            GroupWalk walk = {-1, 0, 0, 0, 0};
             for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
-                const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
-                const int band_a = t.mb * 2 + (int)rank;
-                const bool a_here = band_a < (p.m + 127) / 128;
+                const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
+                const bool a_here = t.here;
                 for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&sf_empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
                         ok = false;
@@ -486,9 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&sf_full[stage], (a_here ? sfa_bytes : 0) + 2 * kT * 512);
                     if (a_here)
                         bulk_load(smem + kOffSfa + stage * kSfaBytes,
-                                  p.sfa + band_a * p.sfa_band_bytes + (int64_t)ks * kT * 512, sfa_bytes, &sf_full[stage],
+                                  p.sfa + t.band * p.sfa_band_bytes + (int64_t)ks * kT * 512, sfa_bytes, &sf_full[stage],
                                   pol);
-                    tma_load_2d(smem + kOffSfb + stage * kSfbBytes, &tmSfb, &sf_full[stage], ks * kT * 64, t.nb * 2, pol);
+                    tma_load_2d(smem + kOffSfb + stage * kSfbBytes, &tmSfb, &sf_full[stage], ks * kT * 64, t.w_row / kRowsCta, pol);
                     issued_mask |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -566,8 +651,12 @@ struct PairInstance {
 template <int kEpi, bool kFull>
 constexpr PairInstance instance_of()
 {
-    return {{gemm_nvf4_pair_kernel<false, kEpi, kFull>, gemm_nvf4_pair_kernel<true, kEpi, kFull>}};
+    return {{gemm_nvf4_pair_kernel<false, kEpi, kFull, false>, gemm_nvf4_pair_kernel<true, kEpi, kFull, false>}};
 }
+
+constexpr PairKernel kGroupedInstances[] = {             // [epilogue variant]
+    gemm_nvf4_pair_kernel<false, kEpiPlain, false, true>, gemm_nvf4_pair_kernel<false, kEpiAct, false, true>,
+    gemm_nvf4_pair_kernel<false, kEpiGated, false, true>};
 
 constexpr PairInstance kPairInstances[] = {instance_of<kEpiPlain, false>(), instance_of<kEpiAct, false>(),
                                            instance_of<kEpiGated, false>(), instance_of<kEpiAct, true>(),
@@ -580,6 +669,26 @@ const PairInstance &pair_instance(const GemmParams &p)
 }
 
 }  // namespace
+
+// Which kernel a grouped GEMM runs on.  A group's odd last band costs the pair
+// kernel a tile of two, so it takes groups of 256 rows and more on average (the
+// host knows only the rows of all groups, paddings and slack included), and with
+// an activation K from 2048 on: below, the epilogue outlasts a tile's MMAs, and
+// the one-CTA kernel's wide layout has the faster one.  Measured (pair / one-CTA,
+// us; 32 groups, n = 2048 weight rows each; 128, 256, 384 rows per group):
+//   plain   K = 768   14.4 / 9.9   16.0 / 17.1  21.9 / 21.6
+//           K = 1024               18.2 / 21.6  23.8 / 26.7
+//           K = 7168  63.4 / 54.2  63.3 / 79.2  86.6 / 98.3
+//   SWIGLU  K = 768   17.4 / 11.1  17.6 / 18.1  26.9 / 25.0
+//           K = 1024               20.0 / 21.0  28.7 / 27.0
+//           K = 2048               25.9 / 29.5  35.0 / 36.6
+//   SILU    K = 1024               24.3 / 24.7  34.9 / 31.6
+//           K = 2048               28.3 / 32.0  38.6 / 40.0
+bool grouped_on_pairs(const GemmParams &p)
+{
+    return p.num_groups <= kPairMaxGroups && p.m >= 2 * kRowsCta * p.num_groups &&
+           (epilogue_variant(p) == kEpiPlain || p.num_k64 >= 32);
+}
 
 cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,
                              const char **why, bool dependent)
@@ -594,6 +703,11 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
                 cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
                 if (e != cudaSuccess) return e;
             }
+        for (PairKernel k : kGroupedInstances) {
+            cudaError_t e =
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytesGrouped);
+            if (e != cudaSuccess) return e;
+        }
         cudaLaunchConfig_t probe = {};
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -643,6 +757,11 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         *why = "cuTensorMapEncodeTiled failed for the residual";
         return cudaErrorInvalidValue;
     }
+    const bool grouped = p.group_offsets != nullptr;
+    if (grouped) {                                      // at most: a group's odd band takes a tile
+        const int bands = (p.m + kRowsCta - 1) / kRowsCta;
+        p.num_m_blk = (bands + std::min(p.num_groups, bands)) / 2;
+    }
     const int tiles = p.num_m_blk * p.num_n_blk;
     const int pairs = tiles < max_pairs ? tiles : max_pairs;
     cudaLaunchConfig_t cfg = {};
@@ -655,11 +774,12 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     attrs[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(2 * pairs, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = grouped ? kSmemBytesGrouped : kSmemBytes;
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = dependent ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, pair_instance(p).kernel[p.mx], tmA, tmB, tmSfb, tmOut, tmRes, p);
+    const PairKernel kernel = grouped ? kGroupedInstances[epilogue_variant(p)] : pair_instance(p).kernel[p.mx];
+    return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmSfb, tmOut, tmRes, p);
 }
 
 }  // namespace nvfp4
