@@ -23,11 +23,16 @@ namespace {
 
 using namespace quant_core;
 
-constexpr int kAloneTiles = 2;      // up to here one block sorts alone
+// Up to here one cluster sorts in one launch, a block per tile (2048 assignments
+// over 64 experts: 3.2 us, 5.0 by one block; 8192 over 32: 3.2, in two launches
+// 4.4; 16384 over 64 with two tiles per block, which count before they rank: 6.2
+// and 4.9).
+constexpr int kClusterTiles = 8;
 
 // ------------------------------------------------------------------- sort ----
 // A stable counting sort.  Block b owns a range of whole 1024-assignment tiles.
-// moe_count_kernel: the block's count per expert.  moe_place_kernel: the sum of
+// moe_count_kernel (more than kClusterTiles tiles): the block's count per expert.
+// moe_place_kernel: the sum of
 // the preceding blocks' counts, the group offsets (every block computes them
 // alike from all counts) and, tile by tile, each assignment's rank among the
 // block's earlier ones of its expert: inside a warp by matching lanes, across
@@ -39,6 +44,14 @@ __device__ __forceinline__ int load_id(const void *ids, int64_t i, int n, int ex
     if (i >= n) return -1;
     const Id v = static_cast<const Id *>(ids)[i];
     return v >= 0 && v < (Id)experts ? (int)v : -1;
+}
+
+// Word of a cluster block's shared memory (address from mapa_shared).
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 template <typename Id>
@@ -58,48 +71,83 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_count_kernel(const MoeSortPa
     for (int e = threadIdx.x; e < p.experts; e += kMoeSortTile) p.hist[(int64_t)blockIdx.x * p.experts + e] = s_count[e];
 }
 
-// kAlone: one block sorts everything, and counts for itself (few assignments: one
-// launch instead of two).
-template <typename Id, bool kAlone>
+// kCluster: the blocks of one cluster, a tile each, sort everything in one launch; a
+// block reads the others' counts from their shared memory.
+template <typename Id, bool kCluster>
 __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortParams p, int tiles_per_block)
 {
     extern __shared__ uint16_t s_warp[];                 // [32 warps][experts] counts of a tile
     __shared__ int s_next[kMoeMaxExperts];               // next row of each expert for this block
-    __shared__ int s_total[kMoeMaxExperts];
+    __shared__ int s_total[kMoeMaxExperts];              // (of the block's tile in a cluster)
     __shared__ int s_scan[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int experts = p.experts;
+    auto clear_warps = [&] {
+        for (int j = tid; j < 16 * experts; j += kMoeSortTile) reinterpret_cast<uint32_t *>(s_warp)[j] = 0;
+    };
+    // ranks the tile's ids: the thread's rank among its warp's equal ones, in
+    // s_warp the count in the warps before (cleared at the call), and as result
+    // the tile's count of expert tid
+    int rank = 0;
+    auto rank_tile = [&](int id) {
+        const unsigned peers = __match_any_sync(kFull, id);
+        rank = __popc(peers & ((1u << lane) - 1));
+        if (id >= 0 && rank == 0) s_warp[warp * experts + id] = (uint16_t)__popc(peers);
+        __syncthreads();
+        int run = 0;
+        if (tid < experts) {                             // exclusive prefix over the warps
+#pragma unroll 8
+            for (int w = 0; w < 32; ++w) {
+                const int c = s_warp[w * experts + tid];
+                s_warp[w * experts + tid] = (uint16_t)run;
+                run += c;
+            }
+        }
+        return run;
+    };
     griddep_launch_dependents();
     for (int e = tid; e < experts; e += kMoeSortTile) s_next[e] = s_total[e] = 0;
+    clear_warps();
     const int64_t first = (int64_t)blockIdx.x * tiles_per_block * kMoeSortTile;
     griddep_wait();
-    int id0 = load_id<Id>(p.ids, first + tid, p.n, experts);      // the first tile's, with the counts in flight
+    int id = load_id<Id>(p.ids, first + tid, p.n, experts);       // the first tile's, with the counts in flight
     __syncthreads();
-    if constexpr (kAlone) {
-        if (id0 >= 0) atomicAdd(&s_total[id0], 1);
-        for (int t = 1; t < tiles_per_block; ++t) {
-            const int id = load_id<Id>(p.ids, first + t * kMoeSortTile + tid, p.n, experts);
-            if (id >= 0) atomicAdd(&s_total[id], 1);
+    int total = 0, run = 0;
+    if constexpr (kCluster) {
+        run = rank_tile(id);
+        if (tid < experts) s_total[tid] = run;
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        if (tid < experts) {
+            int before = 0;
+#pragma unroll
+            for (int r = 0; r < kClusterTiles; ++r) {
+                const int c = r < (int)gridDim.x ? ld_dsmem_s32(mapa_shared(&s_total[tid], r)) : 0;
+                before += r < (int)blockIdx.x ? c : 0;
+                total += c;
+            }
+            s_next[tid] = before;
         }
+        cluster_arrive_release();                        // (waited for at the end: the counts outlive their readers)
     } else {
         // column sums of hist: `groups` threads per expert, each a share of the
         // blocks (integer adds: their order does not matter)
         const int width = (experts + 31) / 32 * 32, groups = kMoeSortTile / width;
         const int e = tid % width, g = tid / width;
         if (e < experts && g < groups) {
-            int before = 0, total = 0;
+            int before = 0, sum = 0;
 #pragma unroll 16
             for (int b = g; b < (int)gridDim.x; b += groups) {
                 const int c = p.hist[(int64_t)b * experts + e];
                 before += b < (int)blockIdx.x ? c : 0;
-                total += c;
+                sum += c;
             }
-            if (total) atomicAdd(&s_total[e], total);
+            if (sum) atomicAdd(&s_total[e], sum);
             if (before) atomicAdd(&s_next[e], before);
         }
+        __syncthreads();
+        if (tid < experts) total = s_total[tid];
     }
-    __syncthreads();
-    const int total = tid < experts ? s_total[tid] : 0;
     const int padded = (total + 127) / 128 * 128;
     int incl = padded;
 #pragma unroll
@@ -123,27 +171,19 @@ __global__ void __launch_bounds__(kMoeSortTile) moe_place_kernel(const MoeSortPa
     }
     for (int t = 0; t < tiles_per_block; ++t) {
         const int64_t i = first + t * kMoeSortTile + tid;
-        for (int j = tid; j < 16 * experts; j += kMoeSortTile) reinterpret_cast<uint32_t *>(s_warp)[j] = 0;
-        __syncthreads();
-        const int id = t == 0 ? id0 : load_id<Id>(p.ids, i, p.n, experts);
-        const unsigned peers = __match_any_sync(kFull, id);
-        const int rank = __popc(peers & ((1u << lane) - 1));
-        if (id >= 0 && rank == 0) s_warp[warp * experts + id] = (uint16_t)__popc(peers);
-        __syncthreads();
-        int run = 0;
-        if (tid < experts) {                             // exclusive prefix over the warps
-#pragma unroll 8
-            for (int w = 0; w < 32; ++w) {
-                const int c = s_warp[w * experts + tid];
-                s_warp[w * experts + tid] = (uint16_t)run;
-                run += c;
-            }
+        if (!kCluster) {
+            if (t > 0) id = load_id<Id>(p.ids, i, p.n, experts);
+            run = rank_tile(id);
         }
         __syncthreads();
         if (i < p.n) p.dest[i] = id < 0 ? -1 : s_next[id] + s_warp[warp * experts + id] + rank;
+        if (t + 1 == tiles_per_block) break;
         __syncthreads();
         if (tid < experts) s_next[tid] += run;           // advance the experts past the tile
+        clear_warps();
+        __syncthreads();
     }
+    if constexpr (kCluster) cluster_wait_acquire();
 }
 
 // --------------------------------------------------------------- dispatch ----
@@ -417,42 +457,52 @@ __global__ void __launch_bounds__(256, kK == 8 ? 4 : kK == 4 ? 5 : 8) moe_combin
 // Every kernel here is launched as a programmatic dependent and waits for the
 // kernel before it (griddepcontrol.wait) before it reads or writes memory.
 template <typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args)
+cudaError_t launch_clusters(int cluster, void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                            Args... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <typename Id, bool kAlone>
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args)
+{
+    return launch_clusters(1, kernel, grid, threads, smem, s, args...);
+}
+
+template <typename Id, bool kCluster>
 cudaError_t launch_place(const MoeSortParams &p, int blocks, int per_block, cudaStream_t s)
 {
     static int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel<Id, kAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(moe_place_kernel<Id, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              32 * kMoeMaxExperts * (int)sizeof(uint16_t));
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
-    return launch_dependent(moe_place_kernel<Id, kAlone>, blocks, kMoeSortTile, (size_t)32 * p.experts * sizeof(uint16_t),
-                            s, p, per_block);
+    return launch_clusters(kCluster ? blocks : 1, moe_place_kernel<Id, kCluster>, blocks, kMoeSortTile,
+                           (size_t)32 * p.experts * sizeof(uint16_t), s, p, per_block);
 }
 
 template <typename Id>
 cudaError_t launch_sort(const MoeSortParams &p, int num_sms, cudaStream_t s)
 {
     const int tiles = p.n > 0 ? (p.n + kMoeSortTile - 1) / kMoeSortTile : 1;   // (no tokens: the offsets are still written)
-    if (tiles <= kAloneTiles) return launch_place<Id, true>(p, 1, tiles, s);
+    if (tiles <= kClusterTiles) return launch_place<Id, true>(p, tiles, 1, s);
     const int per_block = (tiles + num_sms - 1) / num_sms;
     const int blocks = (tiles + per_block - 1) / per_block;
     const cudaError_t e = launch_dependent(moe_count_kernel<Id>, blocks, kMoeSortTile, 0, s, p, per_block);
