@@ -53,6 +53,8 @@
  *   - Outputs may not overlap any input (NVFP4_ERR_ALIAS).
  *   - Row strides are in elements; every base pointer and every row must start
  *     on a 16-byte boundary (NVFP4_ERR_ALIGNMENT).
+ *   - bf16 rows are read in whole 16-byte pieces: the up to 14 bytes that follow a
+ *     row's last element inside its last piece may be read and are not used.
  *   - m == 0 (or n == 0 for the weight) is a valid empty call: NVFP4_OK, no launch
  *     (nvfp4_act_global_scale still writes its defined result for m == 0).
  *   - Global scales and alpha are read on the device, so no call waits for the
