@@ -115,7 +115,7 @@ cudaError_t launch_linear_fused(const GemmParams &p, const uint8_t *w, int num_s
 // Clusters of `splits` one-CTA GEMM blocks that can be resident at once (the
 // split-K plan's wave count).
 int gemm_split_clusters(int splits, int num_sms);
-// CTA-pair variant for m > 128 (tiles of 256 x 256 on two SMs), grouped GEMMs that
+// CTA-pair variant for m > 128 (tiles of 256 x 256 or 256 x 128 on two SMs), grouped GEMMs that
 // grouped_on_pairs() names among them.
 constexpr int kPairMaxGroups = 256;
 bool grouped_on_pairs(const GemmParams &p);

@@ -3,7 +3,7 @@
 //
 // Same operation as gemm.cu (page "TorchNvFp4LinearKernel", vLLM PR #53319,
 // section 关键源码片段: _scaled_mm, * alpha, slice, + bias), with each output
-// tile of 256 x 256 computed by a cluster of two CTAs on two SMs.  Per CTA
+// tile of 256 x 256 (256 x 128 where there are few) computed by a cluster of two CTAs on two SMs.  Per CTA
 // r (r = 0, 1; rank 0 leads), sixteen warps in four warpgroups:
 //   warps 0, 3  TMA producers of the operand ring (5 stages of 32 KB): warp 0
 //               this CTA's A rows [128r, 128r + 128) of the tile, warp 3 its
@@ -48,7 +48,7 @@ using namespace gemm_detail;
 
 constexpr int kTileM = 256;                     // per pair (128 rows per CTA)
 constexpr int kWalkGroup = 32;                  // pair tiles per group of the tile walk (8192 rows)
-constexpr int kTileN = 256;
+constexpr int kTileN = 256, kNarrowN = 128;
 constexpr int kRowsCta = 128;
 constexpr int kBKBytes = 128;                   // 256 FP4 elements of K per stage
 constexpr int kEpiColsBias = 128;                     // bias columns per epilogue warp
@@ -157,7 +157,7 @@ __device__ __forceinline__ void count_group_tiles(const GemmParams &p, int32_t *
     if (lane == 31 && p.num_groups == kPairMaxGroups) tiles_before[kPairMaxGroups] = before;
 }
 
-template <bool kGrouped>
+template <bool kGrouped, int kN>
 __device__ __forceinline__ PairTile pair_tile(int tile, const GemmParams &p, uint32_t rank, const int32_t *tiles_before,
                                               GroupWalk &walk)
 {
@@ -171,11 +171,11 @@ __device__ __forceinline__ PairTile pair_tile(int tile, const GemmParams &p, uin
         }
         const int within = tile - walk.before * p.num_n_blk, rows = walk.next - walk.before;
         const int nb = within / rows, band = walk.first + 2 * (within - nb * rows) + (int)rank;
-        return {band, nb, walk.g * p.group_n + nb * kTileN, walk.g, band < walk.end};
+        return {band, nb, walk.g * p.group_n + nb * kN, walk.g, band < walk.end};
     } else {
         const Tile t = tile_coord(tile, p.num_m_blk, p.num_n_blk, kWalkGroup);
         const int band = t.mb * 2 + (int)rank;
-        return {band, t.nb, t.nb * kTileN, 0, band < (p.m + kRowsCta - 1) / kRowsCta};
+        return {band, t.nb, t.nb * kN, 0, band < (p.m + kRowsCta - 1) / kRowsCta};
     }
 }
 
@@ -207,7 +207,9 @@ __device__ __forceinline__ bool wait_residual(const GemmParams &p, uint64_t *bar
 // given) and columns that end inside 16 bytes; its registers and code stay out
 // of the other instances (8192 x 4096 x 28672 without either: 286 us, 310 us
 // with the tail's code alone).  kGrouped: a grouped GEMM (NVFP4, no residual).
-template <bool kMx, int kEpi, bool kFull, bool kGrouped>
+// kN: weight rows of a tile, 256 or, for few tiles, 128: a CTA then holds 64 rows
+// of B, and the epilogue's second four warps have no columns.
+template <bool kMx, int kEpi, bool kFull, bool kGrouped, int kN>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_nvf4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmSfb, const __grid_constant__ CUtensorMap tmOut,
@@ -282,9 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t res_phase = 0;
         GroupWalk walk = {-1, 0, 0, 0, 0};
         for (int tile = role.pair_id; tile < num_tiles; tile += num_pairs) {
-            const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
-            const int n_cols = kGrouped && !t.here ? 0 : min(kEpiCols, p.n_out - t.nb * kTileN - hcol);   // may be <= 0
-            const int col_base = t.nb * kTileN + hcol;
+            const PairTile t = pair_tile<kGrouped, kN>(tile, p, rank, tiles_before, walk);
+            const int n_cols =                                            // may be <= 0
+                (kGrouped && !t.here) || (kN < kTileN && hcol >= kN) ? 0 : min(kEpiCols, p.n_out - t.nb * kN - hcol);
+            const int col_base = t.nb * kN + hcol;
             if constexpr (kGrouped) alpha = p.alpha[t.group];
             // this warp's 128 bias columns into its own buffer (four per lane)
             // while the accumulator is still being computed
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             GroupWalk walk = {-1, 0, 0, 0, 0};
             for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
-                const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
+                const PairTile t = pair_tile<kGrouped, kN>(tile, p, rank, tiles_before, walk);
                 for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
                         ok = false;
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (a box past the last row is zero-filled and still counts
                     // its full bytes)
                     const bool no_rows = kGrouped && act_side && !t.here;    // (the stage keeps stale rows)
-                    mbar_arrive_expect_tx(&full[stage], no_rows ? 0 : act_side ? kABytes : kBBytes);
+                    mbar_arrive_expect_tx(&full[stage], no_rows ? 0 : act_side ? kABytes : (uint32_t)(kN / 2) * kBKBytes);
                     // (activations first: 333 x 4104 x 2072 with bias, GELU and residual takes 16.5 us,
                     // 16.9 with the branches the other way round)
                     if (act_side) {
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         t.band * kRowsCta, pol);
                     } else {
                         tma_load_2d(smem + kOffB + stage * kBBytes, &tmB, &full[stage], ks * kBKBytes,
-                                    t.w_row + (int)rank * kRowsCta, pol);
+                                    t.w_row + (int)rank * (kN / 2), pol);
                     }
                     issued_mask |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -564,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             GroupWalk walk = {-1, 0, 0, 0, 0};
             for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
-                const PairTile t = pair_tile<kGrouped>(tile, p, rank, tiles_before, walk);
+                const PairTile t = pair_tile<kGrouped, kN>(tile, p, rank, tiles_before, walk);
                 const bool a_here = t.here;
                 for (int ks = 0; ks < role.num_ks; ++ks) {
                     if (!mbar_wait(&sf_empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0, acc_phase = 0;
             const uint32_t a_base = smem_u32(smem + kOffA);
             const uint32_t b_base = smem_u32(smem + kOffB);
-            const uint32_t idesc = idesc_nvf4(kTileM, kTileN);
+            const uint32_t idesc = idesc_nvf4(kTileM, kN);
             bool ok = true;
             for (int tile = role.pair_id; tile < num_tiles && ok; tile += num_pairs) {
                 if (!__all_sync(~0u, mbar_wait(tmem_empty, acc_phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)))
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int kk = 0; kk < kcount; ++kk) {
                             const uint64_t ad = adesc + (uint64_t)(kk * 2), bd = bdesc + (uint64_t)(kk * 2);
                             if constexpr (kMx)      // two UE8M0 scales per row and K-step: half a scale word
-                                tc_mma_pair_mxf4(tmem, ad, bd, idesc_mxf4(kTileM, kTileN, (kk & 1) * 2),
+                                tc_mma_pair_mxf4(tmem, ad, bd, idesc_mxf4(kTileM, kN, (kk & 1) * 2),
                                                  sf_col + (kk >> 1) * 4, sf_col + 8 + (kk >> 1) * 8, (ks | kk) != 0);
                             else
                                 tc_mma_pair_nvf4(tmem, ad, bd, idesc, sf_col + kk * 4, sf_col + 16 + kk * 8,
@@ -652,24 +655,27 @@ struct PairInstance {
     PairKernel kernel[2];                                // [MXFP4]
 };
 
-template <int kEpi, bool kFull>
+template <int kEpi, bool kFull, int kN>
 constexpr PairInstance instance_of()
 {
-    return {{gemm_nvf4_pair_kernel<false, kEpi, kFull, false>, gemm_nvf4_pair_kernel<true, kEpi, kFull, false>}};
+    return {{gemm_nvf4_pair_kernel<false, kEpi, kFull, false, kN>, gemm_nvf4_pair_kernel<true, kEpi, kFull, false, kN>}};
 }
 
 constexpr PairKernel kGroupedInstances[] = {             // [epilogue variant]
-    gemm_nvf4_pair_kernel<false, kEpiPlain, false, true>, gemm_nvf4_pair_kernel<false, kEpiAct, false, true>,
-    gemm_nvf4_pair_kernel<false, kEpiGated, false, true>};
+    gemm_nvf4_pair_kernel<false, kEpiPlain, false, true, kTileN>, gemm_nvf4_pair_kernel<false, kEpiAct, false, true, kTileN>,
+    gemm_nvf4_pair_kernel<false, kEpiGated, false, true, kTileN>};
 
-constexpr PairInstance kPairInstances[] = {instance_of<kEpiPlain, false>(), instance_of<kEpiAct, false>(),
-                                           instance_of<kEpiGated, false>(), instance_of<kEpiAct, true>(),
-                                           instance_of<kEpiGated, true>()};
+constexpr PairInstance kPairInstances[2][5] = {          // [narrow][pair_instance()]
+    {instance_of<kEpiPlain, false, kTileN>(), instance_of<kEpiAct, false, kTileN>(), instance_of<kEpiGated, false, kTileN>(),
+     instance_of<kEpiAct, true, kTileN>(), instance_of<kEpiGated, true, kTileN>()},
+    {instance_of<kEpiPlain, false, kNarrowN>(), instance_of<kEpiAct, false, kNarrowN>(),
+     instance_of<kEpiGated, false, kNarrowN>(), instance_of<kEpiAct, true, kNarrowN>(),
+     instance_of<kEpiGated, true, kNarrowN>()}};
 
-const PairInstance &pair_instance(const GemmParams &p)
+int pair_instance(const GemmParams &p)
 {
     const int v = epilogue_variant(p);
-    return kPairInstances[epilogue_full(p) ? v + 2 : v]; // (v is kEpiAct or kEpiGated when full)
+    return epilogue_full(p) ? v + 2 : v;                 // (v is kEpiAct or kEpiGated when full)
 }
 
 }  // namespace
@@ -702,11 +708,12 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured_device != dev) {
-        for (const PairInstance &i : kPairInstances)
-            for (PairKernel k : i.kernel) {
-                cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-                if (e != cudaSuccess) return e;
-            }
+        for (const auto &widths : kPairInstances)
+            for (const PairInstance &i : widths)
+                for (PairKernel k : i.kernel) {
+                    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                    if (e != cudaSuccess) return e;
+                }
         for (PairKernel k : kGroupedInstances) {
             cudaError_t e =
                 cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytesGrouped);
@@ -724,7 +731,7 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         probe.attrs = &attr;
         probe.numAttrs = 1;
         int clusters = 0;
-        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kPairInstances[0].kernel[0], &probe);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kPairInstances[0][0].kernel[0], &probe);
         if (e != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             clusters = num_sms / 2;
@@ -738,10 +745,18 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     }
     GemmParams p = p_in;
     p.num_m_blk = (p.m + kTileM - 1) / kTileM;
+    const bool grouped = p.group_offsets != nullptr;
+    // Tiles of 128 weight rows where all of them run at once: a pair's time is then its
+    // one tile's.  Measured (256 / 128, us): 333 x 4104 x 2072 13.1 / 10.9 (18 and 34
+    // tiles), 512 x 1024 x 2048 7.6 / 6.9, 300 x 14336 x 4096 23.9 / 22.4, 256 x 4096 x
+    // 8192 11.5 / 11.0 (64 tiles); in two waves 333 x 4096 x 6144 11.5 / 15.4 (96 tiles).
+    const int narrow_n_blk = (p.n_out + kNarrowN - 1) / kNarrowN;
+    const bool narrow = !grouped && (int64_t)p.num_m_blk * narrow_n_blk <= max_pairs;
+    if (narrow) p.num_n_blk = narrow_n_blk;
     CUtensorMap tmA, tmB, tmSfb, tmOut;
     const uint64_t row_bytes = (uint64_t)p.kp / 2;
     if (!make_operand_map(&tmA, a, row_bytes, (uint64_t)p.m, kRowsCta) ||
-        !make_operand_map(&tmB, w, row_bytes, (uint64_t)p.n_w, kRowsCta)) {
+        !make_operand_map(&tmB, w, row_bytes, (uint64_t)p.n_w, (narrow ? kNarrowN : kTileN) / 2)) {
         *why = "cuTensorMapEncodeTiled failed for an FP4 operand";
         return cudaErrorInvalidValue;
     }
@@ -761,7 +776,6 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
         *why = "cuTensorMapEncodeTiled failed for the residual";
         return cudaErrorInvalidValue;
     }
-    const bool grouped = p.group_offsets != nullptr;
     if (grouped) {                                      // at most: a group's odd band takes a tile
         const int bands = (p.m + kRowsCta - 1) / kRowsCta;
         p.num_m_blk = (bands + std::min(p.num_groups, bands)) / 2;
@@ -782,7 +796,8 @@ cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uin
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = dependent ? 2 : 1;
-    const PairKernel kernel = grouped ? kGroupedInstances[epilogue_variant(p)] : pair_instance(p).kernel[p.mx];
+    const PairKernel kernel =
+        grouped ? kGroupedInstances[epilogue_variant(p)] : kPairInstances[narrow][pair_instance(p)].kernel[p.mx];
     return cudaLaunchKernelEx(&cfg, kernel, tmA, tmB, tmSfb, tmOut, tmRes, p);
 }
 
