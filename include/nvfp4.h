@@ -299,8 +299,9 @@ nvfp4_status nvfp4_gemm_ex(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t m,
  *   bias_bf16          in   NULL or [num_groups * n] bf16
  *   out_bf16           out  [rows, ldo] bf16; every row of every computed band is
  *                           written (padding rows get unspecified values)
- * Groups of 256 rows and more on average (rows / num_groups) run on the CTA-pair
- * kernel, smaller ones on the one-CTA kernel (with the same bits); no split-K. */
+ * Many tiles of groups of 256 rows and more on average (rows / num_groups) run on
+ * the CTA-pair kernel, others on the one-CTA kernel (with the same bits); no
+ * split-K. */
 nvfp4_status nvfp4_grouped_gemm(const uint8_t *a_fp4, const uint8_t *a_sf, int64_t rows,
                                 const int32_t *group_offsets_dev, int num_groups,
                                 const uint8_t *w_fp4, const uint8_t *w_sf, int64_t n, int64_t k,

@@ -562,8 +562,8 @@ nvfp4_status grouped_gemm_impl(const uint8_t *a_fp4, const uint8_t *a_sf, int64_
     const char *why = nullptr;
     g.wait_all = 1;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    e = nvfp4::grouped_on_pairs(g) ? nvfp4::launch_gemm_pair(g, a_fp4, w_fp4, num_sms, s, &why, true)
-                                   : nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, s, &why, true);
+    e = nvfp4::grouped_on_pairs(g, num_sms) ? nvfp4::launch_gemm_pair(g, a_fp4, w_fp4, num_sms, s, &why, true)
+                                            : nvfp4::launch_gemm(g, a_fp4, w_fp4, num_sms, s, &why, true);
     if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
     return launch_status(e, "grouped GEMM kernel");
 }

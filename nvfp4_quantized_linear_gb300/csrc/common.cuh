@@ -118,7 +118,7 @@ int gemm_split_clusters(int splits, int num_sms);
 // CTA-pair variant for m > 128 (tiles of 256 x 256 or 256 x 128 on two SMs), grouped GEMMs that
 // grouped_on_pairs() names among them.
 constexpr int kPairMaxGroups = 256;
-bool grouped_on_pairs(const GemmParams &p);
+bool grouped_on_pairs(const GemmParams &p, int num_sms);
 cudaError_t launch_gemm_pair(const GemmParams &p, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,
                              const char **why, bool dependent = false);
 

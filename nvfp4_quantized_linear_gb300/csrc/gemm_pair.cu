@@ -684,7 +684,8 @@ int pair_instance(const GemmParams &p)
 // kernel a tile of two, so it takes groups of 256 rows and more on average (the
 // host knows only the rows of all groups, paddings and slack included), and with
 // an activation K from 2048 on: below, the epilogue outlasts a tile's MMAs, and
-// the one-CTA kernel's wide layout has the faster one.  Measured (pair / one-CTA,
+// the one-CTA kernel's wide layout has the faster one.  And it takes no GEMM whose
+// 128 x 256 tiles all run at once on the one-CTA kernel.  Measured (pair / one-CTA,
 // us; 32 groups, n = 2048 weight rows each; 128, 256, 384 rows per group):
 //   plain   K = 768   14.4 / 9.9   16.0 / 17.1  21.9 / 21.6
 //           K = 1024               18.2 / 21.6  23.8 / 26.7
@@ -694,10 +695,12 @@ int pair_instance(const GemmParams &p)
 //           K = 2048               25.9 / 29.5  35.0 / 36.6
 //   SILU    K = 1024               24.3 / 24.7  34.9 / 31.6
 //           K = 2048               28.3 / 32.0  38.6 / 40.0
-bool grouped_on_pairs(const GemmParams &p)
+// With 8 groups: plain K = 768, 256 rows (128 tiles) 8.5 / 7.0; SWIGLU 1536 x 2048, 384 rows
+// (144 tiles) 14.0 / 9.6; 16 groups of 256 rows (192 tiles) 14.6 / 15.1.
+bool grouped_on_pairs(const GemmParams &p, int num_sms)
 {
     return p.num_groups <= kPairMaxGroups && p.m >= 2 * kRowsCta * p.num_groups &&
-           (epilogue_variant(p) == kEpiPlain || p.num_k64 >= 32);
+           (int64_t)p.num_m_blk * p.num_n_blk > num_sms && (epilogue_variant(p) == kEpiPlain || p.num_k64 >= 32);
 }
 
 cudaError_t launch_gemm_pair(const GemmParams &p_in, const uint8_t *a, const uint8_t *w, int num_sms, cudaStream_t s,

@@ -1,5 +1,5 @@
 """GPU tests of the grouped GEMM on CTA pairs (groups of 256 rows and more on
-average): groups whose last pair tile has one band, empty groups, output columns
+average, more tiles of 128 x 256 than SMs): groups whose last pair tile has one band, empty groups, output columns
 that end inside a tile, unused bands before and after the groups, the largest
 number of groups, agreement with the one-CTA kernel, and offsets that a kernel
 before it on the stream has just written.
@@ -30,6 +30,11 @@ def assert_close(got, ref, what):
     assert np.isfinite(got).all(), what
     err = np.abs(got - ref) - 1.01 * 2.0 ** -8 * np.abs(ref)
     assert err.max() <= 1e-3 * np.sqrt((ref * ref).mean()), f"{what}: {err.max():.3e}"
+
+
+def on_pairs(rows, groups, nw):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return rows >= 256 * groups and (rows + 127) // 128 * ((nw + 255) // 256) > sms
 
 
 class Groups:
@@ -83,20 +88,22 @@ class Groups:
                                    ("geglu", 4104)])
 def test_ragged_groups(act, k):
     """Odd and even numbers of bands, empty groups first, last and between, one
-    row, columns of 384 weight rows (half of the second tile)."""
-    c = Groups([0, 300, 257, 0, 1000, 1, 384, 513, 0], 384, k, seed=5)
+    row, columns of 2176 weight rows (half of the last tile)."""
+    c = Groups([0, 300, 257, 0, 1000, 1, 384, 513, 0], 2176, k, seed=5)
     rows = c.rows + 128
-    assert rows >= 256 * c.count                     # the pair kernel's side of the choice
+    assert on_pairs(rows, c.count, c.nw)
     c.check(c.run(act, rows), act)
 
 
 def test_unused_bands_before_the_groups():
-    c = Groups([200, 640], 256, 512, seed=6, lead=3)
+    c = Groups([200, 640], 3328, 512, seed=6, lead=3)
+    assert on_pairs(c.rows + 256, c.count, c.nw)
     c.check(c.run("none", c.rows + 256), "none")
 
 
 def test_no_rows_at_all():
-    c = Groups([0, 0], 128, 64, seed=7)
+    c = Groups([0, 0], 9984, 64, seed=7)
+    assert on_pairs(512, c.count, c.nw)
     out = c.run("none", 256 * 2)
     assert (out == -5.0).all()
 
@@ -107,6 +114,7 @@ def test_many_groups(count):
     rng = np.random.default_rng(count)
     c = Groups([int(v) for v in rng.integers(0, 3, count) * 256 + rng.integers(0, 129, count)], 128, 64, seed=8)
     rows = max(c.rows, 256 * count)
+    assert on_pairs(rows, count, c.nw)               # (by size; 257 groups are too many)
     c.check(c.run("none", rows), "none", groups=[0, 1, 7, 8, 31, 32, 100, 127, 128, 200, 247, 248, 253, count - 1])
 
 
@@ -114,8 +122,8 @@ def test_many_groups(count):
 def test_same_as_the_one_cta_kernel(act):
     """The rows that the call is told of decide between the kernels: the same
     groups with and without a long unused end have the same bits."""
-    c = Groups([300, 1, 100, 384, 128], 384, 2048, seed=9)
-    assert c.rows < 256 * c.count <= c.rows + 256
+    c = Groups([300, 1, 100, 384, 128], 3456, 2048, seed=9)
+    assert on_pairs(c.rows + 256, c.count, c.nw) and not on_pairs(c.rows, c.count, c.nw)
     a, b = c.run(act, c.rows), c.run(act, c.rows + 256)
     for g, m in enumerate(c.group_m):
         r = slice(int(c.offsets[g]), int(c.offsets[g]) + m)
@@ -125,13 +133,13 @@ def test_same_as_the_one_cta_kernel(act):
 def test_offsets_from_the_kernel_before():
     """Sort, dispatch and GEMM in turn on the same buffers without a
     synchronisation, another routing each time."""
-    tokens, topk, experts, h, n = 1500, 2, 8, 512, 256
+    tokens, topk, experts, h, n = 1500, 2, 8, 512, 1280
     g = torch.Generator(device="cuda").manual_seed(10)
     x = torch.randn(tokens, h, device="cuda", generator=g).bfloat16()
     wq = nv.prepare_weight((torch.randn(experts * n, h, device="cuda", generator=g) * 0.05).bfloat16(), dev_scalar(40.0))
     al = torch.full((experts,), 1e-4, device="cuda")
     rows = nv.nvfp4_moe_rows(tokens, topk, experts)
-    assert rows >= 256 * experts
+    assert on_pairs(rows, experts, n)
     kp = nv.padded_k(h)
     q = torch.zeros(rows, kp // 2, dtype=torch.uint8, device="cuda")
     sf = torch.zeros(nv.nvfp4_scale_bytes(rows, h), dtype=torch.uint8, device="cuda")
