@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
         const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
-        int it = 0;
+        int it = -1;                                            // tiles of this CTA so far, the skipped ones not counted:
+                                                                // only the others move the bias buffers' barriers on
         int q_stage = 0;                                        // fused linear: the quantized stages
         uint32_t q_phase = 0;
         float q_gs = 0.0f;
@@ -477,9 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             griddep_wait();                                     // x and gs may be the preceding kernel's output
             if constexpr (!kMx) q_gs = __ldg(p.quant.gs);       // (MXFP4 has no global scale)
         }
-        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+        for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
             const Work wk = work_of(tile, p, num_ks);
             if (wk.g < 0) continue;                             // every role skips the same tiles
+            ++it;
             // (a timeout drill quantizes nothing: its stages never fill)
             if (kFused && !p.drill &&
                 !fused_quant_stages<kMx>(p, smem, full, x_full, wk, q_stage, q_phase, q_gs, warp - kEpiWarp0, lane))
@@ -914,10 +916,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // that writes the bias has finished: wait for it first.
             griddep_wait();
             uint16_t *s_bias_all = reinterpret_cast<uint16_t *>(smem + kOffBias);
-            int it = 0;
-            for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++it) {
+            int it = -1;                                        // as the epilogue counts them
+            for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
                 const Work wk = work_of(tile, p, num_ks);
                 if (wk.g < 0) continue;
+                ++it;
                 const Tile t = wk.t;
                 const int n_rows = min(kBN, p.n_out - t.nb * kBN);
                 const int b = it & 1;
