@@ -126,15 +126,17 @@ struct Work {
 };
 
 // Group of the 128-row band mb: the last g with offsets[g] <= 128 mb, or -1
-// for a band outside [offsets[0], offsets[num_groups]).
+// for a band outside [offsets[0], offsets[num_groups]).  (Offsets, alpha, bias and
+// residual may be the output of the kernel that this one overlaps: coherent loads,
+// after the wait for it.)
 __device__ __forceinline__ int group_of_band(const GemmParams &p, int mb)
 {
     const int row = mb * 128;
-    if (row < __ldg(p.group_offsets) || row >= __ldg(p.group_offsets + p.num_groups)) return -1;
+    if (row < p.group_offsets[0] || row >= p.group_offsets[p.num_groups]) return -1;
     int lo = 0, hi = p.num_groups - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(p.group_offsets + mid) <= row) lo = mid;
+        if (p.group_offsets[mid] <= row) lo = mid;
         else hi = mid - 1;
     }
     return lo;
@@ -168,7 +170,7 @@ __device__ __forceinline__ void load_residual_row(const GemmParams &p, uint4 (&r
     const int cols = p.residual != nullptr && row < p.m ? p.out_cols - col : 0;
     const uint16_t *src = p.residual + row * p.ldr + col;
 #pragma unroll
-    for (int g = 0; g < kG; ++g) res[g] = 8 * g < cols ? ld_stream_v4(src + 8 * g) : make_uint4(0, 0, 0, 0);
+    for (int g = 0; g < kG; ++g) res[g] = 8 * g < cols ? ld_global_v4(src + 8 * g) : make_uint4(0, 0, 0, 0);
 }
 
 // Up to this many rows below m in an epilogue warp's 32, the rows are written
@@ -205,7 +207,7 @@ template <int kEpi>
 __device__ __forceinline__ void cluster_reduce(const GemmParams &p, const Tile &t, uint32_t part_smem, uint32_t rank,
                                                int tid)
 {
-    const float alpha = p.alpha != nullptr ? __ldg(p.alpha) : 1.0f;
+    const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
     const ActParams actp = act_params(p.act);
     const int rows = min(kBM, p.m - t.mb * kBM);
     const int cols = min(kBN, p.n_out - t.nb * kBN);
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float q_gs = 0.0f;
         if constexpr (kFused) {
             griddep_wait();                                     // x and gs may be the preceding kernel's output
-            if constexpr (!kMx) q_gs = __ldg(p.quant.gs);       // (MXFP4 has no global scale)
+            if constexpr (!kMx) q_gs = *p.quant.gs;             // (MXFP4 has no global scale)
         }
         for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x) {
             const Work wk = work_of(tile, p, num_ks);
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kFused && !p.drill &&
                 !fused_quant_stages<kMx>(p, smem, full, x_full, wk, q_stage, q_phase, q_gs, warp - kEpiWarp0, lane))
                 break;
-            const float alpha = p.alpha != nullptr ? __ldg(p.alpha + wk.g) : 1.0f;
+            const float alpha = p.alpha != nullptr ? p.alpha[wk.g] : 1.0f;
             const Tile t = wk.t;
             const int n_cols = min(kEpiCols, p.n_out - t.nb * kBN - hcol);   // may be <= 0
             const int col_base = t.nb * kBN + hcol;

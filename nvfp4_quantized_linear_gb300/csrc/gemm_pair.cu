@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t leader_tmem_empty = mapa_shared(tmem_empty, 0);
         const bool use_bias = p.bias != nullptr;
         const bool bias_vec = (reinterpret_cast<uintptr_t>(p.bias) & 7) == 0;   // 8-byte loads of 4 columns
-        float alpha = p.alpha != nullptr && !kGrouped ? __ldg(p.alpha) : 1.0f;
+        float alpha = p.alpha != nullptr && !kGrouped ? *p.alpha : 1.0f;
         const uint64_t out_policy = l2_policy_evict_first();   // the output is written once
         const ActParams actp = act_params(p.act);
         uint32_t acc_phase = 0;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint2 bw = make_uint2(0u, 0u);
                 const uint16_t *const bias = kGrouped ? p.bias + (int64_t)t.group * p.group_n : p.bias;
                 if (bias_vec && c0 + 4 <= p.n_out) {
-                    bw = __ldg(reinterpret_cast<const uint2 *>(bias + c0));
+                    bw = *reinterpret_cast<const uint2 *>(bias + c0);
                 } else {
                     uint16_t e[4];
 #pragma unroll
