@@ -27,11 +27,14 @@ constexpr int kEpiPlain = 0, kEpiAct = 1, kEpiGated = 2;
 // SILU is v * sigmoid(v) and GELU, 0.5 v (1 + tanh u) with u = sqrt(2/pi) (v +
 // 0.044715 v^3), is v * sigmoid(2u), which has no cancellation where tanh u is
 // near -1.  Both are v / (1 + 2^(v (c1 + c3 v^2))) with coefficients that hold
-// -log2(e): one code path with coefficients as data.  RELU and NONE are
-// max(v, floor) with floor 0 or -inf.  The epilogue's unrolled code runs once
-// per tile, so its size counts as much as its instructions: a switch over the
-// four functions in every group of eight columns cost 10 us in a launch of one
-// tile per CTA (instruction fetches), this form 2 to 4.
+// -log2(e): one code path with coefficients as data.  SILU's c3 would be 0, which
+// makes NaN of an infinite v^2 (|v| > 1.8e19); it is -2^-100, which c1 swallows whole
+// below |v| = 2^37 and which has c1's sign above, where 2^x is 0 or infinite anyway.
+// (A minimum that keeps v^2 finite instead: 1 to 2 % of a prompt's SWIGLU GEMM.)
+// RELU and NONE are max(v, floor) with floor 0 or -inf.  The epilogue's unrolled
+// code runs once per tile, so its size counts as much as its instructions: a switch
+// over the four functions in every group of eight columns cost 10 us in a launch of
+// one tile per CTA (instruction fetches), this form 2 to 4.
 struct ActParams {
     float c1, c3;       // SILU, GELU and the gates
     float floor;        // RELU, NONE
@@ -44,7 +47,7 @@ __device__ __forceinline__ ActParams act_params(int32_t act)
     const bool gelu = act == kActGelu || act == kActGeglu;
     ActParams a;
     a.c1 = gelu ? -2.0f * 0.7978845608f * kLog2e : -kLog2e;
-    a.c3 = gelu ? -2.0f * 0.7978845608f * 0.044715f * kLog2e : 0.0f;
+    a.c3 = gelu ? -2.0f * 0.7978845608f * 0.044715f * kLog2e : -0x1p-100f;
     a.floor = act == kActRelu ? 0.0f : __int_as_float(0xff800000);
     a.sigmoid = act != kActRelu && act != kActNone;
     return a;
@@ -95,7 +98,8 @@ __device__ __forceinline__ uint64_t bf16x2_to_f32x2(uint32_t w)
 // the special-function unit.  ex2.approx and rcp.approx are good to 2^-22, the
 // products to 2^-24 of an exponent below 40 where the result matters: the
 // value's error is under 2^-17, against the 2^-9 of its rounding to bf16.
-// 2^x = inf gives 0.
+// 2^x = inf gives 0, as does 2^x > 2^126, whose reciprocal is flushed: the value
+// itself is under 2^-119 there.
 __device__ __forceinline__ uint64_t times_sigmoid2(uint64_t v, const ActParams &a)
 {
     float x0, x1, e0, e1, r0, r1;
