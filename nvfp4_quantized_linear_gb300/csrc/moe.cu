@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(128, kK == 1 ? 6 : 8) moe_combine_kernel(const
                     if (p.residual != nullptr) add_residual8(acc[i], res[i]);
                     store8<kWhole>(p.out + (int64_t)(t0 + i) * p.ldo, c, p.h, bf16x8_of(acc[i]));
                 }
+        if (p.tokens - t0 <= step) break;                    // (t0 + step may pass 2^31: up to 2^31 tokens of topk 1)
         mine = next_mine;
         my_w = next_w;
     }

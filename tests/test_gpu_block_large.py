@@ -100,3 +100,38 @@ def test_graph_capture_of_both_ffn_blocks():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, dense(x, r)) and torch.equal(b, moe(x))
+
+
+@pytest.fixture
+def room():
+    """room(gb): skips without that much free memory; what a test cached is given back."""
+    def need(gb):
+        torch.cuda.empty_cache()
+        if torch.cuda.mem_get_info()[0] < gb << 30:
+            pytest.skip(f"needs {gb} GB of device memory")
+    yield need
+    torch.cuda.empty_cache()
+
+
+def test_combine_of_more_than_2_30_tokens(room):
+    """topk 1 takes a step of all blocks for (almost) all tokens: the token number plus
+    the step passes 2^31.  The expert rows repeat, so the output does."""
+    tokens, h, rows = (1 << 30) + 4096 * 3 + 77, 8, 4096
+    room(40)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    y = torch.randn(rows, h, generator=g, device="cuda").bfloat16()
+    whole = tokens // rows
+    dest = torch.empty(tokens, 1, dtype=torch.int32, device="cuda")
+    order = torch.randperm(rows, generator=g, device="cuda").int()
+    order[5] = -1                                            # a dropped assignment: zeros
+    dest[:whole * rows].view(whole, rows).copy_(order.expand(whole, rows))
+    dest[whole * rows:, 0] = order[:tokens - whole * rows]
+    out = torch.full((tokens + 8, h), -3.0, dtype=torch.bfloat16, device="cuda")
+    nv.moe_combine(y, dest, out=out[:tokens])
+    want = y[order.clamp_min(0).long()]
+    want[5] = 0
+    assert (out[tokens:] == -3.0).all()
+    assert torch.equal(out[whole * rows:tokens], want[:tokens - whole * rows])
+    full = out[:whole * rows].view(whole, rows * h)
+    for i in range(0, whole, 1 << 16):
+        assert (full[i:i + (1 << 16)].view(torch.int16) == want.view(1, -1).view(torch.int16)).all(), i
