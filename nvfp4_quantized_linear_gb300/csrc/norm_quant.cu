@@ -268,15 +268,16 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
     }
     __syncthreads();
     const uint64_t pol = l2_policy_evict_first();
-    auto request = [&](int row, int s) {                  // thread 0
+    auto request = [&](uint32_t row, int s) {             // thread 0
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         bulk_load(ring + s * stage_bytes, p.x + (int64_t)row * p.ldx, row_bytes, &full[s], pol);
         if (use_res)
             bulk_load(ring + s * stage_bytes + row_bytes, p.residual + (int64_t)row * p.ldr, row_bytes, &full[s], pol);
     };
-    const int step = gridDim.x;
+    // (row numbers with the steps past the last one go beyond 2^31: unsigned)
+    const uint32_t step = gridDim.x, m = (uint32_t)p.m;
     if (tid == 0)
-        for (int s = 0; s < stages && (int)blockIdx.x + s * step < p.m; ++s) request(blockIdx.x + s * step, s);
+        for (int s = 0; s < stages && blockIdx.x + s * step < m; ++s) request(blockIdx.x + s * step, s);
     Raw16 gamma[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -284,15 +285,15 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
         gamma[u] = load16_coherent(p.gamma, k0, p.k);
     }
     const float gs = kFmt == kFmtNvfp4 ? *p.gs : 1.0f;
-    for (int row = p.m + blockIdx.x; row < p.mp; row += step) zero_scale_row(p, row);
+    for (uint32_t row = m + blockIdx.x; row < (uint32_t)p.mp; row += step) zero_scale_row(p, (int)row);
     int s = 0;
     uint32_t phase = 0;
     int it = 0;
-    for (int row = blockIdx.x; row < p.m; row += step, ++it) {
+    for (uint32_t row = blockIdx.x; row < m; row += step, ++it) {
         if (!mbar_wait(&full[s], phase, p.err_flag, kErrTimeout, kDefaultWaitNs)) {
             // expired: give the copies in flight (this row's and the next ones')
             // as long once more, then end the block
-            for (int i = 0; i < stages && row + i * step < p.m; ++i)
+            for (int i = 0; i < stages && row + i * step < m; ++i)
                 mbar_wait(&full[(s + i) % stages], phase ^ (s + i >= stages ? 1u : 0u), p.err_flag, kErrTimeout,
                           kDefaultWaitNs);
             return;
@@ -309,10 +310,10 @@ __global__ void __launch_bounds__(512, U == 1 ? 2 : 1) norm_quant_ring_kernel(co
         }
         // after the sum's barrier every thread has read the stage: refill it
         const float rstd = rstd_of(block_sum<16>(sum, s_part[it & 1]), p);
-        if (tid == 0 && row + stages * step < p.m) request(row + stages * step, s);
+        if (tid == 0 && row + stages * step < m) request(row + stages * step, s);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            finish16<kFmt>(p, row, (u * blockDim.x + tid) * 16, h[u], rstd, gamma[u], gs);
+            finish16<kFmt>(p, (int)row, (u * blockDim.x + tid) * 16, h[u], rstd, gamma[u], gs);
         }
         if (++s == stages) { s = 0; phase ^= 1; }
     }

@@ -135,3 +135,24 @@ def test_combine_of_more_than_2_30_tokens(room):
     full = out[:whole * rows].view(whole, rows * h)
     for i in range(0, whole, 1 << 16):
         assert (full[i:i + (1 << 16)].view(torch.int16) == want.view(1, -1).view(torch.int16)).all(), i
+
+
+def test_norm_of_almost_2_31_rows(room):
+    """The last rows of the largest row count: the blocks' next row numbers pass 2^31.
+    The rows repeat every 1024, so codes and scales do."""
+    m, k, period = (1 << 31) - 1024, 8, 1024
+    room(100)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rows = (torch.randn(period, k, generator=g, device="cuda") * 3).bfloat16()
+    gamma, gs = torch.ones(k, dtype=torch.bfloat16, device="cuda"), dev_scalar(40.0)
+    x = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
+    x.view(m // period, period * k).copy_(rows.view(1, -1).expand(m // period, -1))
+    want_q, want_sf, _ = nv.add_rmsnorm_quant(rows, gamma, 1e-6, gs=gs)
+    q, sf, _ = nv.add_rmsnorm_quant(x, gamma, 1e-6, gs=gs)
+    torch.cuda.synchronize()
+    nv.nvfp4_device_error()
+    step = 1 << 15
+    for got, want in ((q, want_q), (sf, want_sf)):
+        got, want = got.view(m // period, -1), want.view(1, -1)
+        for i in range(0, m // period, step):
+            assert (got[i:i + step] == want).all(), i
