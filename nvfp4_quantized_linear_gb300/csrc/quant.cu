@@ -148,16 +148,16 @@ template <int U>
 __global__ void __launch_bounds__(256) quant_mx_kernel(const QuantParams p)
 {
     const int lane = threadIdx.x & 31;
-    const int warp = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-    const int nwarps = (int)((gridDim.x * blockDim.x) >> 5);
+    const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const uint32_t nwarps = (gridDim.x * blockDim.x) >> 5;
     if (threadIdx.x == 0) griddep_launch_dependents();
     const int segs = (p.kp + 511) >> 9;
-    const int tasks = p.mp * segs;                    // < 2^31: checked on the host
+    const uint32_t tasks = (uint32_t)p.mp * segs;     // < 2^31: checked on the host; with a step more below 2^32
     const int64_t out_ld = p.kp >> 1;
 
-    for (int base = warp * U; base < tasks; base += nwarps * U) {
-        int r0 = base / segs;
-        int s0 = base - r0 * segs;
+    for (uint32_t base = warp * U; base < tasks; base += nwarps * U) {
+        int r0 = (int)(base / segs);
+        int s0 = (int)(base - (uint32_t)r0 * segs);
         Raw16 raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -207,19 +207,18 @@ template <int U>
 __global__ void __launch_bounds__(256) act_amax_kernel(const QuantParams p, unsigned int *amax_out)
 {
     const int lane = threadIdx.x & 31;
-    const int warp = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-    const int nwarps = (int)((gridDim.x * blockDim.x) >> 5);
+    const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const uint32_t nwarps = (gridDim.x * blockDim.x) >> 5;
     const int segs = (p.k + 511) >> 9;
-    const int tasks = p.m * segs;                     // < 2^31: checked on the host
+    const uint32_t tasks = (uint32_t)p.m * segs;      // as in quant_mx_kernel
     uint32_t mx = 0;                                  // two 16-bit maxima
-    for (int base = warp * U; base < tasks; base += nwarps * U) {
+    for (uint32_t base = warp * U; base < tasks; base += nwarps * U) {
         Raw16 raw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = base + u;
-            const int r = t / segs;
+            const uint32_t t = base + u, r = t / segs;
             const bool ok = t < tasks;
-            raw[u] = load16(ok ? p.x + (int64_t)r * p.ldx : p.x, (t - r * segs) * 512 + lane * 16, p.k, ok);
+            raw[u] = load16(ok ? p.x + (int64_t)r * p.ldx : p.x, (int)(t - r * segs) * 512 + lane * 16, p.k, ok);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {

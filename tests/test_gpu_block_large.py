@@ -137,22 +137,46 @@ def test_combine_of_more_than_2_30_tokens(room):
         assert (full[i:i + (1 << 16)].view(torch.int16) == want.view(1, -1).view(torch.int16)).all(), i
 
 
-def test_norm_of_almost_2_31_rows(room):
-    """The last rows of the largest row count: the blocks' next row numbers pass 2^31.
-    The rows repeat every 1024, so codes and scales do."""
+class AlmostTwoToThe31Rows:
+    """The largest row count; the rows repeat every 1024, so what is computed row by row does."""
     m, k, period = (1 << 31) - 1024, 8, 1024
+
+    def __init__(self):
+        g = torch.Generator(device="cuda").manual_seed(12)
+        self.rows = (torch.randn(self.period, self.k, generator=g, device="cuda") * 3).bfloat16()
+        self.x = torch.empty(self.m, self.k, dtype=torch.bfloat16, device="cuda")
+        self.x.view(self.m // self.period, -1).copy_(self.rows.view(1, -1).expand(self.m // self.period, -1))
+
+    def check(self, *outputs):
+        """(output of x, output of rows) pairs"""
+        torch.cuda.synchronize()
+        nv.nvfp4_device_error()
+        for got, want in outputs:
+            got, want = got.view(self.m // self.period, -1), want.view(1, -1)
+            for i in range(0, got.shape[0], 1 << 15):
+                assert (got[i:i + (1 << 15)] == want).all(), i
+
+
+def test_norm_of_almost_2_31_rows(room):
+    """The blocks' next row numbers pass 2^31."""
     room(100)
-    g = torch.Generator(device="cuda").manual_seed(12)
-    rows = (torch.randn(period, k, generator=g, device="cuda") * 3).bfloat16()
-    gamma, gs = torch.ones(k, dtype=torch.bfloat16, device="cuda"), dev_scalar(40.0)
-    x = torch.empty(m, k, dtype=torch.bfloat16, device="cuda")
-    x.view(m // period, period * k).copy_(rows.view(1, -1).expand(m // period, -1))
-    want_q, want_sf, _ = nv.add_rmsnorm_quant(rows, gamma, 1e-6, gs=gs)
-    q, sf, _ = nv.add_rmsnorm_quant(x, gamma, 1e-6, gs=gs)
-    torch.cuda.synchronize()
-    nv.nvfp4_device_error()
-    step = 1 << 15
-    for got, want in ((q, want_q), (sf, want_sf)):
-        got, want = got.view(m // period, -1), want.view(1, -1)
-        for i in range(0, m // period, step):
-            assert (got[i:i + step] == want).all(), i
+    c = AlmostTwoToThe31Rows()
+    gamma, gs = torch.ones(c.k, dtype=torch.bfloat16, device="cuda"), dev_scalar(40.0)
+    q, sf, _ = nv.add_rmsnorm_quant(c.x, gamma, 1e-6, gs=gs)
+    want_q, want_sf, _ = nv.add_rmsnorm_quant(c.rows, gamma, 1e-6, gs=gs)
+    c.check((q, want_q), (sf, want_sf))
+
+
+def test_quantizers_of_almost_2_31_rows(room):
+    """The warps' next task numbers pass 2^31 (MXFP4, the global scale's maximum)."""
+    room(100)
+    c = AlmostTwoToThe31Rows()
+    c.x[-1, -1] = 100.0                                      # (the maximum is in the last task)
+    assert float(nv.act_global_scale(c.x)[0]) == float(torch.tensor(2688.0 / 100.0))
+    c.x[-1, -1] = c.rows[-1, -1]
+    q, sf = nv.quant_act_mx(c.x)
+    c.check(*zip((q, sf), nv.quant_act_mx(c.rows)))
+    del q, sf
+    gs = dev_scalar(40.0)
+    q, sf = nv.quant_act(c.x, gs)
+    c.check(*zip((q, sf), nv.quant_act(c.rows, gs)))
