@@ -168,6 +168,78 @@ def _ld(t, name):
     return t.stride(0)
 
 
+# What the tensor-level helpers check before they hand a pointer on: the library sees
+# addresses only, and would read a tensor of another type or shape past its end.  (A raw
+# address in place of a vector or scalar goes through unchecked.)
+
+def _require_dtype(t, name, dtype):
+    """`dtype`, by name; raw 16-bit storage passes for bfloat16."""
+    got = str(t.dtype)[len("torch."):]
+    if got != dtype and not (dtype == "bfloat16" and got in ("int16", "uint16")):
+        raise ValueError(f"{name} must be {dtype}, got {got}")
+
+
+def _rows_of(t, name, rows, cols):
+    """Row stride of a 2-D bf16 tensor that holds rows x cols elements."""
+    ld = _ld(t, name)
+    _require_dtype(t, name, "bfloat16")
+    if t.shape[0] < rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must hold {rows} x {cols} elements, got {tuple(t.shape)}")
+    return ld
+
+
+def _flat(t, name, dtype, count):
+    """A contiguous tensor of at least `count` elements."""
+    if t is None or isinstance(t, int):
+        return
+    _require_dtype(t, name, dtype)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < count:
+        raise ValueError(f"{name} must have {count} elements, got {tuple(t.shape)}")
+
+
+def _routing(dest, group_offsets=None, group_counts=None, weights=None):
+    """(tokens, topk) of moe_sort's outputs and the weights that go with them."""
+    if dest.dim() != 2:
+        raise ValueError(f"dest must be [tokens, topk], got {tuple(dest.shape)}")
+    _flat(dest, "dest", "int32", 0)
+    if group_counts is not None:
+        _flat(group_counts, "group_counts", "int32", 1)
+        _flat(group_offsets, "group_offsets", "int32", group_counts.numel() + 1)
+    if weights is not None:
+        _flat(weights, "weights", "float32", 0)
+        if weights.shape != dest.shape and (weights.dim() != 1 or weights.numel() != dest.numel()):
+            raise ValueError(f"weights must be {tuple(dest.shape)} like dest, got {tuple(weights.shape)}")
+    return dest.shape
+
+
+def _on_gpu(**tensors):
+    device = None
+    for name, t in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise ValueError(f"{name} is on another device than the tensors before it")
+
+
+def _check_linear(x, k, n_out, bias, act, residual, out, **operands):
+    """The checks of linear() and mxfp4_linear(); returns (ldx, activation code, ldr, ldo)."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}, not one of {', '.join(ACTIVATIONS)}")
+    m = x.shape[0]
+    ldx = _rows_of(x, "x", m, k)
+    _flat(bias, "bias", "bfloat16", 2 * n_out if act in GATED_ACTIVATIONS else n_out)
+    ldr = _rows_of(residual, "residual", m, n_out) if residual is not None else 0
+    ldo = _rows_of(out, "out", m, n_out) if out is not None else n_out
+    _on_gpu(x=x, **operands, bias=bias, residual=residual, out=out)
+    return ldx, ACTIVATIONS[act], ldr, ldo
+
+
 # ------------------------------------------------------------- queries ----
 
 def padded_k(k: int) -> int:
@@ -424,17 +496,16 @@ def mxfp4_linear(x, w_fp4, w_sf, k: int, n_out: int, bias=None, out=None, worksp
     import torch
     m = x.shape[0]
     n_w = w_fp4.shape[0]
+    ldx, code, ldr, ldo = _check_linear(x, k, n_out, bias, act, residual, out, w_fp4=w_fp4, w_sf=w_sf)
     if out is None:
         out = torch.empty((m, n_out), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = torch.empty(max(nvfp4_mxfp4_linear_workspace_bytes(m, k, n_w), 1), dtype=torch.uint8,
                                 device=x.device)
     if act == "none" and residual is None:
-        nvfp4_mxfp4_linear(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, out, _ld(out, "out"), workspace,
-                           workspace.numel(), stream)
+        nvfp4_mxfp4_linear(x, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias, out, ldo, workspace, workspace.numel(), stream)
         return out
-    nvfp4_mxfp4_linear_act(x, m, k, _ld(x, "x"), w_fp4, w_sf, n_w, n_out, bias, ACTIVATIONS[act], residual,
-                           _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,
+    nvfp4_mxfp4_linear_act(x, m, k, ldx, w_fp4, w_sf, n_w, n_out, bias, code, residual, ldr, out, ldo, workspace,
                            workspace.numel(), stream)
     return out
 
@@ -457,19 +528,21 @@ def linear(x, w_fp4, w_sf, k: int, n_out: int, gs, alpha, bias=None, transform=N
     import torch
     m = x.shape[0]
     n_w = w_fp4.shape[0]
+    _flat(gs, "gs", "float32", 1)
+    _flat(alpha, "alpha", "float32", 1)
+    ldx, code, ldr, ldo = _check_linear(x, k, n_out, bias, act, residual, out, w_fp4=w_fp4, w_sf=w_sf, gs=gs,
+                                        alpha=alpha, transform=transform)
     if out is None:
         out = torch.empty((m, n_out), dtype=torch.bfloat16, device=x.device)
     need = nvfp4_linear_workspace_bytes(m, k, n_w)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     if act == "none" and residual is None:
-        nvfp4_linear(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
-                     alpha, bias, out, _ld(out, "out"), workspace, workspace.numel(), stream)
+        nvfp4_linear(x, m, k, ldx, gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out, alpha,
+                     bias, out, ldo, workspace, workspace.numel(), stream)
         return out
-    nvfp4_linear_act(x, m, k, _ld(x, "x"), gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out,
-                     alpha, bias, ACTIVATIONS[act], residual,
-                     _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), workspace,
-                     workspace.numel(), stream)
+    nvfp4_linear_act(x, m, k, ldx, gs, transform, bs if transform is not None else 0, w_fp4, w_sf, n_w, n_out, alpha,
+                     bias, code, residual, ldr, out, ldo, workspace, workspace.numel(), stream)
     return out
 
 
@@ -486,15 +559,22 @@ def add_rmsnorm_quant(x, gamma, eps: float, residual=None, gs=None, fmt: int = N
     returns (x_q, flat x_sf, h).  h (the updated residual stream, None without a
     residual) is allocated unless given; pass residual itself to update it in place."""
     import torch
+    ldx = _rows_of(x, "x", 0, 0)
     m, k = x.shape
+    ldr = _rows_of(residual, "residual", m, k) if residual is not None else 0
+    if h is not None:
+        _rows_of(h, "h", m, k)
+    _flat(gamma, "gamma", "bfloat16", k)
+    _flat(gs, "gs", "float32", 1)
+    _on_gpu(x=x, gamma=gamma, residual=residual, gs=gs, h=h)
     cols = padded_k(k) if fmt == NVFP4_FORMAT_MXFP8 else padded_k(k) // 2
     n_sf = nvfp4_scale_bytes(m, k) if fmt == NVFP4_FORMAT_NVFP4 else nvfp4_mxfp4_scale_bytes(m, k)
     x_q = torch.empty((m, cols), dtype=torch.uint8, device=x.device)
     x_sf = torch.empty(max(n_sf, 1), dtype=torch.uint8, device=x.device)
     if h is None and residual is not None:
         h = torch.empty((m, k), dtype=torch.bfloat16, device=x.device)
-    nvfp4_add_rmsnorm_quant(x, _ld(x, "x"), residual, _ld(residual, "residual") if residual is not None else 0, gamma,
-                            eps, m, k, fmt, gs, h, _ld(h, "h") if h is not None else 0, x_q, x_sf, stream)
+    nvfp4_add_rmsnorm_quant(x, ldx, residual, ldr, gamma, eps, m, k, fmt, gs, h, h.stride(0) if h is not None else 0, x_q,
+                            x_sf, stream)
     return x_q, x_sf, h
 
 
@@ -505,6 +585,7 @@ def moe_sort(expert_ids, experts: int, stream=None):
     tokens, topk = expert_ids.shape
     if not expert_ids.is_contiguous() or expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be a contiguous int32 or int64 tensor")
+    _on_gpu(expert_ids=expert_ids)
     new = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device=expert_ids.device)  # noqa: E731
     offsets, counts, dest = new(experts + 1), new(experts), new(tokens, topk)
     ws = new(nvfp4_moe_sort_workspace_bytes(tokens, topk, experts), dtype=torch.uint8)
@@ -516,47 +597,64 @@ def moe_sort(expert_ids, experts: int, stream=None):
 def moe_dispatch(x, dest, group_offsets, group_counts, out=None, stream=None):
     """Rows of a [tokens, h] bf16 CUDA tensor in the order of moe_sort, [nvfp4_moe_rows, h]."""
     import torch
-    tokens, topk = dest.shape
+    tokens, topk = _routing(dest, group_offsets, group_counts)
+    ldx = _rows_of(x, "x", tokens, 0)
     experts, h = group_counts.numel(), x.shape[1]
+    if out is not None:
+        _rows_of(out, "out", 0, h)                           # (its rows: the library's check)
+    _on_gpu(x=x, dest=dest, group_offsets=group_offsets, group_counts=group_counts, out=out)
     if out is None:
         out = torch.empty((nvfp4_moe_rows(tokens, topk, experts), h), dtype=torch.bfloat16, device=x.device)
-    nvfp4_moe_dispatch(x, _ld(x, "x"), dest, tokens, topk, out.shape[0], h, group_offsets, group_counts, experts, out,
-                       _ld(out, "out"), stream)
+    nvfp4_moe_dispatch(x, ldx, dest, tokens, topk, out.shape[0], h, group_offsets, group_counts, experts, out,
+                       out.stride(0), stream)
     return out
 
 
 def moe_dispatch_quant(x, gs, dest, experts: int, stream=None):
     """The same as the NVFP4 operand of nvfp4_grouped_gemm; returns (x_fp4, flat x_sf)."""
     import torch
-    tokens, topk = dest.shape
+    tokens, topk = _routing(dest)
+    ldx = _rows_of(x, "x", tokens, 0)
+    _flat(gs, "gs", "float32", 1)
+    _on_gpu(x=x, gs=gs, dest=dest)
     h = x.shape[1]
     rows = nvfp4_moe_rows(tokens, topk, experts)
     x_fp4 = torch.empty((rows, padded_k(h) // 2), dtype=torch.uint8, device=x.device)
     x_sf = torch.empty(max(nvfp4_scale_bytes(rows, h), 1), dtype=torch.uint8, device=x.device)
-    nvfp4_moe_dispatch_quant(x, _ld(x, "x"), gs, dest, tokens, topk, rows, h, x_fp4, x_sf, stream)
+    nvfp4_moe_dispatch_quant(x, ldx, gs, dest, tokens, topk, rows, h, x_fp4, x_sf, stream)
     return x_fp4, x_sf
 
 
 def moe_combine(y, dest, weights=None, residual=None, out=None, stream=None):
-    """[tokens, h] bf16: each token's expert rows, weighted and summed, plus residual."""
+    """[tokens, h] bf16: each token's expert rows, weighted (fp32 [tokens, topk]) and summed,
+    plus residual."""
     import torch
-    tokens, topk = dest.shape
+    tokens, topk = _routing(dest, weights=weights)
+    ldy = _rows_of(y, "y", 0, 0)
     h = y.shape[1]
+    ldr = _rows_of(residual, "residual", tokens, h) if residual is not None else 0
+    if out is not None:
+        _rows_of(out, "out", tokens, h)
+    _on_gpu(y=y, dest=dest, weights=weights, residual=residual, out=out)
     if out is None:
         out = torch.empty((tokens, h), dtype=torch.bfloat16, device=y.device)
-    nvfp4_moe_combine(y, _ld(y, "y"), weights, dest, tokens, topk, y.shape[0], h, residual,
-                      _ld(residual, "residual") if residual is not None else 0, out, _ld(out, "out"), stream)
+    nvfp4_moe_combine(y, ldy, weights, dest, tokens, topk, y.shape[0], h, residual, ldr, out, out.stride(0), stream)
     return out
 
 
 def moe_combine_backward(dout, y, weights, dest, group_offsets, group_counts, dy=None, stream=None):
     """Gradients (dy [rows, h] bf16, dweights [tokens, topk] fp32) of moe_combine."""
     import torch
-    tokens, topk = dest.shape
+    tokens, topk = _routing(dest, group_offsets, group_counts, weights)
+    ldy = _rows_of(y, "y", 0, 0)
     rows, h = y.shape
+    ldd = _rows_of(dout, "dout", tokens, h)
+    if dy is not None:
+        _rows_of(dy, "dy", rows, h)
+    _on_gpu(dout=dout, y=y, weights=weights, dest=dest, group_offsets=group_offsets, group_counts=group_counts, dy=dy)
     if dy is None:
         dy = torch.empty((rows, h), dtype=torch.bfloat16, device=y.device)
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=y.device)
-    nvfp4_moe_combine_backward(dout, _ld(dout, "dout"), y, _ld(y, "y"), weights, dest, tokens, topk, rows, h,
-                               group_offsets, group_counts, group_counts.numel(), dy, _ld(dy, "dy"), dweights, stream)
+    nvfp4_moe_combine_backward(dout, ldd, y, ldy, weights, dest, tokens, topk, rows, h, group_offsets, group_counts,
+                               group_counts.numel(), dy, dy.stride(0), dweights, stream)
     return dy, dweights
