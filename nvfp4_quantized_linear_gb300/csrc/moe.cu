@@ -9,6 +9,8 @@
 // The gradient of dispatch is combine without weights.  Every kernel but the
 // sort is a stream over rows: bytes bound it.  No atomics on values anywhere:
 // sums run over k in order, so results do not depend on scheduling.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "block_launch.cuh"
@@ -315,8 +317,9 @@ __global__ void __launch_bounds__(256) moe_dispatch_quant_kernel(const MoeRowsPa
 // thread, are requested together, with the next step's row numbers and weights
 // behind them, so that one memory latency passes per step instead of two and a
 // block start.  Small topk takes more tokens per step: with one row in flight
-// per thread 16384 tokens of topk 1 moved 1.6 TB/s, with four 5.4 TB/s (at 85
-// registers).  topk > kK (= 8) goes round.
+// per thread 16384 tokens of topk 1 moved 1.6 TB/s, with four 5.4 TB/s (the
+// instance's bound of six blocks is 80 registers, 28 bytes spilled; 108 where
+// h % 8 != 0).  topk > kK (= 8) goes round.
 template <bool kWhole, int kK, int kT>
 __global__ void __launch_bounds__(128, kK == 1 ? 6 : 8) moe_combine_kernel(const MoeRowsParams p)
 {
@@ -539,12 +542,21 @@ namespace {
 template <bool kWhole, int kK, int kT>
 cudaError_t launch_combine(const MoeRowsParams &p, int num_sms, cudaStream_t s)
 {
-    // 128 threads (fewer for short rows) of 64 registers: 1024 threads per SM
+    // 128 threads (fewer for short rows) of 64 registers at most: 1024 threads per SM
+    // (topk 1: 80 registers and 768 threads; it has a block per step)
     const int threads = p.h >= 1024 ? 128 : ((p.h + 7) / 8 + 31) / 32 * 32, parts = (p.h + threads * 8 - 1) / (threads * 8);
-    const int64_t resident = ((int64_t)num_sms * (1024 / threads) + parts - 1) / parts, steps = (p.tokens + kT - 1) / kT;
-    // Persistent blocks from six rounds on, but for topk 1 (16384 tokens, topk 8, 2048 columns:
-    // 87 us, 93 us with a block per step); below, whole rounds are too coarse
-    // (1003 tokens, topk 6, 5120 columns: 15.5 us persistent, 13.5 us not).
+    // (rounded down: one part of a step more than fits, and its blocks run alone at the end,
+    // topk 8, 5120 columns, 6561 tokens: 119 us instead of 87)
+    const int64_t resident = std::max<int64_t>(1, (int64_t)num_sms * (1024 / threads) / parts);
+    const int64_t steps = (p.tokens + kT - 1) / kT;
+    // Persistent blocks from six rounds on, but for topk 1.  A block per step / persistent,
+    // us, at 2, 6, 12 and 27 rounds:
+    //   topk 1, 5120 columns   7.4 / 8.4   22.0 / 24.8   42.8 / 48.8  106.7 / 107.7
+    //   topk 2, 2048           5.4 / 5.0   15.1 / 14.3   34.0 / 29.8   76.1 / 62.9
+    //   topk 8, 2048           8.4 / 8.0   21.7 / 22.2   43.1 / 40.8   92.7 / 87.2
+    //   topk 8, 5120           8.6 / 8.9   22.2 / 22.5   41.5 / 41.0   94.1 / 86.8
+    //   topk 3, 7168           4.3 / 4.4   10.9 / 11.1   21.9 / 21.5   46.9 / 45.0
+    // Below six some sizes win by it and others lose, by a few percent either way.
     const int64_t blocks = kK == 1 || steps < 6 * resident ? steps : resident;
     return launch_dependent(moe_combine_kernel<kWhole, kK, kT>, dim3((unsigned)blocks, (unsigned)parts, 1), threads, 0, s,
                             p);

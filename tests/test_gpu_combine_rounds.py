@@ -21,7 +21,7 @@ def tokens_per_round(topk, h):
     threads = 128 if h >= 1024 else ((h + 7) // 8 + 31) // 32 * 32
     parts = -(-h // (threads * 8))
     sms = torch.cuda.get_device_properties(0).multi_processor_count
-    resident = (sms * (1024 // threads) + parts - 1) // parts
+    resident = max(1, sms * (1024 // threads) // parts)
     return resident * (2 if topk == 2 else 1)
 
 
