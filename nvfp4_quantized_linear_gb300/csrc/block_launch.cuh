@@ -11,7 +11,7 @@ namespace nvfp4 {
 // Quantized formats of the norm's output (values of the C ABI's nvfp4_format).
 enum Format : int32_t { kFmtNvfp4 = 0, kFmtMxfp4 = 1, kFmtMxfp8 = 2 };
 
-constexpr int64_t kNormMaxK = 65536;     // the row stays in one CTA's registers
+constexpr int64_t kNormMaxK = 65536;     // 1024 threads x 4 steps x 16 elements: a row is one CTA's
 
 struct NormQuantParams {
     const uint16_t *x, *residual, *gamma;   // bf16 bits; residual may be nullptr

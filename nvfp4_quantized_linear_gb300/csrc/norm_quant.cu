@@ -7,9 +7,11 @@
 //
 // A CTA works on one row at a time.  A thread owns 16 consecutive elements per
 // step, one NVFP4 block or half of an MX block, so block maxima, scales and
-// packed codes need no shared memory; the row's fp32 values stay in registers
+// packed codes need no shared memory; the row's fp32 values stay with their thread
 // between the sum of squares and the quantization, so each input byte is read
-// once.
+// once.  They stay in registers up to k = 16384 (64 registers for two steps of 16, 16
+// bytes of MXFP8's spilled); the instances of four steps, for longer rows, hold 1024
+// threads at 64 registers and spill 224 bytes a thread.
 #include <algorithm>
 
 #include <cuda_bf16.h>

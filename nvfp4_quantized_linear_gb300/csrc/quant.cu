@@ -59,8 +59,9 @@ __device__ __forceinline__ uint4 transpose_bytes(uint32_t a, uint32_t b, uint32_
 // they are four words in four sectors.  Units follow each other along the rows and
 // from one four rows to the next, so that short rows leave no lane idle; those past
 // m store scales of zero and nothing else.  Measured against a row's 512 elements per
-// warp and a word of scales at a time: 65536 x 4096 121 to 112 us, 8192 x 4096 17.1 to
-// 15.6, 12256 x 768 8.7 to 6.0, 64 x 4096 2.7 to 2.0.
+// warp and a word of scales at a time: 65536 x 4096 120 to 112 us, 8192 x 4096 15.5 to
+// 13.6, 12256 x 768 8.4 to 5.3, 64 x 4096 2.9 to 2.2, 333 x 4104 3.1 to 3.0; slower is
+// 1024 x 4104, 4.1 to 4.5.
 __global__ void __launch_bounds__(256) quant_kernel(const QuantParams p)
 {
     const int lane = threadIdx.x & 31;
