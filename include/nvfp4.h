@@ -519,7 +519,8 @@ nvfp4_status nvfp4_moe_dispatch_quant(const void *x_bf16, int64_t ldx, const flo
  *   y_bf16         in   [rows, ldy] bf16
  *   weights        in   NULL (all 1) or fp32 [tokens, topk]
  *   residual_bf16  in   NULL or [tokens, ldr] bf16
- *   out_bf16       out  [tokens, ldo] bf16 */
+ *   out_bf16       out  [tokens, ldo] bf16
+ *   h              at most 65535 * 1024 columns */
 nvfp4_status nvfp4_moe_combine(const void *y_bf16, int64_t ldy, const float *weights, const int32_t *dest,
                                int64_t tokens, int topk, int64_t rows, int64_t h, const void *residual_bf16,
                                int64_t ldr, void *out_bf16, int64_t ldo, nvfp4_stream_t stream);

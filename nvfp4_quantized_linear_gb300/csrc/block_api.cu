@@ -256,6 +256,9 @@ nvfp4_status nvfp4_moe_combine(const void *y_bf16, int64_t ldy, const float *wei
     nvfp4_status st = check_moe(tokens, topk);
     if (st == NVFP4_OK) st = check_moe_rows(rows, h);
     if (st != NVFP4_OK) return st;
+    if (h > nvfp4::kMoeCombineMaxH)
+        return fail(NVFP4_ERR_INVALID_ARG, "h must be at most %lld (got %lld)", (long long)nvfp4::kMoeCombineMaxH,
+                    (long long)h);
     if (tokens == 0) return ok();
     if (rows < 1) return fail(NVFP4_ERR_INVALID_ARG, "no rows for %lld tokens", (long long)tokens);
     if ((st = check_rows(y_bf16, h, ldy, "y")) != NVFP4_OK) return st;

@@ -37,6 +37,7 @@ cudaError_t launch_norm_quant(const NormQuantParams &p, int num_sms, cudaStream_
 constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopk = 64;
 constexpr int kMoeSortTile = 1024;           // assignments sorted per step of a block
+constexpr int64_t kMoeCombineMaxH = 65535 * 1024;   // column parts of 1024 are the grid's y
 
 struct MoeSortParams {
     const void *ids;                         // int32 or int64 [tokens * topk]

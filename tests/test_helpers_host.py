@@ -102,3 +102,12 @@ def test_combine_backward():
 
 def test_sort():
     refused(nv.moe_sort, "expert_ids must be a CUDA", expert_ids=zeros(T, TOPK, dtype=torch.int32), experts=E)
+
+
+def test_combine_refuses_more_columns_than_its_grid_takes():
+    """On the host, with the reason, instead of a failed launch."""
+    nv.build()
+    f = nv.load_library().nvfp4_moe_combine
+    h, (y, dest, out) = 65535 * 1024 + 8, (1 << 40, 1 << 20, 1 << 42)
+    assert f(y, h, None, dest, 1, 1, 1, h, None, 0, out, h, None) == 1
+    assert str(65535 * 1024) in nv.nvfp4_last_error_string()
