@@ -536,6 +536,124 @@ nvfp4_status nvfp4_moe_combine_backward(const void *dout_bf16, int64_t ldd, cons
                                         const int32_t *group_counts, int experts, void *dy_bf16, int64_t lddy,
                                         float *dweights, nvfp4_stream_t stream);
 
+/* ---- routing, 8-bit activation checkpoints and their gradients ------------
+ * What stands in front of nvfp4_moe_sort (the router's choice of experts) and,
+ * for training, behind nvfp4_moe_combine_backward: the gradient of that choice,
+ * what is kept of a GEMM's output for the backward pass, and the two gradients
+ * that read it. */
+
+/* Element types of the arguments that take either. */
+typedef enum {
+    NVFP4_TYPE_F32 = 0,
+    NVFP4_TYPE_BF16 = 1
+} nvfp4_type;
+
+/* Scores of a router's logits. */
+typedef enum {
+    NVFP4_SCORE_SOFTMAX = 0,   /* exp(l_i) / sum_j exp(l_j) over the token's experts */
+    NVFP4_SCORE_SIGMOID = 1    /* 1 / (1 + exp(-l_i)) */
+} nvfp4_score;
+
+/* Experts of each token from its router logits:
+ *   l_i    = the logit, +inf as the largest finite float; an expert whose logit
+ *            is -inf or NaN (or whose bias is) is never chosen
+ *   s_i    = its score;  key_i = s_i + bias[i]  (without a bias the order of l)
+ *   groups > 1: experts [g * experts/groups, (g+1) * experts/groups) are group g.
+ *            A group's value is the sum of its group_top (1 or 2) highest keys
+ *            (scores + bias; of its only one where one expert can be chosen),
+ *            and only the topk_groups groups of highest value stay in the choice
+ *   chosen = the topk highest keys in descending order; equal keys (and group
+ *            values) go to the lower index
+ *   weight = scale * s_i, with renormalize scale * s_i / sum of the chosen s
+ * The choice is that of keys in 64 bits: they are computed in 32, and a token
+ * with keys (or groups) too near each other for them is decided again in 64.
+ * Renormalised weights do not underflow, whatever the logits' range.
+ *   logits      in   [tokens, ldl] fp32 or bf16 (an nvfp4_type), rows and base
+ *                    aligned to their elements only
+ *   bias        in   NULL or fp32 [experts]
+ *   topk        <= experts, at most 64; experts at most 1024
+ *   groups      1 .. 32, divides experts;  1 <= topk_groups <= groups
+ *   expert_ids  out  int32 [tokens, topk], as nvfp4_moe_sort takes them; -1
+ *                    past the experts that can be chosen (a token whose logits
+ *                    are all -inf is routed nowhere)
+ *   weights     out  fp32 [tokens, topk], 0 where the id is -1 */
+nvfp4_status nvfp4_moe_route(const void *logits, int type, int64_t ldl, const float *bias, int64_t tokens,
+                             int experts, int score, int topk, int groups, int group_top, int topk_groups,
+                             int renormalize, float scale, int32_t *expert_ids, float *weights,
+                             nvfp4_stream_t stream);
+
+/* Gradient of the routing weights with respect to the logits, the choice held
+ * fixed (the bias has none):
+ *   dlogits[t, i] = sum_j dweights[t, j] * d weights[t, j] / d l[t, i]
+ * Ids outside [0, experts) take no part.  Every column of a row is written:
+ * zeros for experts without a gradient, and for masked ones.
+ *   dweights    in   fp32 [tokens, topk], e.g. of nvfp4_moe_combine_backward
+ *   expert_ids  in   from nvfp4_moe_route
+ *   logits      in   as there
+ *   dlogits     out  [tokens, ldd], the logits' type */
+nvfp4_status nvfp4_moe_route_backward(const float *dweights, const int32_t *expert_ids, const void *logits, int type,
+                                      int64_t ldl, int64_t tokens, int experts, int score, int topk,
+                                      int renormalize, float scale, void *dlogits, int64_t ldd,
+                                      nvfp4_stream_t stream);
+
+/* An activation and the checkpoint of its input, for the backward pass:
+ *   out      = bf16(act(x)) (fp32 inside), gated: bf16(g(x[:, 2j]) * x[:, 2j+1])
+ *   q, sf    = x in MXFP8 (nvfp4_add_rmsnorm_quant's format and layouts)
+ * x is a GEMM's output before the activation; with NVFP4_ACT_NONE and out NULL
+ * the call is a plain MXFP8 quantizer.  A block of 32 with an infinity or NaN
+ * gets scale code 255 (E8M0's NaN), and all its values read back as NaN.
+ *   x_bf16    in   [m, ldx] bf16; k = n_out columns, 2 * n_out with a gated act
+ *   group_offsets, group_counts   in   NULL (num_groups 0), or as
+ *                  nvfp4_moe_sort's: x then holds the sorted rows of an expert
+ *                  layer, and only the groups' real rows are read and written
+ *   out_bf16  out  NULL or [m, ldo] bf16
+ *   q         out  nvfp4_mxfp8_bytes(m, k)
+ *   sf        out  nvfp4_mxfp4_scale_bytes(m, k) (padding columns, and without
+ *                  groups padding rows, zero) */
+nvfp4_status nvfp4_act_checkpoint(const void *x_bf16, int64_t ldx, int64_t m, int64_t n_out, int act,
+                                  const int32_t *group_offsets, const int32_t *group_counts, int num_groups,
+                                  void *out_bf16, int64_t ldo, uint8_t *q, uint8_t *sf, nvfp4_stream_t stream);
+
+/* Gradient of the activation from the checkpoint, and the activation again:
+ *   dx       = bf16(act'(x) * dout), x the checkpoint's values (fp32 inside);
+ *              gated: dx[:, 2j] = g'(x[:, 2j]) x[:, 2j+1] dout, dx[:, 2j+1] = g(x[:, 2j]) dout
+ *   act_q, act_sf = act(x) in MXFP8, the operand of the next layer's
+ *              nvfp4_checkpoint_wgrad, so that it need not be kept
+ *   dout_bf16  in   [m, ldd] bf16, n_out columns
+ *   q, sf      in   from nvfp4_act_checkpoint
+ *   dx_bf16    out  [m, ldx] bf16, k columns.  NULL (with dout NULL): not computed
+ *   act_q      out  nvfp4_mxfp8_bytes(m, n_out), act_sf nvfp4_mxfp4_scale_bytes(m,
+ *                   n_out).  Both NULL: not computed
+ * With groups the groups' real rows are computed, dx's padding rows set to zero,
+ * and everything else left alone, as in nvfp4_moe_combine_backward. */
+nvfp4_status nvfp4_act_checkpoint_backward(const void *dout_bf16, int64_t ldd, const uint8_t *q, const uint8_t *sf,
+                                           int64_t m, int64_t n_out, int act, const int32_t *group_offsets,
+                                           const int32_t *group_counts, int num_groups, void *dx_bf16, int64_t ldx,
+                                           uint8_t *act_q, uint8_t *act_sf, nvfp4_stream_t stream);
+
+/* Weight gradient of a linear from the checkpoint of its input:
+ *   dw[j, c] = sum_r dy[r, j] * x[r, c]     (dW = dY^T X, the weight's [n, k])
+ * on the bf16 tensor cores: every MXFP8 value of magnitude 2^-126 or more (and
+ * below 2^127) is exact in bf16, products are exact and sums in fp32.  With
+ * groups every expert has its own sum, over its group's real rows, stacked as
+ * nvfp4_grouped_gemm's weights: dw[g * n + j, c].  What dy and x hold in
+ * padding rows does not matter.  No rows: zeros.  For a gated activation in
+ * front n counts gate and up columns, interleaved.
+ *   dy_bf16     in   [m, ldd] bf16, n columns
+ *   q, sf       in   x [m, k] in MXFP8
+ *   type        an nvfp4_type: of dw
+ *   accumulate  1: dw += the sum (fp32 only)
+ *   dw          out  [n, ldw] (groups: [num_groups * n, ldw]), ldw >= k, rows on
+ *                    16-byte boundaries; columns past k are left alone
+ *   workspace   device scratch of nvfp4_checkpoint_wgrad_workspace_bytes: a
+ *               weight of few tiles splits its rows, and the ranges' sums meet
+ *               there (added in order: results do not depend on scheduling) */
+size_t nvfp4_checkpoint_wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int num_groups);
+nvfp4_status nvfp4_checkpoint_wgrad(const void *dy_bf16, int64_t ldd, const uint8_t *q, const uint8_t *sf, int64_t m,
+                                    int64_t n, int64_t k, const int32_t *group_offsets, const int32_t *group_counts,
+                                    int num_groups, int type, int accumulate, void *dw, int64_t ldw, void *workspace,
+                                    size_t workspace_bytes, nvfp4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

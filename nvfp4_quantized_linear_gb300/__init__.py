@@ -31,6 +31,9 @@ __all__ = [
     "nvfp4_moe_combine_backward", "ACTIVATIONS", "NVFP4_FORMAT_NVFP4", "NVFP4_FORMAT_MXFP4", "NVFP4_FORMAT_MXFP8",
     "interleave_gate_up", "add_rmsnorm_quant", "moe_sort", "moe_dispatch", "moe_dispatch_quant", "moe_combine",
     "moe_combine_backward",
+    "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_act_checkpoint", "nvfp4_act_checkpoint_backward",
+    "nvfp4_checkpoint_wgrad", "nvfp4_checkpoint_wgrad_workspace_bytes", "SCORES", "NVFP4_TYPE_F32", "NVFP4_TYPE_BF16",
+    "moe_route", "moe_route_backward", "act_checkpoint", "act_checkpoint_backward", "checkpoint_wgrad",
     "padded_k", "scale_shape", "quant_act", "quant_act_mx", "prepare_weight", "linear", "act_global_scale",
 ]
 
@@ -48,6 +51,9 @@ STATUS_NAMES = {0: "NVFP4_OK", 1: "NVFP4_ERR_INVALID_ARG", 2: "NVFP4_ERR_UNSUPPO
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4, "geglu": 5}
 GATED_ACTIVATIONS = ("swiglu", "geglu")
 NVFP4_FORMAT_NVFP4, NVFP4_FORMAT_MXFP4, NVFP4_FORMAT_MXFP8 = 0, 1, 2
+# Values of nvfp4_score and nvfp4_type.
+SCORES = {"softmax": 0, "sigmoid": 1}
+NVFP4_TYPE_F32, NVFP4_TYPE_BF16 = 0, 1
 
 # (name, restype, argtypes) of every exported symbol of include/nvfp4.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
@@ -94,6 +100,13 @@ EXPORTS = [
     ("nvfp4_moe_combine", _I32, [_P, _I64, _P, _P, _I64, _I32, _I64, _I64, _P, _I64, _P, _I64, _P]),
     ("nvfp4_moe_combine_backward", _I32, [_P, _I64, _P, _I64, _P, _P, _I64, _I32, _I64, _I64, _P, _P, _I32, _P, _I64,
                                           _P, _P]),
+    ("nvfp4_moe_route", _I32, [_P, _I32, _I64, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _P,
+                               _P]),
+    ("nvfp4_moe_route_backward", _I32, [_P, _P, _P, _I32, _I64, _I64, _I32, _I32, _I32, _I32, ctypes.c_float, _P, _I64, _P]),
+    ("nvfp4_act_checkpoint", _I32, [_P, _I64, _I64, _I64, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P]),
+    ("nvfp4_act_checkpoint_backward", _I32, [_P, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _I32, _P, _I64, _P, _P, _P]),
+    ("nvfp4_checkpoint_wgrad_workspace_bytes", _SZ, [_I64, _I64, _I64, _I32]),
+    ("nvfp4_checkpoint_wgrad", _I32, [_P, _I64, _P, _P, _I64, _I64, _I64, _P, _P, _I32, _I32, _I32, _P, _I64, _P, _SZ, _P]),
 ]
 
 
@@ -452,6 +465,45 @@ def nvfp4_moe_combine_backward(dout, ldd: int, y, ldy: int, weights, dest, token
                                                      _ptr(dy), lddy, _ptr(dweights), _stream(stream)))
 
 
+def nvfp4_moe_route(logits, type: int, ldl: int, bias, tokens: int, experts: int, score: int, topk: int, groups: int,
+                    group_top: int, topk_groups: int, renormalize: bool, scale: float, expert_ids, weights,
+                    stream=None) -> None:
+    _check(load_library().nvfp4_moe_route(_ptr(logits), type, ldl, _ptr(bias), tokens, experts, score, topk, groups,
+                                          group_top, topk_groups, renormalize, scale, _ptr(expert_ids), _ptr(weights),
+                                          _stream(stream)))
+
+
+def nvfp4_moe_route_backward(dweights, expert_ids, logits, type: int, ldl: int, tokens: int, experts: int, score: int,
+                             topk: int, renormalize: bool, scale: float, dlogits, ldd: int, stream=None) -> None:
+    _check(load_library().nvfp4_moe_route_backward(_ptr(dweights), _ptr(expert_ids), _ptr(logits), type, ldl, tokens,
+                                                   experts, score, topk, renormalize, scale, _ptr(dlogits), ldd,
+                                                   _stream(stream)))
+
+
+def nvfp4_act_checkpoint(x, ldx: int, m: int, n_out: int, act: int, group_offsets, group_counts, num_groups: int, out,
+                         ldo: int, q, sf, stream=None) -> None:
+    _check(load_library().nvfp4_act_checkpoint(_ptr(x), ldx, m, n_out, act, _ptr(group_offsets), _ptr(group_counts),
+                                               num_groups, _ptr(out), ldo, _ptr(q), _ptr(sf), _stream(stream)))
+
+
+def nvfp4_act_checkpoint_backward(dout, ldd: int, q, sf, m: int, n_out: int, act: int, group_offsets, group_counts,
+                                  num_groups: int, dx, ldx: int, act_q, act_sf, stream=None) -> None:
+    _check(load_library().nvfp4_act_checkpoint_backward(_ptr(dout), ldd, _ptr(q), _ptr(sf), m, n_out, act,
+                                                        _ptr(group_offsets), _ptr(group_counts), num_groups, _ptr(dx), ldx,
+                                                        _ptr(act_q), _ptr(act_sf), _stream(stream)))
+
+
+def nvfp4_checkpoint_wgrad_workspace_bytes(m: int, n: int, k: int, num_groups: int = 0) -> int:
+    return load_library().nvfp4_checkpoint_wgrad_workspace_bytes(m, n, k, num_groups)
+
+
+def nvfp4_checkpoint_wgrad(dy, ldd: int, q, sf, m: int, n: int, k: int, group_offsets, group_counts, num_groups: int,
+                           type: int, accumulate: bool, dw, ldw: int, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(load_library().nvfp4_checkpoint_wgrad(_ptr(dy), ldd, _ptr(q), _ptr(sf), m, n, k, _ptr(group_offsets),
+                                                 _ptr(group_counts), num_groups, type, accumulate, _ptr(dw), ldw,
+                                                 _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
 # --------------------------------------------- tensor-level conveniences ----
 # Thin helpers that allocate the caller-owned outputs with torch and call the
 # entry points above; they add no computation.
@@ -658,3 +710,161 @@ def moe_combine_backward(dout, y, weights, dest, group_offsets, group_counts, dy
     nvfp4_moe_combine_backward(dout, ldd, y, ldy, weights, dest, tokens, topk, rows, h, group_offsets, group_counts,
                                group_counts.numel(), dy, dy.stride(0), dweights, stream)
     return dy, dweights
+
+
+def _logits(logits, topk, score):
+    """(type, row stride, tokens, experts, score code) of a router's logits."""
+    if score not in SCORES:
+        raise ValueError(f"unknown score {score!r}, not one of {', '.join(SCORES)}")
+    ld = _ld(logits, "logits")
+    got = str(logits.dtype)[len("torch."):]
+    if got not in ("float32", "bfloat16"):
+        raise ValueError(f"logits must be float32 or bfloat16, got {got}")
+    tokens, experts = logits.shape
+    return NVFP4_TYPE_F32 if got == "float32" else NVFP4_TYPE_BF16, max(ld, experts), tokens, experts, SCORES[score]
+
+
+def moe_route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, group_top: int = 1,
+              topk_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Experts of [tokens, experts] fp32 or bf16 router logits; returns (expert_ids int32, weights
+    fp32), both [tokens, topk], as moe_sort and moe_combine take them.  bias (fp32 [experts])
+    takes part in the choice only; score is a key of SCORES."""
+    import torch
+    kind, ld, tokens, experts, code = _logits(logits, topk, score)
+    _flat(bias, "bias", "float32", experts)
+    _on_gpu(logits=logits, bias=bias)
+    ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+    nvfp4_moe_route(logits, kind, ld, bias, tokens, experts, code, topk, groups, group_top, topk_groups, renormalize, scale,
+                    ids, weights, stream)
+    return ids, weights
+
+
+def moe_route_backward(dweights, expert_ids, logits, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                       stream=None):
+    """Gradient of moe_route's weights: dlogits, of the logits' shape and type."""
+    import torch
+    if expert_ids.dim() != 2:
+        raise ValueError(f"expert_ids must be [tokens, topk], got {tuple(expert_ids.shape)}")
+    topk = expert_ids.shape[1]
+    kind, ld, tokens, experts, code = _logits(logits, topk, score)
+    _flat(expert_ids, "expert_ids", "int32", 0)
+    _flat(dweights, "dweights", "float32", 0)
+    if expert_ids.shape[0] != tokens:
+        raise ValueError(f"expert_ids must have a row per token ({tokens}), got {tuple(expert_ids.shape)}")
+    if dweights.shape != expert_ids.shape:
+        raise ValueError(f"dweights must be {tuple(expert_ids.shape)} like expert_ids, got {tuple(dweights.shape)}")
+    _on_gpu(logits=logits, expert_ids=expert_ids, dweights=dweights)
+    dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    nvfp4_moe_route_backward(dweights, expert_ids, logits, kind, ld, tokens, experts, code, topk, renormalize, scale, dlogits,
+                             experts, stream)
+    return dlogits
+
+
+def _group_rows(group_offsets, group_counts):
+    """num_groups of a pair of group tensors of moe_sort (0 without them)."""
+    if (group_offsets is None) != (group_counts is None):
+        raise ValueError("group_offsets and group_counts go together")
+    if group_counts is None:
+        return 0
+    _flat(group_counts, "group_counts", "int32", 1)
+    _flat(group_offsets, "group_offsets", "int32", group_counts.numel() + 1)
+    return group_counts.numel()
+
+
+def _mxfp8(q, sf, rows, cols, names=("q", "sf")):
+    """An MXFP8 operand of rows x cols, as act_checkpoint returns it."""
+    _flat(q, names[0], "uint8", rows * padded_k(cols))
+    _flat(sf, names[1], "uint8", nvfp4_mxfp4_scale_bytes(rows, cols))
+
+
+def _new_mxfp8(rows, cols, device):
+    import torch
+    return (torch.empty((rows, padded_k(cols)), dtype=torch.uint8, device=device),
+            torch.empty(max(nvfp4_mxfp4_scale_bytes(rows, cols), 1), dtype=torch.uint8, device=device))
+
+
+def _act_columns(columns, act):
+    """(activation code, output columns) of an activation over `columns`."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}, not one of {', '.join(ACTIVATIONS)}")
+    if act in GATED_ACTIVATIONS and columns % 2:
+        raise ValueError(f"{act} needs gate and up columns, got {columns}")
+    return ACTIVATIONS[act], columns // 2 if act in GATED_ACTIVATIONS else columns
+
+
+def act_checkpoint(x, act: str = "none", group_offsets=None, group_counts=None, out=None, stream=None):
+    """Activation of a [m, k] bf16 CUDA tensor and its checkpoint; returns (out bf16, q [m, Kp], flat
+    sf), q and sf being x in MXFP8.  act "none" without out: the checkpoint alone (out is None).  With
+    group_offsets and group_counts (of moe_sort) x holds sorted expert rows; other rows of
+    the results are then not written."""
+    import torch
+    ldx = _rows_of(x, "x", 0, 0)
+    m, k = x.shape
+    code, n = _act_columns(k, act)
+    groups = _group_rows(group_offsets, group_counts)
+    if out is not None:
+        _rows_of(out, "out", m, n)
+    _on_gpu(x=x, group_offsets=group_offsets, group_counts=group_counts, out=out)
+    if out is None and act != "none":
+        out = torch.empty((m, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=x.device)[:, :n]
+    q, sf = _new_mxfp8(m, k, x.device)
+    nvfp4_act_checkpoint(x, ldx, m, n, code, group_offsets, group_counts, groups, out,
+                         out.stride(0) if out is not None else 0, q, sf, stream)
+    return out, q, sf
+
+
+def act_checkpoint_backward(dout, q, sf, act: str = "none", group_offsets=None, group_counts=None, dx=None,
+                            recompute: bool = False, stream=None):
+    """Gradient of act_checkpoint's activation from its checkpoint; returns (dx bf16, act_q, act_sf), the
+    latter two, act(x) in MXFP8, None unless recompute."""
+    import torch
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}, not one of {', '.join(ACTIVATIONS)}")
+    ldd = _rows_of(dout, "dout", 0, 0)
+    m, n = dout.shape
+    k = 2 * n if act in GATED_ACTIVATIONS else n
+    groups = _group_rows(group_offsets, group_counts)
+    _mxfp8(q, sf, m, k)
+    if dx is not None:
+        _rows_of(dx, "dx", m, k)
+    _on_gpu(dout=dout, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dx=dx)
+    if dx is None:
+        dx = torch.empty((m, (k + 7) // 8 * 8), dtype=torch.bfloat16, device=dout.device)[:, :k]
+    act_q, act_sf = _new_mxfp8(m, n, dout.device) if recompute else (None, None)
+    nvfp4_act_checkpoint_backward(dout, ldd, q, sf, m, n, ACTIVATIONS[act], group_offsets, group_counts, groups, dx,
+                                  dx.stride(0), act_q, act_sf, stream)
+    return dx, act_q, act_sf
+
+
+def checkpoint_wgrad(dy, q, sf, k: int, group_offsets=None, group_counts=None, dw=None, accumulate: bool = False,
+                     dtype=None, workspace=None, stream=None):
+    """Weight gradient dY^T X of a [m, n] bf16 CUDA tensor dy and x [m, k] in MXFP8: [n, k], with groups
+    [num_groups * n, k].  dw gives the output (fp32 or bf16; accumulate adds to an fp32 one), else one
+    of `dtype` (default torch.float32) is allocated."""
+    import torch
+    ldd = _rows_of(dy, "dy", 0, 0)
+    m, n = dy.shape
+    groups = _group_rows(group_offsets, group_counts)
+    _mxfp8(q, sf, m, k)
+    if accumulate and dw is None:
+        raise ValueError("accumulate adds to dw: it needs one")
+    if dw is not None:
+        kind = str(dw.dtype)[len("torch."):]
+        if kind not in ("float32", "bfloat16"):
+            raise ValueError(f"dw must be float32 or bfloat16, got {kind}")
+        _ld(dw, "dw")
+        if dw.shape[0] < max(1, groups) * n or dw.shape[1] < k:
+            raise ValueError(f"dw must hold {max(1, groups) * n} x {k} elements, got {tuple(dw.shape)}")
+    elif dtype not in (None, torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    _flat(workspace, "workspace", "uint8", 0)
+    _on_gpu(dy=dy, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dw=dw, workspace=workspace)
+    if dw is None:
+        dw = torch.empty((max(1, groups) * n, (k + 7) // 8 * 8), dtype=dtype or torch.float32, device=dy.device)[:, :k]
+    if workspace is None:
+        workspace = torch.empty(nvfp4_checkpoint_wgrad_workspace_bytes(m, n, k, groups), dtype=torch.uint8, device=dy.device)
+    kind = NVFP4_TYPE_F32 if dw.dtype == torch.float32 else NVFP4_TYPE_BF16
+    nvfp4_checkpoint_wgrad(dy, ldd, q, sf, m, n, k, group_offsets, group_counts, groups, kind, accumulate, dw, dw.stride(0),
+                           workspace, workspace.numel(), stream)
+    return dw

@@ -1,0 +1,469 @@
+// Weight gradient of a linear from the 8-bit checkpoint of its input:
+//   dw[j, c] = sum_r dy[r, j] * x[r, c],   dy bf16, x MXFP8,
+// dense or per expert group, on the bf16 tensor cores of CTA pairs (tcgen05
+// cta_group::2, kind::f16, fp32 accumulation in TMEM).
+//
+// An MXFP8 value is an E4M3 code times a power of two: four significant bits, so
+// exact in bf16.  The kernel reads x at its 8 bits and widens it in shared memory
+// on the way to the MMA.  The reduction runs over rows, along which both operands
+// are strided, so both are MN-major: their tiles lie in shared memory as the rows
+// lie in memory, 64 columns (128 bytes, 128-byte swizzle) a row.
+//
+// A tile is 256 (dy columns) x 256 (x columns); CTA r of the pair holds dy
+// columns [128r, +128) and x columns [128r, +128) of it, 64 rows a stage.  Sixteen
+// warps per CTA:
+//   warp 0       copies: two 64 x 64 boxes of dy, 64 x 128 codes and the 512-byte
+//                scale tile of a stage
+//   warp 1       allocates TMEM; in the leader one lane issues the pair's MMAs
+//   warps 4..7   epilogue, one TMEM lane quarter each
+//   warps 8..15  widen the codes of a stage to bf16 and clear the rows past a
+//                group's last one in both operands (they may hold anything)
+// Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the
+// next one's MMAs.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "ptx.cuh"
+#include "train_launch.cuh"
+
+namespace nvfp4 {
+namespace {
+
+using namespace gemm_detail;
+
+constexpr int kTile = 256;                               // per pair, both ways
+constexpr int kHalf = 128;                               // per CTA
+constexpr int kRows = 64;                                // of a stage
+constexpr int kStages = 5;
+constexpr uint32_t kBoxBytes = kRows * 128;              // 64 rows x 64 bf16 columns
+constexpr uint32_t kOperandBytes = 2 * kBoxBytes;        // of one stage and CTA: 128 columns
+constexpr uint32_t kCodeBytes = kRows * kHalf;
+constexpr uint32_t kSfBytes = 512;
+constexpr uint32_t kOffA = 0;
+constexpr uint32_t kOffB = kOffA + kStages * kOperandBytes;
+constexpr uint32_t kOffCodes = kOffB + kStages * kOperandBytes;
+constexpr uint32_t kOffSf = kOffCodes + kStages * kCodeBytes;
+constexpr uint32_t kOffBar = kOffSf + kStages * kSfBytes;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;    // barriers + alignment slack
+constexpr uint32_t kTmemCols = 512;
+constexpr int kThreads = 512;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 4;
+constexpr int kConvWarp0 = 8, kConvWarps = 8;
+constexpr uint16_t kBothCtas = 0x3;
+
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kRows * kHalf / 16 == 2 * kConvWarps * 32, "two 16-byte pieces of codes per thread and stage");
+
+// Descriptor of an MN-major operand: 64-column boxes of kBoxBytes (leading byte
+// offset), inside a box groups of eight rows 1024 bytes apart (stride byte offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// bf16 x bf16 with both operands MN-major (bits 15 and 16).
+constexpr uint32_t kIdesc = idesc_bf16(kTile, kTile) | (1u << 15) | (1u << 16);
+
+__device__ __forceinline__ void tc_mma_pair_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// A tile of the walk: its group's rows and its first dy and x columns.
+struct WTile {
+    int first, rows;                                     // rows [first, first + rows)
+    int group, n0, k0;
+};
+
+__device__ __forceinline__ WTile tile_of(const WgradParams &p, int tile)
+{
+    const int per_group = p.num_n_blk * p.num_k_blk;
+    const int g = tile / per_group;
+    const Tile t = tile_coord(tile - g * per_group, p.num_n_blk, p.num_k_blk, 16);
+    WTile w = {0, p.m, g, t.mb * kTile, t.nb * kTile};
+    if (p.offsets != nullptr) {
+        w.first = min(max(p.offsets[g], 0), p.m);
+        w.rows = min(max(p.counts[g], 0), p.m - w.first);
+    }
+    return w;
+}
+
+// Eight codes (two words) of a block with scale factors f1 (and f2, where a power
+// of two beyond bf16 is needed) as four bf16 pairs.  A code's exponent and mantissa
+// moved to bf16's places are its value times 2^-120 (the difference of the
+// exponent biases), subnormals included.
+__device__ __forceinline__ uint32_t widen2(uint32_t pair, uint32_t f1)
+{
+    return mul_bf16x2((pair & 0x80008000u) | ((pair >> 4) & 0x07F007F0u), f1);
+}
+
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t f1, uint32_t &lo, uint32_t &hi)
+{
+    lo = widen2(__byte_perm(w, 0, 0x1404), f1);
+    hi = widen2(__byte_perm(w, 0, 0x3424), f1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmCodes,
+                      const WgradParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);    // this CTA's copies of the stage landed
+    uint64_t *ready = full + kStages;                                  // (leader) both CTAs widened it
+    uint64_t *empty = ready + kStages;                                 // the pair's MMAs released it
+    uint64_t *tmem_full = empty + kStages;                             // [2] accumulator complete
+    uint64_t *tmem_empty = tmem_full + 2;                              // [2] (leader) both CTAs drained it
+    uint64_t *mma_done = tmem_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&ready[s], 2 * kConvWarps);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tmem_full[b], 1);
+            mbar_init(&tmem_empty[b], 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbarrier_init();
+        prefetch_tensormap(&tmDy);
+        prefetch_tensormap(&tmCodes);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    griddep_launch_dependents();
+    griddep_wait();
+
+    const uint32_t tmem = role_tmem(tmem_slot);
+    const uint32_t rank = cluster_ctarank();
+    const int num_pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int num_tiles = p.num_groups * p.num_n_blk * p.num_k_blk;
+
+    if (warp >= kConvWarp0) {
+        // ------------------------------------------------------- widening --
+        const int tid = threadIdx.x - kConvWarp0 * 32;
+        const uint32_t leader_ready = mapa_shared(ready, 0);
+        const uint32_t a_base = smem_u32(smem + kOffA), b_base = smem_u32(smem + kOffB);
+        const uint32_t codes_base = smem_u32(smem + kOffCodes);
+        const int c16 = tid & 7;                         // 16-column piece of a row
+        // (lanes of columns 64 on take their two 16-byte stores the other way round, so
+        // that eight lanes hit eight different banks of four)
+        const int swap = c16 >> 2;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
+            const WTile t = tile_of(p, tile);
+            const int band_row = t.first & 127;
+            for (int r0 = 0; r0 < t.rows; r0 += kRows) {
+                ok = __all_sync(~0u, mbar_wait(&full[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
+                if (!ok) break;
+                const int valid = t.rows - r0;
+                const uint8_t *sf = smem + kOffSf + stage * kSfBytes;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = (tid >> 3) + 32 * i;
+                    const int br = (band_row + r0 + row) & 127;
+                    const uint4 w = ld_shared_v4(codes_base + stage * kCodeBytes + row * kHalf + c16 * 16);
+                    const uint32_t code = sf[(br & 31) * 16 + (br >> 5) * 4 + (c16 >> 1)];
+                    // 2^(code - 127 + 120), the part past bf16's range as a second factor
+                    const uint32_t e = code + 120, e1 = min(e, 254u);
+                    const uint32_t f1 = code == 255 ? 0x7FC07FC0u : (e1 << 7) * 0x10001u;
+                    uint32_t v[8];
+                    widen4(w.x, f1, v[0], v[1]);
+                    widen4(w.y, f1, v[2], v[3]);
+                    widen4(w.z, f1, v[4], v[5]);
+                    widen4(w.w, f1, v[6], v[7]);
+                    if (__any_sync(~0u, e > e1)) {
+                        const uint32_t f2 = ((127 + e - e1) << 7) * 0x10001u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], f2);
+                    }
+                    if (row >= valid)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[j] = 0;
+                    const uint32_t at = b_base + stage * kOperandBytes + (c16 >> 2) * kBoxBytes + row * 128;
+                    const int piece = (c16 & 3) * 2;
+                    const uint32_t first = at + (((piece + swap) ^ (row & 7)) << 4);
+                    const uint32_t second = at + (((piece + 1 - swap) ^ (row & 7)) << 4);
+                    st_shared_v4(first, swap ? v[4] : v[0], swap ? v[5] : v[1], swap ? v[6] : v[2], swap ? v[7] : v[3]);
+                    st_shared_v4(second, swap ? v[0] : v[4], swap ? v[1] : v[5], swap ? v[2] : v[6], swap ? v[3] : v[7]);
+                    if (row >= valid) {                  // dy's row: as many bytes, any order
+                        const uint32_t a = a_base + stage * kOperandBytes + (c16 >> 2) * kBoxBytes + row * 128 + (c16 & 3) * 32;
+                        st_shared_v4(a, 0, 0, 0, 0);
+                        st_shared_v4(a + 16, 0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&ready[stage]);
+                    else mbar_arrive_remote(leader_ready + stage * (uint32_t)sizeof(uint64_t));
+                }
+                if (++stage == kStages) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else if (warp >= kEpiWarp0) {
+        // ------------------------------------------------------- epilogue --
+        const int q = warp & 3;
+        const uint32_t leader_empty = mapa_shared(tmem_empty, 0);
+        uint32_t phase[2] = {0, 0};
+        int buf = 0;
+        for (int tile = pair; tile < num_tiles; tile += num_pairs) {
+            const WTile t = tile_of(p, tile);
+            if (t.rows > 0) {
+                if (!__all_sync(~0u, mbar_wait(&tmem_full[buf], phase[buf], p.err_flag, kErrTimeout, p.wait_ns))) break;
+                phase[buf] ^= 1;
+                tc_fence_after_sync();
+            } else if (p.accumulate) {
+                continue;
+            }
+            const int n = t.n0 + (int)rank * kHalf + q * 32 + lane;
+            const int64_t row = ((int64_t)t.group * p.n + n) * p.ldw;
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile;
+            for (int ch = 0; ch < kTile / 32; ++ch) {
+                const int c = t.k0 + ch * 32;
+                if (c >= p.k) break;
+                uint32_t v[32];
+                if (t.rows > 0) {
+                    tmem_ld_32cols(acc + ch * 32, v);
+                    tmem_ld_wait_regs(v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                }
+                if (n >= p.n) continue;
+                if (p.type == kTypeF32) {
+                    float *o = static_cast<float *>(p.dw) + row + c;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (c + 4 * i + 4 <= p.k) {
+                            float4 f = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                            if (p.accumulate) {
+                                const float4 old = *reinterpret_cast<const float4 *>(o + 4 * i);
+                                f.x += old.x; f.y += old.y; f.z += old.z; f.w += old.w;
+                            }
+                            *reinterpret_cast<float4 *>(o + 4 * i) = f;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (c + 4 * i + j < p.k)
+                                    o[4 * i + j] = __uint_as_float(v[4 * i + j]) + (p.accumulate ? o[4 * i + j] : 0.0f);
+                        }
+                    }
+                } else {
+                    uint16_t *o = static_cast<uint16_t *>(p.dw) + row + c;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = bf16x2_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+                        if (c + 8 * i + 8 <= p.k) {
+                            *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                if (c + 8 * i + j < p.k) o[8 * i + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+                        }
+                    }
+                }
+            }
+            if (t.rows > 0) {
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&tmem_empty[buf]);
+                    else mbar_arrive_remote(leader_empty + buf * (uint32_t)sizeof(uint64_t));
+                }
+                buf ^= 1;
+            }
+        }
+    } else if (warp == 0 && lane == 0) {
+        // --------------------------------------------------------- copies --
+        const uint64_t pol = l2_policy_evict_last();
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, issued_phase = 0;
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
+            const WTile t = tile_of(p, tile);
+            const int n = t.n0 + (int)rank * kHalf, k = t.k0 + (int)rank * kHalf;
+            const bool sf_here = k < p.sf_tiles * 128;
+            for (int r0 = 0; r0 < t.rows; r0 += kRows) {
+                if (!mbar_wait(&empty[stage], phase ^ 1, p.err_flag, kErrTimeout, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                const int row = t.first + r0;
+                // (boxes past the last row or column are zero-filled and count their bytes)
+                mbar_arrive_expect_tx(&full[stage], kOperandBytes + kCodeBytes + (sf_here ? kSfBytes : 0));
+                tma_load_2d(smem + kOffCodes + stage * kCodeBytes, &tmCodes, &full[stage], k, row, pol);
+                if (sf_here)
+                    bulk_load(smem + kOffSf + stage * kSfBytes,
+                              p.sf + ((int64_t)(row >> 7) * p.sf_tiles + (k >> 7)) * kSfBytes, kSfBytes, &full[stage], pol);
+                tma_load_2d(smem + kOffA + stage * kOperandBytes, &tmDy, &full[stage], n, row, pol);
+                tma_load_2d(smem + kOffA + stage * kOperandBytes + kBoxBytes, &tmDy, &full[stage], n + 64, row, pol);
+                issued |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == kStages) { stage = 0; phase ^= 1; }
+            }
+        }
+        for (int s = 0; s < kStages; ++s)                // nothing in flight when the CTA ends
+            if (issued & (1u << s)) mbar_wait(&full[s], (issued_phase >> s) & 1u, p.err_flag, kErrTimeout, p.wait_ns);
+    } else if (warp == 1 && rank == 0) {
+        // ------------------------------------------------------------ MMA --
+        const bool issuer = elect_one();
+        const uint32_t a_base = smem_u32(smem + kOffA), b_base = smem_u32(smem + kOffB);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, acc_phase[2] = {0, 0};
+        bool ok = true;
+        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
+            const WTile t = tile_of(p, tile);
+            if (t.rows == 0) continue;
+            ok = __all_sync(~0u, mbar_wait(&tmem_empty[buf], acc_phase[buf] ^ 1, p.err_flag, kErrTimeout, p.wait_ns));
+            if (!ok) break;
+            tc_fence_after_sync();
+            for (int r0 = 0; r0 < t.rows; r0 += kRows) {
+                ok = __all_sync(~0u, mbar_wait(&ready[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const int steps = min(kRows / 16, (t.rows - r0 + 15) / 16);
+                const uint64_t ad = desc_mn_sw128(a_base + stage * kOperandBytes);
+                const uint64_t bd = desc_mn_sw128(b_base + stage * kOperandBytes);
+                if (issuer) {
+                    for (int kk = 0; kk < steps; ++kk)   // 16 rows of 128 bytes
+                        tc_mma_pair_bf16(tmem + buf * kTile, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), kIdesc,
+                                         (r0 | kk) != 0);
+                    tc_commit_pair_multicast(&empty[stage], kBothCtas);
+                }
+                if (++stage == kStages) { stage = 0; phase ^= 1; }
+            }
+            if (!ok) break;
+            if (issuer) tc_commit_pair_multicast(&tmem_full[buf], kBothCtas);
+            __syncwarp();
+            acc_phase[buf] ^= 1;
+            buf ^= 1;
+        }
+        if (issuer) tc_commit_pair(mma_done);
+        __syncwarp();
+        mbar_wait(mma_done, 0, p.err_flag, kErrTimeout, p.wait_ns);
+    }
+
+    tc_fence_before_sync();
+    __syncwarp();
+    cluster_sync_all();                 // no peer access to this CTA's smem or TMEM after this point
+    tc_fence_after_sync();
+    if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
+              uint32_t box_cols, CUtensorMapSwizzle swizzle)
+{
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_cols, kRows};
+    cuuint32_t estr[2] = {1, 1};
+    return encode(map, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+size_t wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int groups)
+{
+    (void)m; (void)n; (void)k; (void)groups;
+    return 16;
+}
+
+cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ldd, const uint8_t *q, int num_sms,
+                         cudaStream_t s, const char **why)
+{
+    static int configured_device = -1;
+    static int max_pairs = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        cudaError_t e = cudaFuncSetAttribute(wgrad_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t probe = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        probe.gridDim = dim3(2 * (num_sms / 2), 1, 1);
+        probe.blockDim = dim3(kThreads, 1, 1);
+        probe.dynamicSmemBytes = kSmemBytes;
+        probe.attrs = &attr;
+        probe.numAttrs = 1;
+        int clusters = 0;
+        e = cudaOccupancyMaxActiveClusters(&clusters, wgrad_pair_kernel, &probe);
+        if (e != cudaSuccess || clusters < 1) {
+            cudaGetLastError();
+            clusters = num_sms / 2;
+        }
+        max_pairs = clusters;
+        configured_device = dev;
+    }
+    WgradParams p = p_in;
+    p.num_n_blk = (p.n + kTile - 1) / kTile;
+    p.num_k_blk = (p.k + kTile - 1) / kTile;
+    // (no rows: the maps are not read)
+    const void *dy_base = p.m > 0 ? static_cast<const void *>(dy) : p.dw, *q_base = p.m > 0 ? q : p.dw;
+    const uint64_t rows = p.m > 0 ? (uint64_t)p.m : 1;
+    CUtensorMap tmDy, tmCodes;
+    if (!make_map(&tmDy, CU_TENSOR_MAP_DATA_TYPE_UINT16, dy_base, (uint64_t)p.n, rows,
+                  p.m > 0 ? (uint64_t)ldd * 2 : ((uint64_t)p.n * 2 + 15) / 16 * 16, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&tmCodes, CU_TENSOR_MAP_DATA_TYPE_UINT8, q_base, (uint64_t)p.kp, rows, (uint64_t)p.kp, kHalf,
+                  CU_TENSOR_MAP_SWIZZLE_NONE)) {
+        *why = "cuTensorMapEncodeTiled failed for an operand of the weight gradient";
+        return cudaErrorInvalidValue;
+    }
+    const int tiles = p.num_groups * p.num_n_blk * p.num_k_blk;
+    const int pairs = std::min(tiles, max_pairs);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, wgrad_pair_kernel, tmDy, tmCodes, p);
+}
+
+}  // namespace nvfp4
