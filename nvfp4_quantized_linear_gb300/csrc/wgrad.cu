@@ -10,14 +10,15 @@
 // lie in memory, 64 columns (128 bytes, 128-byte swizzle) a row.
 //
 // A tile is 256 (dy columns) x 256 (x columns); CTA r of the pair holds dy
-// columns [128r, +128) and x columns [128r, +128) of it, 64 rows a stage.  Sixteen
+// columns [128r, +128) and x columns [128r, +128) of it, 64 rows a stage.  Twenty
 // warps per CTA:
 //   warp 0       copies: two 64 x 64 boxes of dy, 64 x 128 codes and the 512-byte
 //                scale tile of a stage
 //   warp 1       allocates TMEM; in the leader one lane issues the pair's MMAs
 //   warps 4..7   epilogue, one TMEM lane quarter each
-//   warps 8..15  widen the codes of a stage to bf16 and clear the rows past a
-//                group's last one in both operands (they may hold anything)
+//   warps 8..19  three groups, each widening every third stage's codes to bf16 (a ring
+//                of its own: three slots, six stages of copies) and clearing the rows
+//                past a group's last one in both operands (they may hold anything)
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the
 // next one's MMAs.
 #include <algorithm>
@@ -37,25 +38,33 @@ using namespace gemm_detail;
 constexpr int kTile = 256;                               // per pair, both ways
 constexpr int kHalf = 128;                               // per CTA
 constexpr int kRows = 64;                                // of a stage
-constexpr int kStages = 5;
+constexpr int kStages = 6;                               // of the copies
+constexpr int kSlots = 3;                                // of widened x
 constexpr uint32_t kBoxBytes = kRows * 128;              // 64 rows x 64 bf16 columns
 constexpr uint32_t kOperandBytes = 2 * kBoxBytes;        // of one stage and CTA: 128 columns
 constexpr uint32_t kCodeBytes = kRows * kHalf;
 constexpr uint32_t kSfBytes = 512;
 constexpr uint32_t kOffA = 0;
 constexpr uint32_t kOffB = kOffA + kStages * kOperandBytes;
-constexpr uint32_t kOffCodes = kOffB + kStages * kOperandBytes;
+constexpr uint32_t kOffCodes = kOffB + kSlots * kOperandBytes;
 constexpr uint32_t kOffSf = kOffCodes + kStages * kCodeBytes;
 constexpr uint32_t kOffBar = kOffSf + kStages * kSfBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;    // barriers + alignment slack
 constexpr uint32_t kTmemCols = 512;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 4;
-constexpr int kConvWarp0 = 8, kConvWarps = 8;
+// Warps of a group that widens every kSlots-th stage: a group for every slot, so that
+// each group waits for every use of its barriers in turn.  (Groups that take turns on a
+// stage do not: copies land out of order, and a parity cannot tell a use from the one two
+// back.)
+constexpr int kConvWarp0 = 8, kConvWarps = 4;
+constexpr int kPieces = kRows * kHalf / 8 / (kConvWarps * 32);    // 8-byte pieces of codes per thread and stage
+static_assert((kConvWarp0 + kConvWarps * kSlots) * 32 == kThreads, "warps");
+static_assert(kStages % kSlots == 0, "a group's stages are its own");
+static_assert(kPieces == 8 && kRows == 64, "a thread's rows are eight apart");
 constexpr uint16_t kBothCtas = 0x3;
 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kRows * kHalf / 16 == 2 * kConvWarps * 32, "two 16-byte pieces of codes per thread and stage");
 
 // Descriptor of an MN-major operand: 64-column boxes of kBoxBytes (leading byte
 // offset), inside a box groups of eight rows 1024 bytes apart (stride byte offset).
@@ -79,6 +88,20 @@ __device__ __forceinline__ void tc_mma_pair_bf16(uint32_t d_tmem, uint64_t a_des
         : "memory");
 }
 
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
     uint32_t d;
@@ -96,7 +119,7 @@ __device__ __forceinline__ WTile tile_of(const WgradParams &p, int tile)
 {
     const int per_group = p.num_n_blk * p.num_k_blk;
     const int g = tile / per_group;
-    const Tile t = tile_coord(tile - g * per_group, p.num_n_blk, p.num_k_blk, 16);
+    const Tile t = tile_coord(tile - g * per_group, p.num_n_blk, p.num_k_blk, 5);
     WTile w = {0, p.m, g, t.mb * kTile, t.nb * kTile};
     if (p.offsets != nullptr) {
         w.first = min(max(p.offsets[g], 0), p.m);
@@ -105,20 +128,82 @@ __device__ __forceinline__ WTile tile_of(const WgradParams &p, int tile)
     return w;
 }
 
-// Eight codes (two words) of a block with scale factors f1 (and f2, where a power
-// of two beyond bf16 is needed) as four bf16 pairs.  A code's exponent and mantissa
-// moved to bf16's places are its value times 2^-120 (the difference of the
-// exponent biases), subnormals included.
-__device__ __forceinline__ uint32_t widen2(uint32_t pair, uint32_t f1)
+// Four codes times a power of two as two bf16 pairs.  A code's exponent and mantissa
+// moved to bf16's places are its value times 2^-120 (the difference of the exponent
+// biases), subnormals included.
+__device__ __forceinline__ uint32_t widen2(uint32_t pair, uint32_t factor)
 {
-    return mul_bf16x2((pair & 0x80008000u) | ((pair >> 4) & 0x07F007F0u), f1);
+    return mul_bf16x2((pair & 0x80008000u) | ((pair >> 4) & 0x07F007F0u), factor);
 }
 
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t f1, uint32_t &lo, uint32_t &hi)
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &lo, uint32_t &hi)
 {
-    lo = widen2(__byte_perm(w, 0, 0x1404), f1);
-    hi = widen2(__byte_perm(w, 0, 0x3424), f1);
+    lo = widen2(__byte_perm(w, 0, 0x1404), factor);
+    hi = widen2(__byte_perm(w, 0, 0x3424), factor);
 }
+
+// 32 columns of a thread's row, the first `cols` of them, in whole 32-byte sectors where
+// the row allows it.
+__device__ __forceinline__ void store_row_f32(float *o, int cols, const uint32_t (&v)[32], bool accumulate)
+{
+    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = v[8 * i + j];
+        if (8 * i + 8 <= cols) {
+            uint4 *q = reinterpret_cast<uint4 *>(o + 8 * i);
+            if (accumulate) {
+                const uint4 a = q[0], b = q[1];
+                const uint32_t old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(old[j]));
+            }
+            if (sectors) {
+                st_global_v8(q, w);
+            } else {
+                q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (8 * i + j < cols) o[8 * i + j] = __uint_as_float(w[j]) + (accumulate ? o[8 * i + j] : 0.0f);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_row_bf16(uint16_t *o, int cols, const uint32_t (&v)[32])
+{
+    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = bf16x2_rn(__uint_as_float(v[16 * i + 2 * j]), __uint_as_float(v[16 * i + 2 * j + 1]));
+        if (16 * i + 16 <= cols && sectors) {
+            st_global_v8(o + 16 * i, w);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint16_t *q = o + 16 * i + 8 * h;
+                const int left = cols - 16 * i - 8 * h;
+                if (left >= 8) {
+                    *reinterpret_cast<uint4 *>(q) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < left) q[j] = (uint16_t)(w[4 * h + (j >> 1)] >> (16 * (j & 1)));
+                }
+            }
+        }
+    }
+}
+
+// Largest scale code whose factor 2^(code - 127 + 120) bf16 holds.
+constexpr uint32_t kOneFactor = 134;
 
 __global__ void __launch_bounds__(kThreads, 1)
     wgrad_pair_kernel(const __grid_constant__ CUtensorMap tmDy, const __grid_constant__ CUtensorMap tmCodes,
@@ -127,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);    // this CTA's copies of the stage landed
-    uint64_t *ready = full + kStages;                                  // (leader) both CTAs widened it
-    uint64_t *empty = ready + kStages;                                 // the pair's MMAs released it
+    uint64_t *ready = full + kStages;                                  // (leader) both CTAs widened into the slot
+    uint64_t *empty = ready + kSlots;                                  // the pair's MMAs released the stage and its slot
     uint64_t *tmem_full = empty + kStages;                             // [2] accumulator complete
     uint64_t *tmem_empty = tmem_full + 2;                              // [2] (leader) both CTAs drained it
     uint64_t *mma_done = tmem_empty + 2;
@@ -138,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&ready[s], 2 * kConvWarps);
             mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < kSlots; ++s) mbar_init(&ready[s], 2 * kConvWarps);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tmem_full[b], 1);
             mbar_init(&tmem_empty[b], 2 * kEpiWarps);
@@ -168,67 +253,84 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kConvWarp0) {
         // ------------------------------------------------------- widening --
-        const int tid = threadIdx.x - kConvWarp0 * 32;
-        const uint32_t leader_ready = mapa_shared(ready, 0);
-        const uint32_t a_base = smem_u32(smem + kOffA), b_base = smem_u32(smem + kOffB);
-        const uint32_t codes_base = smem_u32(smem + kOffCodes);
-        const int c16 = tid & 7;                         // 16-column piece of a row
-        // (lanes of columns 64 on take their two 16-byte stores the other way round, so
-        // that eight lanes hit eight different banks of four)
-        const int swap = c16 >> 2;
-        int stage = 0;
-        uint32_t phase = 0;
+        // A thread widens eight codes of each of its eight rows, eight rows apart: 16 lanes
+        // a row, so that both the 8-byte loads and the 16-byte stores hit every bank once,
+        // and rows that are alike modulo 8 have one place in the swizzle.
+        const int group = (warp - kConvWarp0) / kConvWarps;
+        const int row0 = ((warp - kConvWarp0) % kConvWarps) * 2 + (lane >> 4);
+        const int col8 = lane & 15;                      // 8-column piece
+        const uint32_t leader_ready = mapa_shared(&ready[group], 0);
+        const uint32_t in_codes = smem_u32(smem + kOffCodes) + row0 * kHalf + col8 * 8;
+        const uint32_t in_sf = smem_u32(smem + kOffSf) + row0 * 16 + (col8 >> 2);
+        const uint32_t a_row = smem_u32(smem + kOffA) + (col8 >> 3) * kBoxBytes + row0 * 128 + (col8 & 7) * 16;
+        const uint32_t out = smem_u32(smem + kOffB) + group * kOperandBytes + (col8 >> 3) * kBoxBytes + row0 * 128 +
+                             (((col8 & 7) ^ row0) << 4);
+        int next = group, stage = group;                 // the group's next stage, of the tile and of the ring
+        int before = -1;                                 // the stage whose MMAs read the slot last
+        uint32_t phase = 0, before_phase = 0;
         bool ok = true;
         for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
             const WTile t = tile_of(p, tile);
-            const int band_row = t.first & 127;
-            for (int r0 = 0; r0 < t.rows; r0 += kRows) {
+            const int num_ks = (t.rows + kRows - 1) / kRows;
+            for (; next < num_ks; next += kSlots) {
                 ok = __all_sync(~0u, mbar_wait(&full[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
                 if (!ok) break;
-                const int valid = t.rows - r0;
-                const uint8_t *sf = smem + kOffSf + stage * kSfBytes;
+                const uint32_t band_half = (uint32_t)next & 1u;
+                uint2 w[kPieces];
+                uint32_t code[kPieces], top = 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int row = (tid >> 3) + 32 * i;
-                    const int br = (band_row + r0 + row) & 127;
-                    const uint4 w = ld_shared_v4(codes_base + stage * kCodeBytes + row * kHalf + c16 * 16);
-                    const uint32_t code = sf[(br & 31) * 16 + (br >> 5) * 4 + (c16 >> 1)];
-                    // 2^(code - 127 + 120), the part past bf16's range as a second factor
-                    const uint32_t e = code + 120, e1 = min(e, 254u);
-                    const uint32_t f1 = code == 255 ? 0x7FC07FC0u : (e1 << 7) * 0x10001u;
-                    uint32_t v[8];
-                    widen4(w.x, f1, v[0], v[1]);
-                    widen4(w.y, f1, v[2], v[3]);
-                    widen4(w.z, f1, v[4], v[5]);
-                    widen4(w.w, f1, v[6], v[7]);
-                    if (__any_sync(~0u, e > e1)) {
-                        const uint32_t f2 = ((127 + e - e1) << 7) * 0x10001u;
+                for (int i = 0; i < kPieces; ++i) {
+                    w[i] = ld_shared_v2(in_codes + stage * kCodeBytes + i * 8 * kHalf);
+                    code[i] = ld_shared_u8(in_sf + stage * kSfBytes + band_half * 8 + (i & 3) * 128 + (i >> 2) * 4);
+                    top = max(top, code[i]);
+                }
+                if (before >= 0) {
+                    ok = __all_sync(~0u, mbar_wait(&empty[before], before_phase, p.err_flag, kErrTimeout, p.wait_ns));
+                    if (!ok) break;
+                }
+                if (!__any_sync(~0u, top > kOneFactor)) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = mul_bf16x2(v[j], f2);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const uint32_t f = code[i] * 0x00800080u + 120 * 0x00800080u;
+                        uint32_t v[4];
+                        widen4(w[i].x, f, v[0], v[1]);
+                        widen4(w[i].y, f, v[2], v[3]);
+                        st_shared_v4(out + i * 1024, v[0], v[1], v[2], v[3]);
                     }
-                    if (row >= valid)
+                } else {
+                    // the part of a factor past bf16's range as a second one, and NaN blocks
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) v[j] = 0;
-                    const uint32_t at = b_base + stage * kOperandBytes + (c16 >> 2) * kBoxBytes + row * 128;
-                    const int piece = (c16 & 3) * 2;
-                    const uint32_t first = at + (((piece + swap) ^ (row & 7)) << 4);
-                    const uint32_t second = at + (((piece + 1 - swap) ^ (row & 7)) << 4);
-                    st_shared_v4(first, swap ? v[4] : v[0], swap ? v[5] : v[1], swap ? v[6] : v[2], swap ? v[7] : v[3]);
-                    st_shared_v4(second, swap ? v[0] : v[4], swap ? v[1] : v[5], swap ? v[2] : v[6], swap ? v[3] : v[7]);
-                    if (row >= valid) {                  // dy's row: as many bytes, any order
-                        const uint32_t a = a_base + stage * kOperandBytes + (c16 >> 2) * kBoxBytes + row * 128 + (c16 & 3) * 32;
-                        st_shared_v4(a, 0, 0, 0, 0);
-                        st_shared_v4(a + 16, 0, 0, 0, 0);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const uint32_t c1 = min(code[i], kOneFactor);
+                        const uint32_t f1 = code[i] == 255 ? 0x7FC07FC0u : (c1 + 120) * 0x00800080u;
+                        const uint32_t f2 = (127 + code[i] - c1) * 0x00800080u;
+                        uint32_t v[4];
+                        widen4(w[i].x, f1, v[0], v[1]);
+                        widen4(w[i].y, f1, v[2], v[3]);
+                        st_shared_v4(out + i * 1024, mul_bf16x2(v[0], f2), mul_bf16x2(v[1], f2), mul_bf16x2(v[2], f2),
+                                     mul_bf16x2(v[3], f2));
                     }
                 }
+                const int valid = t.rows - next * kRows;
+                if (valid < kRows)                       // rows of nobody: zeros, in dy's boxes too
+#pragma unroll
+                    for (int i = 0; i < kPieces; ++i)
+                        if (row0 + 8 * i >= valid) {
+                            st_shared_v4(out + i * 1024, 0, 0, 0, 0);
+                            st_shared_v4(a_row + stage * kOperandBytes + i * 1024, 0, 0, 0, 0);
+                        }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    if (rank == 0) mbar_arrive(&ready[stage]);
-                    else mbar_arrive_remote(leader_ready + stage * (uint32_t)sizeof(uint64_t));
+                    if (rank == 0) mbar_arrive(&ready[group]);
+                    else mbar_arrive_remote(leader_ready);
                 }
-                if (++stage == kStages) { stage = 0; phase ^= 1; }
+                before = stage;
+                before_phase = phase;
+                stage += kSlots;
+                if (stage >= kStages) { stage -= kStages; phase ^= 1; }
             }
+            next -= num_ks;
         }
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------- epilogue --
@@ -259,43 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0;
                 }
-                if (n >= p.n) continue;
-                if (p.type == kTypeF32) {
-                    float *o = static_cast<float *>(p.dw) + row + c;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (c + 4 * i + 4 <= p.k) {
-                            float4 f = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                   __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-                            if (p.accumulate) {
-                                const float4 old = *reinterpret_cast<const float4 *>(o + 4 * i);
-                                f.x += old.x; f.y += old.y; f.z += old.z; f.w += old.w;
-                            }
-                            *reinterpret_cast<float4 *>(o + 4 * i) = f;
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (c + 4 * i + j < p.k)
-                                    o[4 * i + j] = __uint_as_float(v[4 * i + j]) + (p.accumulate ? o[4 * i + j] : 0.0f);
-                        }
-                    }
-                } else {
-                    uint16_t *o = static_cast<uint16_t *>(p.dw) + row + c;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = bf16x2_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-                        if (c + 8 * i + 8 <= p.k) {
-                            *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (c + 8 * i + j < p.k) o[8 * i + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-                        }
-                    }
+                if (n < p.n) {
+                    if (p.type == kTypeF32) store_row_f32(static_cast<float *>(p.dw) + row + c, p.k - c, v, p.accumulate);
+                    else store_row_bf16(static_cast<uint16_t *>(p.dw) + row + c, p.k - c, v);
                 }
+                __syncwarp();
             }
             if (t.rows > 0) {
                 tc_fence_before_sync();
@@ -342,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ MMA --
         const bool issuer = elect_one();
         const uint32_t a_base = smem_u32(smem + kOffA), b_base = smem_u32(smem + kOffB);
-        int stage = 0, buf = 0;
+        int stage = 0, slot = 0, buf = 0;
         uint32_t phase = 0, acc_phase[2] = {0, 0};
         bool ok = true;
         for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
@@ -352,19 +422,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after_sync();
             for (int r0 = 0; r0 < t.rows; r0 += kRows) {
-                ok = __all_sync(~0u, mbar_wait(&ready[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
+                ok = __all_sync(~0u, mbar_wait(&ready[slot], phase, p.err_flag, kErrTimeout, p.wait_ns));
                 if (!ok) break;
                 tc_fence_after_sync();
                 const int steps = min(kRows / 16, (t.rows - r0 + 15) / 16);
                 const uint64_t ad = desc_mn_sw128(a_base + stage * kOperandBytes);
-                const uint64_t bd = desc_mn_sw128(b_base + stage * kOperandBytes);
+                const uint64_t bd = desc_mn_sw128(b_base + slot * kOperandBytes);
                 if (issuer) {
                     for (int kk = 0; kk < steps; ++kk)   // 16 rows of 128 bytes
                         tc_mma_pair_bf16(tmem + buf * kTile, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), kIdesc,
                                          (r0 | kk) != 0);
                     tc_commit_pair_multicast(&empty[stage], kBothCtas);
                 }
-                if (++stage == kStages) { stage = 0; phase ^= 1; }
+                if (++stage == kStages) stage = 0;
+                if (++slot == kSlots) { slot = 0; phase ^= 1; }
             }
             if (!ok) break;
             if (issuer) tc_commit_pair_multicast(&tmem_full[buf], kBothCtas);
