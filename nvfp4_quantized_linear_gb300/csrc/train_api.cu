@@ -311,7 +311,7 @@ nvfp4_status nvfp4_checkpoint_wgrad(const void *dy_bf16, int64_t ldd, const uint
     cudaError_t e = nvfp4::device_error_word(&p.err_flag);
     if (e != cudaSuccess) return launch_status(e, "weight-gradient kernel (error word)");
     const char *why = nullptr;
-    e = nvfp4::launch_wgrad(p, static_cast<const uint16_t *>(dy_bf16), ldd, q, num_sms,
+    e = nvfp4::launch_wgrad(p, static_cast<const uint16_t *>(dy_bf16), ldd, q, workspace, num_sms,
                             reinterpret_cast<cudaStream_t>(stream), &why);
     if (why) return fail(NVFP4_ERR_CUDA, "%s", why);
     return launch_status(e, "weight-gradient kernel");

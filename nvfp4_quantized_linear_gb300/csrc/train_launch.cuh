@@ -58,17 +58,20 @@ struct WgradParams {
     int32_t sf_tiles;                        // 512-byte scale tiles per 128-row band
     const uint8_t *sf;
     const int32_t *offsets, *counts;         // groups' rows, or nullptr
-    int32_t num_groups;                      // >= 1 (1 without groups)
+    int32_t num_groups;                      // >= 1; without groups row ranges of `span` rows
+    int32_t span;
+    int32_t part_rows;                       // rows of one accumulator
     int32_t type, accumulate;
-    void *dw;
+    void *dw;                                // [num_groups][n][ldw], dw_cols columns
     int64_t ldw;
+    int32_t dw_cols;
     int32_t num_n_blk, num_k_blk;
     unsigned int *err_flag;                  // device error word (bounded waits)
     uint64_t wait_ns;
 };
 
-cudaError_t launch_wgrad(const WgradParams &p, const uint16_t *dy, int64_t ldd, const uint8_t *q, int num_sms,
-                         cudaStream_t s, const char **why);
+cudaError_t launch_wgrad(const WgradParams &p, const uint16_t *dy, int64_t ldd, const uint8_t *q, void *workspace,
+                         int num_sms, cudaStream_t s, const char **why);
 size_t wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int groups);
 
 }  // namespace nvfp4

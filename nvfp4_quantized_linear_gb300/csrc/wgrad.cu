@@ -10,21 +10,23 @@
 // lie in memory, 64 columns (128 bytes, 128-byte swizzle) a row.
 //
 // A tile is 256 (dy columns) x 256 (x columns); CTA r of the pair holds dy
-// columns [128r, +128) and x columns [128r, +128) of it, 64 rows a stage.  Twenty
+// columns [128r, +128) and x columns [128r, +128) of it, 64 rows a stage.  Twenty-four
 // warps per CTA:
 //   warp 0       copies: two 64 x 64 boxes of dy, 64 x 128 codes and the 512-byte
 //                scale tile of a stage
 //   warp 1       allocates TMEM; in the leader one lane issues the pair's MMAs
-//   warps 4..7   epilogue, one TMEM lane quarter each
-//   warps 8..19  three groups, each widening every third stage's codes to bf16 (a ring
+//   warps 4..11  epilogue, two per TMEM lane quarter
+//   warps 12..23 three groups, each widening every third stage's codes to bf16 (a ring
 //                of its own: three slots, six stages of copies) and clearing the rows
 //                past a group's last one in both operands (they may hold anything)
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the
 // next one's MMAs.
 #include <algorithm>
+#include <climits>
 
 #include <cuda_bf16.h>
 
+#include "block_launch.cuh"
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "ptx.cuh"
@@ -49,20 +51,27 @@ constexpr uint32_t kOffB = kOffA + kStages * kOperandBytes;
 constexpr uint32_t kOffCodes = kOffB + kSlots * kOperandBytes;
 constexpr uint32_t kOffSf = kOffCodes + kStages * kCodeBytes;
 constexpr uint32_t kOffBar = kOffSf + kStages * kSfBytes;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;    // barriers + alignment slack
+constexpr uint32_t kOffTable = kOffBar + 256;            // groups by size
+constexpr uint32_t kSmemBytes = kOffTable + 16 * kMoeMaxExperts + 1024;   // + alignment slack
 constexpr uint32_t kTmemCols = 512;
-constexpr int kThreads = 640;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 4;
+constexpr int kThreads = 768;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kEpiCols = 128;      // columns of a tile per warp
 // Warps of a group that widens every kSlots-th stage: a group for every slot, so that
 // each group waits for every use of its barriers in turn.  (Groups that take turns on a
 // stage do not: copies land out of order, and a parity cannot tell a use from the one two
 // back.)
-constexpr int kConvWarp0 = 8, kConvWarps = 4;
+constexpr int kConvWarp0 = 12, kConvWarps = 4;
 constexpr int kPieces = kRows * kHalf / 8 / (kConvWarps * 32);    // 8-byte pieces of codes per thread and stage
 static_assert((kConvWarp0 + kConvWarps * kSlots) * 32 == kThreads, "warps");
 static_assert(kStages % kSlots == 0, "a group's stages are its own");
 static_assert(kPieces == 8 && kRows == 64, "a thread's rows are eight apart");
 constexpr uint16_t kBothCtas = 0x3;
+
+// Rows of one sum on the tensor cores where dw is fp32: their accumulator is truncated, not
+// rounded, at every step of 16 rows, and falls short by about 4e-10 of itself per row (8192 rows:
+// 3.5e-6); further parts are added to dw in memory, rounded to nearest.  A bf16 dw is rounded to
+// 2^-9 anyway and takes all rows at once.
+constexpr int kPartRows = 2048, kAllRows = INT_MAX;
 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -115,17 +124,58 @@ struct WTile {
     int group, n0, k0;
 };
 
-__device__ __forceinline__ WTile tile_of(const WgradParams &p, int tile)
+// Tile number `at` of the walk; table: {group, first row, rows} of the groups by
+// descending size.
+__device__ __forceinline__ WTile tile_of(const WgradParams &p, int at, const int4 *table)
 {
     const int per_group = p.num_n_blk * p.num_k_blk;
-    const int g = tile / per_group;
-    const Tile t = tile_coord(tile - g * per_group, p.num_n_blk, p.num_k_blk, 5);
+    const int g = at / per_group;
+    const Tile t = tile_coord(at - g * per_group, p.num_n_blk, p.num_k_blk, 5);
     WTile w = {0, p.m, g, t.mb * kTile, t.nb * kTile};
     if (p.offsets != nullptr) {
-        w.first = min(max(p.offsets[g], 0), p.m);
-        w.rows = min(max(p.counts[g], 0), p.m - w.first);
+        const int4 e = table[g];
+        w.group = e.x;
+        w.first = e.y;
+        w.rows = e.z;
+    } else {                                             // a range of the rows
+        w.first = min(g * p.span, p.m);
+        w.rows = min(p.span, p.m - w.first);
     }
     return w;
+}
+
+// The tiles of a pair: rounds over the pairs, every other one backwards, so that with
+// the groups by descending size the pairs' shares of the rows are about even
+// (in plain turns the busiest pair of the routed case has 10 to 45 % more
+// rows than the mean one, this way 3 to 5 %).
+struct Walk {
+    int pair, pairs, tiles, round;
+    __device__ __forceinline__ int first() { round = 0; return pair; }
+    __device__ __forceinline__ int next()
+    {
+        ++round;
+        return round * pairs + (round & 1 ? pairs - 1 - pair : pair);
+    }
+};
+
+// The block's threads: the groups by size (equal ones by number) into the table.
+// `counts`: shared memory for num_groups (rounded up to 4) words.
+__device__ __forceinline__ void order_groups(const WgradParams &p, int4 *table, int32_t *counts)
+{
+    const int padded = (p.num_groups + 3) / 4 * 4;
+    for (int g = threadIdx.x; g < padded; g += kThreads) counts[g] = g < p.num_groups ? p.counts[g] : INT_MIN;
+    __syncthreads();
+    for (int g = threadIdx.x; g < p.num_groups; g += kThreads) {
+        const int mine = counts[g], first = min(max(p.offsets[g], 0), p.m);
+        int rank = 0;
+        for (int h = 0; h < padded; h += 4) {
+            const int4 c = *reinterpret_cast<const int4 *>(counts + h);
+            rank += (c.x > mine || (c.x == mine && h < g)) + (c.y > mine || (c.y == mine && h + 1 < g)) +
+                    (c.z > mine || (c.z == mine && h + 2 < g)) + (c.w > mine || (c.w == mine && h + 3 < g));
+        }
+        table[rank] = make_int4(g, first, min(max(mine, 0), p.m - first), 0);
+    }
+    __syncthreads();
 }
 
 // Four codes times a power of two as two bf16 pairs.  A code's exponent and mantissa
@@ -142,61 +192,112 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &lo
     hi = widen2(__byte_perm(w, 0, 0x3424), factor);
 }
 
-// 32 columns of a thread's row, the first `cols` of them, in whole 32-byte sectors where
-// the row allows it.
-__device__ __forceinline__ void store_row_f32(float *o, int cols, const uint32_t (&v)[32], bool accumulate)
+// Adds four floats to memory without waiting for them (rounded to nearest, subnormals
+// flushed).
+__device__ __forceinline__ void red_add_v4(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(__uint_as_float(a)), "f"(__uint_as_float(b)),
+                 "f"(__uint_as_float(c)), "f"(__uint_as_float(d))
+                 : "memory");
+}
+
+// Transposes units of kUnit words among groups of kWords / kUnit neighbouring lanes: lane j of a
+// group has its row's units before, and unit j of the group's rows after, row i's at v[i * kUnit].
+template <int kUnit, int kWords>
+__device__ __forceinline__ void transpose_units(uint32_t (&v)[kWords], int lane)
+{
+    constexpr int kLanes = kWords / kUnit;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t w[8];
+    for (int b = 1; b < kLanes; b <<= 1) {
+        const bool high = lane & b;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = v[8 * i + j];
-        if (8 * i + 8 <= cols) {
-            uint4 *q = reinterpret_cast<uint4 *>(o + 8 * i);
-            if (accumulate) {
-                const uint4 a = q[0], b = q[1];
-                const uint32_t old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        for (int i = 0; i < kLanes; ++i) {
+            if (i & b) continue;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) + __uint_as_float(old[j]));
+            for (int j = 0; j < kUnit; ++j) {
+                uint32_t &lo = v[i * kUnit + j], &hi = v[(i | b) * kUnit + j];
+                const uint32_t got = __shfl_xor_sync(~0u, high ? lo : hi, b);
+                if (high) lo = got;
+                else hi = got;
             }
-            if (sectors) {
-                st_global_v8(q, w);
-            } else {
-                q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (8 * i + j < cols) o[8 * i + j] = __uint_as_float(w[j]) + (accumulate ? o[8 * i + j] : 0.0f);
         }
     }
 }
 
-__device__ __forceinline__ void store_row_bf16(uint16_t *o, int cols, const uint32_t (&v)[32])
+// A warp's 32 rows x 32 whole columns (a row per lane; o: the first row, `ld` elements apart; `rows` of
+// them are there) to memory, neighbouring lanes side by side: whole 128-byte lines.  Stored
+// a row per lane, 32-byte sectors of another line each, 117 million fp32 took 105 us, so
+// 90; added that way, 8192 routed tokens' gradients took 250 us, so 190.
+__device__ __forceinline__ void store_rows_f32(float *o, int64_t ld, int rows, uint32_t (&v)[32], int lane)
+{
+    transpose_units<8>(v, lane);
+    o += (lane & ~3) * ld + (lane & 3) * 8;
+    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0 && (ld & 7) == 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i, o += ld) {
+        if ((lane & ~3) + i >= rows) continue;
+        if (sectors) {
+            st_global_v8(o, *reinterpret_cast<const uint32_t(*)[8]>(v + 8 * i));
+        } else {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+            *reinterpret_cast<uint4 *>(o + 4) = make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+        }
+    }
+}
+
+__device__ __forceinline__ void add_rows_f32(float *o, int64_t ld, int rows, uint32_t (&v)[32], int lane)
+{
+    transpose_units<4>(v, lane);
+    o += (lane & ~7) * ld + (lane & 7) * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i, o += ld)
+        if ((lane & ~7) + i < rows) red_add_v4(o, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// bf16: 64 bytes per lane, in whole sectors where the row allows it (two lanes
+// side by side instead: 67 us where this takes 63).
+__device__ __forceinline__ void store_row_bf16(uint16_t *o, const uint32_t (&v)[32])
 {
     const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i, o += 16) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             w[j] = bf16x2_rn(__uint_as_float(v[16 * i + 2 * j]), __uint_as_float(v[16 * i + 2 * j + 1]));
-        if (16 * i + 16 <= cols && sectors) {
-            st_global_v8(o + 16 * i, w);
+        if (sectors) {
+            st_global_v8(o, w);
+        } else {
+            *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+
+// The first `cols` (< 32) of 32 columns of one thread's row: where a row ends inside them.
+__device__ __forceinline__ void store_row_end(const WgradParams &p, int64_t at, int cols, const uint32_t (&v)[32], bool add)
+{
+    const bool f32 = p.type == kTypeF32;
+    float *o = static_cast<float *>(p.dw) + at;
+    uint16_t *h = static_cast<uint16_t *>(p.dw) + at;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        if (j >= cols) break;
+        if (j + 8 <= cols && !f32) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = bf16x2_rn(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
+            *reinterpret_cast<uint4 *>(h + j) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (j + 8 <= cols && !add) {
+            *reinterpret_cast<uint4 *>(o + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            *reinterpret_cast<uint4 *>(o + j + 4) = make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
         } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint16_t *q = o + 16 * i + 8 * h;
-                const int left = cols - 16 * i - 8 * h;
-                if (left >= 8) {
-                    *reinterpret_cast<uint4 *>(q) = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < left) q[j] = (uint16_t)(w[4 * h + (j >> 1)] >> (16 * (j & 1)));
-                }
+            for (int i = 0; i < 8; ++i) {
+                if (j + i >= cols) break;
+                if (f32) o[j + i] = __uint_as_float(v[j + i]) + (add ? o[j + i] : 0.0f);
+                else h[j + i] = (uint16_t)bf16_bits_rn(__uint_as_float(v[j + i]));
             }
         }
     }
@@ -218,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tmem_empty = tmem_full + 2;                              // [2] (leader) both CTAs drained it
     uint64_t *mma_done = tmem_empty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    int4 *const table = reinterpret_cast<int4 *>(smem + kOffTable);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -245,11 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     griddep_launch_dependents();
     griddep_wait();
+    if (p.offsets != nullptr) order_groups(p, table, reinterpret_cast<int32_t *>(smem + kOffB));   // (not in use yet)
 
     const uint32_t tmem = role_tmem(tmem_slot);
     const uint32_t rank = cluster_ctarank();
-    const int num_pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
-    const int num_tiles = p.num_groups * p.num_n_blk * p.num_k_blk;
+    Walk walk = {(int)(blockIdx.x >> 1), (int)(gridDim.x >> 1), p.num_groups * p.num_n_blk * p.num_k_blk, 0};
 
     if (warp >= kConvWarp0) {
         // ------------------------------------------------------- widening --
@@ -269,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int before = -1;                                 // the stage whose MMAs read the slot last
         uint32_t phase = 0, before_phase = 0;
         bool ok = true;
-        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
-            const WTile t = tile_of(p, tile);
+        for (int tile = walk.first(); tile < walk.tiles && ok; tile = walk.next()) {
+            const WTile t = tile_of(p, tile, table);
             const int num_ks = (t.rows + kRows - 1) / kRows;
             for (; next < num_ks; next += kSlots) {
                 ok = __all_sync(~0u, mbar_wait(&full[stage], phase, p.err_flag, kErrTimeout, p.wait_ns));
@@ -335,46 +437,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kEpiWarp0) {
         // ------------------------------------------------------- epilogue --
         const int q = warp & 3;
+        const int col0 = (warp - kEpiWarp0) / 4 * kEpiCols;
         const uint32_t leader_empty = mapa_shared(tmem_empty, 0);
         uint32_t phase[2] = {0, 0};
         int buf = 0;
-        for (int tile = pair; tile < num_tiles; tile += num_pairs) {
-            const WTile t = tile_of(p, tile);
-            if (t.rows > 0) {
-                if (!__all_sync(~0u, mbar_wait(&tmem_full[buf], phase[buf], p.err_flag, kErrTimeout, p.wait_ns))) break;
-                phase[buf] ^= 1;
-                tc_fence_after_sync();
-            } else if (p.accumulate) {
-                continue;
-            }
-            const int n = t.n0 + (int)rank * kHalf + q * 32 + lane;
-            const int64_t row = ((int64_t)t.group * p.n + n) * p.ldw;
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile;
-            for (int ch = 0; ch < kTile / 32; ++ch) {
-                const int c = t.k0 + ch * 32;
-                if (c >= p.k) break;
-                uint32_t v[32];
+        bool ok = true;
+        for (int tile = walk.first(); tile < walk.tiles && ok; tile = walk.next()) {
+            const WTile t = tile_of(p, tile, table);
+            if (t.rows == 0 && p.accumulate) continue;
+            const int n0 = t.n0 + (int)rank * kHalf + q * 32;
+            const int64_t plane = ((int64_t)t.group * p.n + n0) * p.ldw;
+            for (int r0 = 0; r0 == 0 || r0 < t.rows; r0 += p.part_rows) {
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile + col0;
                 if (t.rows > 0) {
-                    tmem_ld_32cols(acc + ch * 32, v);
-                    tmem_ld_wait_regs(v);
-                } else {
+                    ok = __all_sync(~0u, mbar_wait(&tmem_full[buf], phase[buf], p.err_flag, kErrTimeout, p.wait_ns));
+                    if (!ok) break;
+                    phase[buf] ^= 1;
+                    tc_fence_after_sync();
+                }
+                const bool add = p.accumulate || r0 > 0;
+#pragma unroll 1
+                for (int ch = 0; ch < kEpiCols / 32; ++ch) {
+                    const int c = t.k0 + col0 + ch * 32;
+                    if (c >= p.dw_cols || n0 >= p.n) break;
+                    uint32_t v[32];
+                    if (t.rows > 0) {
+                        tmem_ld_32cols(acc + ch * 32, v);
+                        tmem_ld_wait_regs(v);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0;
+                        for (int i = 0; i < 32; ++i) v[i] = 0;
+                    }
+                    const int rows = p.n - n0;
+                    const int64_t at = plane + c;
+                    if (c + 32 > p.dw_cols) {
+                        if (lane < rows) store_row_end(p, at + lane * p.ldw, p.dw_cols - c, v, add);
+                    } else if (p.type != kTypeF32) {
+                        if (lane < rows) store_row_bf16(static_cast<uint16_t *>(p.dw) + at + lane * p.ldw, v);
+                    } else if (add) {
+                        add_rows_f32(static_cast<float *>(p.dw) + at, p.ldw, rows, v, lane);
+                    } else {
+                        store_rows_f32(static_cast<float *>(p.dw) + at, p.ldw, rows, v, lane);
+                    }
+                    __syncwarp();
                 }
-                if (n < p.n) {
-                    if (p.type == kTypeF32) store_row_f32(static_cast<float *>(p.dw) + row + c, p.k - c, v, p.accumulate);
-                    else store_row_bf16(static_cast<uint16_t *>(p.dw) + row + c, p.k - c, v);
+                if (t.rows > 0) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(&tmem_empty[buf]);
+                        else mbar_arrive_remote(leader_empty + buf * (uint32_t)sizeof(uint64_t));
+                    }
+                    buf ^= 1;
                 }
-                __syncwarp();
-            }
-            if (t.rows > 0) {
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive(&tmem_empty[buf]);
-                    else mbar_arrive_remote(leader_empty + buf * (uint32_t)sizeof(uint64_t));
-                }
-                buf ^= 1;
             }
         }
     } else if (warp == 0 && lane == 0) {
@@ -383,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, issued = 0, issued_phase = 0;
         bool ok = true;
-        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
-            const WTile t = tile_of(p, tile);
+        for (int tile = walk.first(); tile < walk.tiles && ok; tile = walk.next()) {
+            const WTile t = tile_of(p, tile, table);
             const int n = t.n0 + (int)rank * kHalf, k = t.k0 + (int)rank * kHalf;
             const bool sf_here = k < p.sf_tiles * 128;
             for (int r0 = 0; r0 < t.rows; r0 += kRows) {
@@ -415,33 +530,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         int stage = 0, slot = 0, buf = 0;
         uint32_t phase = 0, acc_phase[2] = {0, 0};
         bool ok = true;
-        for (int tile = pair; tile < num_tiles && ok; tile += num_pairs) {
-            const WTile t = tile_of(p, tile);
-            if (t.rows == 0) continue;
-            ok = __all_sync(~0u, mbar_wait(&tmem_empty[buf], acc_phase[buf] ^ 1, p.err_flag, kErrTimeout, p.wait_ns));
-            if (!ok) break;
-            tc_fence_after_sync();
-            for (int r0 = 0; r0 < t.rows; r0 += kRows) {
-                ok = __all_sync(~0u, mbar_wait(&ready[slot], phase, p.err_flag, kErrTimeout, p.wait_ns));
+        for (int tile = walk.first(); tile < walk.tiles && ok; tile = walk.next()) {
+            const WTile t = tile_of(p, tile, table);
+            for (int part = 0; part < t.rows && ok; part += p.part_rows) {
+                ok = __all_sync(~0u, mbar_wait(&tmem_empty[buf], acc_phase[buf] ^ 1, p.err_flag, kErrTimeout, p.wait_ns));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int steps = min(kRows / 16, (t.rows - r0 + 15) / 16);
-                const uint64_t ad = desc_mn_sw128(a_base + stage * kOperandBytes);
-                const uint64_t bd = desc_mn_sw128(b_base + slot * kOperandBytes);
-                if (issuer) {
-                    for (int kk = 0; kk < steps; ++kk)   // 16 rows of 128 bytes
-                        tc_mma_pair_bf16(tmem + buf * kTile, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), kIdesc,
-                                         (r0 | kk) != 0);
-                    tc_commit_pair_multicast(&empty[stage], kBothCtas);
+                const int rows = min(p.part_rows, t.rows - part);
+                for (int r0 = 0; r0 < rows; r0 += kRows) {
+                    ok = __all_sync(~0u, mbar_wait(&ready[slot], phase, p.err_flag, kErrTimeout, p.wait_ns));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int steps = min(kRows / 16, (rows - r0 + 15) / 16);
+                    const uint64_t ad = desc_mn_sw128(a_base + stage * kOperandBytes);
+                    const uint64_t bd = desc_mn_sw128(b_base + slot * kOperandBytes);
+                    if (issuer) {
+                        for (int kk = 0; kk < steps; ++kk)   // 16 rows of 128 bytes
+                            tc_mma_pair_bf16(tmem + buf * kTile, ad + kk * (2048 >> 4), bd + kk * (2048 >> 4), kIdesc,
+                                             (r0 | kk) != 0);
+                        tc_commit_pair_multicast(&empty[stage], kBothCtas);
+                    }
+                    if (++stage == kStages) stage = 0;
+                    if (++slot == kSlots) { slot = 0; phase ^= 1; }
                 }
-                if (++stage == kStages) stage = 0;
-                if (++slot == kSlots) { slot = 0; phase ^= 1; }
+                if (!ok) break;
+                if (issuer) tc_commit_pair_multicast(&tmem_full[buf], kBothCtas);
+                __syncwarp();
+                acc_phase[buf] ^= 1;
+                buf ^= 1;
             }
-            if (!ok) break;
-            if (issuer) tc_commit_pair_multicast(&tmem_full[buf], kBothCtas);
-            __syncwarp();
-            acc_phase[buf] ^= 1;
-            buf ^= 1;
         }
         if (issuer) tc_commit_pair(mma_done);
         __syncwarp();
@@ -453,6 +570,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_all();                 // no peer access to this CTA's smem or TMEM after this point
     tc_fence_after_sync();
     if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// dw = (dw +) the ranges' sums, in their order; a thread takes eight columns.
+__global__ void __launch_bounds__(256) wgrad_sum_kernel(const WgradParams p, const float *parts, int splits, int64_t part, int cols)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t pieces = (int64_t)p.n * (cols / 8);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = i / (cols / 8);
+        const int c = (int)(i - row * (cols / 8)) * 8;
+        const float *src = parts + row * cols + c;
+        const int left = min(8, p.k - c);
+        float v[8] = {};
+        float *o32 = static_cast<float *>(p.dw) + row * p.ldw + c;
+        if (p.accumulate)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < left) v[j] = o32[j];
+        for (int s = 0; s < splits; ++s) {
+            const float4 a = *reinterpret_cast<const float4 *>(src + s * part);
+            const float4 b = *reinterpret_cast<const float4 *>(src + s * part + 4);
+            const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += u[j];
+        }
+        if (p.type == kTypeF32) {
+            if (left == 8) {
+                *reinterpret_cast<float4 *>(o32) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4 *>(o32 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < left) o32[j] = v[j];
+            }
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(p.dw) + row * p.ldw + c;
+            if (left == 8) {
+                *reinterpret_cast<uint4 *>(o) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]),
+                                                           bf16x2_rn(v[6], v[7]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < left) o[j] = (uint16_t)bf16_bits_rn(v[j]);
+            }
+        }
+    }
 }
 
 bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
@@ -470,14 +634,30 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint
 
 }  // namespace
 
-size_t wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int groups)
+namespace {
+
+// Row ranges of one weight of few tiles: as many as keep the pairs of a GPU of 152 SMs
+// busy in one round, of 512 rows at least.
+constexpr int kPairs = 76, kMinSpan = 512;
+
+int wgrad_splits(int64_t m, int64_t n, int64_t k)
 {
-    (void)m; (void)n; (void)k; (void)groups;
-    return 16;
+    const int64_t tiles = ((n + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({kPairs / tiles, 8, m / kMinSpan}));
 }
 
-cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ldd, const uint8_t *q, int num_sms,
-                         cudaStream_t s, const char **why)
+int64_t padded_cols(int64_t k) { return (k + 7) / 8 * 8; }
+
+}  // namespace
+
+size_t wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int groups)
+{
+    const int splits = groups > 0 ? 1 : wgrad_splits(m, n, k);
+    return splits > 1 ? (size_t)splits * n * padded_cols(k) * sizeof(float) : 0;
+}
+
+cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ldd, const uint8_t *q, void *workspace,
+                         int num_sms, cudaStream_t s, const char **why)
 {
     static int configured_device = -1;
     static int max_pairs = 0;
@@ -508,6 +688,18 @@ cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ld
     WgradParams p = p_in;
     p.num_n_blk = (p.n + kTile - 1) / kTile;
     p.num_k_blk = (p.k + kTile - 1) / kTile;
+    p.dw_cols = p.k;
+    p.span = p.m;
+    const int splits = p.offsets != nullptr ? 1 : wgrad_splits(p.m, p.n, p.k);
+    if (splits > 1) {                                    // fp32 sums of the ranges, added by a second kernel
+        p.span = ((p.m + splits - 1) / splits + 127) / 128 * 128;
+        p.num_groups = splits;
+        p.type = kTypeF32;
+        p.accumulate = 0;
+        p.dw = workspace;
+        p.ldw = p.dw_cols = (int32_t)padded_cols(p.k);
+    }
+    p.part_rows = p.type == kTypeF32 ? kPartRows : kAllRows;
     // (no rows: the maps are not read)
     const void *dy_base = p.m > 0 ? static_cast<const void *>(dy) : p.dw, *q_base = p.m > 0 ? q : p.dw;
     const uint64_t rows = p.m > 0 ? (uint64_t)p.m : 1;
@@ -534,7 +726,17 @@ cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ld
     cfg.stream = s;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, wgrad_pair_kernel, tmDy, tmCodes, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wgrad_pair_kernel, tmDy, tmCodes, p);
+    if (splits == 1 || e != cudaSuccess) return e;
+    const int cols = p.dw_cols;
+    const int64_t pieces = (int64_t)p.n * (cols / 8);
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>((pieces + 255) / 256, (int64_t)num_sms * 8));
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attrs + 1;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, wgrad_sum_kernel, p_in, static_cast<const float *>(workspace), splits,
+                              (int64_t)p.n * cols, cols);
 }
 
 }  // namespace nvfp4
