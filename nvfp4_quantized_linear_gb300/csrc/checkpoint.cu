@@ -2,9 +2,12 @@
 // is kept in MXFP8 for the backward pass, which reads
 //   dx = act'(x) dout   and   act(x) again, in MXFP8, for the next weight gradient.
 //
-// A thread owns 16 consecutive columns of x, half an MX block; 4 or 2 lanes make a
-// block of the activation.  Everything is one pass: bytes bound it.
+// One pass over memory, so bytes bound it; the arithmetic has to stay below them.  A warp
+// takes 512 columns of the rows r, r + 32, r + 64 and r + 96 of a 128-row band: a
+// thread 16 columns (half an MX block) of each, all four rows' loads in flight at once, and
+// the four rows' scale codes of 128 columns are one 16-byte line of the tiled layout.
 #include <algorithm>
+#include <climits>
 
 #include <cuda_bf16.h>
 
@@ -51,257 +54,370 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(const float *v)
+// Four E4M3 codes times a factor, as two pairs.
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float factor, uint64_t &a, uint64_t &b)
 {
-    return cvt_e4m3x2(v[1], v[0]) | (cvt_e4m3x2(v[3], v[2]) << 16);
+    uint32_t lo, hi;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    const uint64_t scale = pack2(factor, factor);
+    a = mul2(pack2(f.x, f.y), scale);
+    b = mul2(pack2(g.x, g.y), scale);
 }
 
-// Four E4M3 codes times a factor.
-__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float factor, float *v)
-{
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(w >> (16 * h))));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-        v[2 * h] = f.x * factor;
-        v[2 * h + 1] = f.y * factor;
-    }
-}
-
-// sigmoid(b (v + c v^3)) and its argument's derivative: b = 1, c = 0 for SILU,
-// b = 2 sqrt(2 / pi), c = 0.044715 for GELU (v sigmoid(2 u) = 0.5 v (1 + tanh u)).
-struct Act {
-    float b, bc, bc3;
-    bool sigmoid, relu;
+// The activation and its slope of a pair.  With u = b (v + c v^3) (b = 1, c = 0 for SILU,
+// b = 2 sqrt(2 / pi), c = 0.044715 for GELU) both are v sigmoid(u), with slope
+// s + v s (1 - s) u'.  The codes of act(v) sit 2^-4 apart, so an error of the value
+// shows as a share of codes on the wrong side of a threshold: e = 2^(-u log2 e) has its
+// argument split into a whole and a fraction (one rounding of 2^-25), 1 / (1 + e) a
+// Newton step.  v is clamped where e leaves the floats, beyond which s is 0 or 1 for
+// fp32.
+struct Slope {
+    uint64_t c1, c3;     // -log2(e) b and -log2(e) b c
+    uint64_t d1, d3;     // u' = d1 + d3 v^2
+    float limit;         // |u| <= 87
+    bool sigmoid, cubic, relu;
 };
 
-__device__ __forceinline__ Act act_of(int act)
+__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+
+__device__ __forceinline__ Slope slope_of(int act)
 {
     const bool gelu = act == kActGelu || act == kActGeglu;
-    Act a;
-    a.b = gelu ? 1.5957691216f : 1.0f;
-    a.bc = gelu ? 1.5957691216f * 0.044715f : 0.0f;
-    a.bc3 = 3.0f * a.bc;
+    const float b = gelu ? 1.5957691216f : 1.0f, c = gelu ? 0.044715f : 0.0f;
+    Slope a;
+    a.c1 = both(-1.44269504089f * b);
+    a.c3 = both(-1.44269504089f * b * c);
+    a.d1 = both(b);
+    a.d3 = both(3.0f * b * c);
+    a.limit = gelu ? 9.9f : 87.0f;
     a.relu = act == kActRelu;
     a.sigmoid = act != kActRelu && act != kActNone;
+    a.cubic = gelu;
     return a;
 }
 
-// act(v) and act'(v).
-__device__ __forceinline__ void apply(const Act &a, float v, float &f, float &df)
+__device__ __forceinline__ float clamp_to(float v, float limit) { return fminf(fmaxf(v, -limit), limit); }
+
+// f = act(v), df = act'(v).
+__device__ __forceinline__ void act_and_slope(const Slope &a, uint64_t v, uint64_t &f, uint64_t &df)
 {
-    if (a.sigmoid) {
-        const float vv = a.bc != 0.0f ? v * v : 0.0f;
-        const float u = v * fmaf(a.bc, vv, a.b), du = fmaf(a.bc3, vv, a.b);
-        const float e = expf(-fabsf(u));                 // sigmoid and 1 - sigmoid without cancellation
-        const float r = 1.0f / (1.0f + e), er = e * r;
-        const float s = u >= 0.0f ? r : er, t = u >= 0.0f ? er : r;
-        f = v * s;
-        df = s == 0.0f || t == 0.0f ? s : fmaf(f * t, du, s);
-    } else {
-        f = a.relu ? max_nan(v, 0.0f) : v;
-        df = a.relu && !(v > 0.0f) ? 0.0f * v : 1.0f;    // (NaN stays NaN)
+    float v0, v1;
+    unpack2(v, v0, v1);
+    if (!a.sigmoid) {
+        f = a.relu ? pack2(max_nan(v0, 0.0f), max_nan(v1, 0.0f)) : v;
+        // (NaN stays NaN)
+        df = a.relu ? pack2(v0 > 0.0f ? 1.0f : 0.0f * v0, v1 > 0.0f ? 1.0f : 0.0f * v1) : both(1.0f);
+        return;
     }
+    const uint64_t one = both(1.0f), minus = both(-1.0f), magic = both(0x1.8p23f);
+    const uint64_t w = pack2(clamp_to(v0, a.limit), clamp_to(v1, a.limit));
+    uint64_t c = a.c1, du = a.d1;
+    if (a.cubic) {
+        const uint64_t vv = mul2(w, w);
+        c = fma2(vv, a.c3, c);
+        du = fma2(vv, a.d3, du);
+    }
+    const uint64_t t = fma2(w, c, magic);                // the whole part in the low bits
+    const uint64_t frac = fma2(w, c, fma2(t, minus, magic));
+    float t0, t1, x0, x1, e0, e1, r0, r1;
+    unpack2(t, t0, t1);
+    unpack2(frac, x0, x1);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x1));
+    const uint64_t e = pack2(__int_as_float(__float_as_int(e0) + (__float_as_int(t0) << 23)),
+                             __int_as_float(__float_as_int(e1) + (__float_as_int(t1) << 23)));
+    const uint64_t d = add2(e, one);
+    unpack2(d, x0, x1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(x0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(x1));
+    const uint64_t r = pack2(r0, r1);
+    const uint64_t s = fma2(mul2(r, minus), fma2(d, r, minus), r);
+    f = mul2(pack2(fmaxf(v0, -a.limit), fmaxf(v1, -a.limit)), s);
+    df = fma2(mul2(mul2(w, s), mul2(e, s)), du, s);      // 1 - s = e s
+    if (v0 != v0 || v1 != v1) f = df = v;                // (minima and maxima drop a NaN; a block is NaN as a whole)
 }
 
-// Whether a row of the sorted rows holds a token (1), is padding of a group (0) or
-// lies behind the last group (-1).
-__device__ __forceinline__ int row_kind(const CheckpointParams &p, int row)
+// Real rows of a band, of the sorted rows of an expert layer: the group that holds it (its
+// rows start on a band) and how many of its rows are tokens; padding rows follow.  -1
+// behind the last group.  Two rounds of 32 lanes find the last group that starts at or
+// before the band.
+__device__ __forceinline__ int real_rows(const CheckpointParams &p, int band, int lane)
 {
-    if (p.offsets == nullptr) return 1;
-    int lo = 0, hi = p.num_groups;                       // the last group that starts at or before the row
-    if (row >= p.offsets[hi]) return -1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (p.offsets[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    return row - p.offsets[lo] < p.counts[lo] ? 1 : 0;
+    if (p.offsets == nullptr) return min(128, max(0, p.m - band * 128));
+    const int row = band * 128, step = (p.num_groups + 31) / 32;
+    const int end = p.offsets[p.num_groups];
+    const int coarse = lane * step < p.num_groups ? p.offsets[lane * step] : INT_MAX;
+    if (row >= end) return -1;
+    const int part = max(0, __popc(__ballot_sync(kFull, coarse <= row)) - 1) * step;
+    const int g = part + lane;
+    const int fine = lane < step && g < p.num_groups ? p.offsets[g] : INT_MAX;
+    const int found = part + max(0, __popc(__ballot_sync(kFull, fine <= row)) - 1);
+    return min(128, max(0, p.counts[found] - (row - p.offsets[found])));
 }
 
-// 16 (kGated: 8) bf16 from c on; columns past n are not written.
+// N values as bf16 from column c on; columns past n are not written.
 template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const float (&v)[N])
+__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const uint64_t (&v)[N / 2])
 {
     if (c >= n) return;
     uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16x2_of(v[i]);
+    uint16_t *o = row + c;
     if (c + N <= n) {
+        if constexpr (N == 16) {
+            if ((reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+                st_global_v8(o, w);
+                return;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < N / 8; ++i)
-            *reinterpret_cast<uint4 *>(row + c + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            if (c + i < n) row[c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+            if (c + i < n) o[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
-// N values of a thread (32 / N lanes a block) into codes and the block's scale byte.
+// N values of a thread (32 / N lanes a block) into codes; returns the block's scale code.
 template <int N>
-__device__ __forceinline__ void store_mxfp8(uint8_t *q, uint8_t *sf, int row, int c, int kp, int nbp, const float (&v)[N])
+__device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const uint64_t (&v)[N / 2], bool write)
 {
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) amax = max_abs3_nan(amax, v[i], v[i + 1]);
+    for (int i = 0; i < N / 2; ++i) {
+        float a, b;
+        unpack2(v[i], a, b);
+        amax = max_abs3_nan(amax, a, b);
+    }
 #pragma unroll
     for (int o = 1; o < 32 / N; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, o));
     const uint32_t code = mx8_code(amax);
     const float mul = __uint_as_float((254u - min(code, 253u)) << 23);   // 2^-s (a NaN block's codes mean nothing)
-    if (c < kp) {
+    if (write && c < kp) {
         uint32_t w[N / 4];
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            const float u[4] = {v[4 * i] * mul, v[4 * i + 1] * mul, v[4 * i + 2] * mul, v[4 * i + 3] * mul};
-            w[i] = e4m3x4(u);
+            float a, b, x, y;
+            unpack2(mul2(v[2 * i], both(mul)), a, b);
+            unpack2(mul2(v[2 * i + 1], both(mul)), x, y);
+            w[i] = cvt_e4m3x2(b, a) | (cvt_e4m3x2(y, x) << 16);
         }
-        uint8_t *o = q + (int64_t)row * kp + c;
-        if constexpr (N == 16) *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-        else *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+        if constexpr (N == 16) *reinterpret_cast<uint4 *>(q + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(q + c) = make_uint2(w[0], w[1]);
     }
-    if (c % 32 == 0 && c / 32 < nbp) sf[sf_offset(row, c / 32, nbp)] = c < kp ? (uint8_t)code : 0;
+    return c < kp ? code : 0;
 }
 
-// Rows and column steps of a block: blockIdx.x = row * steps + step.
-template <bool kGated>
-__global__ void __launch_bounds__(kThreads) act_checkpoint_kernel(const CheckpointParams p, int steps)
+// The four rows' scale codes of a lane's block, row j's in byte j, to the tiled layout: the
+// four blocks of 128 columns, kLanes lanes each, trade bytes, and one lane of each block
+// stores a row's word.  `rows`: bit j, row j's codes are written.
+template <int kLanes>
+__device__ __forceinline__ void store_scales(uint8_t *sf, int band, int r, int c, int nbp, uint32_t codes, unsigned rows)
 {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int row = blockIdx.x / steps;
-    const int c = ((blockIdx.x % steps) * kThreads + threadIdx.x) * 16;
-    const int kind = row < p.m ? row_kind(p, row) : 0;
-    if (row >= p.m ? p.offsets != nullptr : kind <= 0) return;
-    if (row >= p.m) {                                    // padding rows of the last scale band
-        if (c % 32 == 0 && c / 32 < p.nbp) p.sf[sf_offset(row, c / 32, p.nbp)] = 0;
-        return;
-    }
-    const Raw16 raw = load16_coherent(p.x + (int64_t)row * p.ldx, c, p.k);
-    float v[16];
-    unpack8(raw.a, *reinterpret_cast<float(*)[8]>(v));
-    unpack8(raw.b, *reinterpret_cast<float(*)[8]>(v + 8));
-    if (p.out != nullptr) {
-        const Act act = act_of(p.act);
-        uint16_t *out = p.out + (int64_t)row * p.ldo;
-        float f[kGated ? 8 : 16], df;
+    const int lane = threadIdx.x & 31, first = lane & ~(4 * kLanes - 1), j = (lane / kLanes) & 3;
+    uint32_t b[4];
 #pragma unroll
-        for (int i = 0; i < (kGated ? 8 : 16); ++i) {
-            apply(act, v[kGated ? 2 * i : i], f[i], df);
-            if (kGated) f[i] *= v[2 * i + 1];
-        }
-        store_bf16(out, kGated ? c / 2 : c, p.n_out, f);
-    }
-    store_mxfp8(p.q, p.sf, row, c, p.kp, p.nbp, v);
+    for (int i = 0; i < 4; ++i) b[i] = __shfl_sync(kFull, codes, first + i * kLanes);
+    // byte j of each
+    const uint32_t lo = __byte_perm(b[0], b[1], j | (4 + j) << 4), hi = __byte_perm(b[2], b[3], j | (4 + j) << 4);
+    if (lane % kLanes == 0 && c / 32 < nbp && ((rows >> j) & 1))
+        *reinterpret_cast<uint32_t *>(sf + ((int64_t)band * (nbp / 4) + c / 128) * 512 + r * 16 + j * 4) =
+            (lo & 0xFFFFu) | (hi << 16);
+}
+
+// blockIdx.x = (band * 4 + quarter of its 32 lines) * chunks + chunk; a warp takes a line.
+struct Place {
+    int band, r, c;                                      // the first row's line, the thread's first column
+};
+
+__device__ __forceinline__ Place place_of(int chunks)
+{
+    const unsigned unit = blockIdx.x / chunks;
+    return {(int)(unit >> 2), (int)(unit & 3) * 8 + (int)(threadIdx.x >> 5),
+            (int)(blockIdx.x % chunks) * 512 + (int)(threadIdx.x & 31) * 16};
 }
 
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads) act_checkpoint_backward_kernel(const CheckpointParams p, int steps)
+__global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const CheckpointParams p, int chunks)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int row = blockIdx.x / steps;
-    const int c = ((blockIdx.x % steps) * kThreads + threadIdx.x) * 16;
+    const Place at = place_of(chunks);
+    const int lane = threadIdx.x & 31, c = at.c;
+    const int real = real_rows(p, at.band, lane);
+    // (without groups the rows past m get zero scales: the last band's padding)
+    if (real <= at.r && p.offsets != nullptr) return;
+    Raw16 raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = (int64_t)at.band * 128 + at.r + 32 * j;
+        raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
+        if (at.r + 32 * j < real) raw[j] = load16_coherent(p.x + row * p.ldx, c, p.k);
+    }
+    const ActParams act = act_params(p.act);
+    uint32_t codes = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const bool here = at.r + 32 * j < real;          // (the same in the whole warp)
+        if (!here) continue;
+        const int64_t row = (int64_t)at.band * 128 + at.r + 32 * j;
+        const uint32_t w[8] = {raw[j].a.x, raw[j].a.y, raw[j].a.z, raw[j].a.w, raw[j].b.x, raw[j].b.y, raw[j].b.z, raw[j].b.w};
+        uint64_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bf16x2_to_f32x2(w[i]);
+        codes |= store_codes<16>(p.q + row * p.kp, c, p.kp, v, true) << (8 * j);
+        if (p.out != nullptr) {
+            uint16_t *out = p.out + row * p.ldo;
+            if constexpr (kGated) {
+                uint64_t o[4];
+                apply_gate(o, v, act);
+                store_bf16<8>(out, c / 2, p.n_out, o);
+            } else {
+                apply_act(v, act);
+                store_bf16<16>(out, c, p.n_out, v);
+            }
+        }
+    }
+    unsigned rows = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) rows |= (p.offsets == nullptr || at.r + 32 * j < real ? 1u : 0u) << j;
+    store_scales<2>(p.sf, at.band, at.r, c, p.nbp, codes, rows);
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const Place at = place_of(chunks);
+    const int lane = threadIdx.x & 31, c = at.c;
     constexpr int kN = kGated ? 8 : 16;
     const int oc = kGated ? c / 2 : c;                   // the first of the activation's columns
-    const int kind = row < p.m ? row_kind(p, row) : -1;
-    if (row >= p.m) {
-        if (p.offsets == nullptr && p.act_q != nullptr && oc % 32 == 0 && oc / 32 < p.act_nbp)
-            p.act_sf[sf_offset(row, oc / 32, p.act_nbp)] = 0;
-        return;
-    }
-    if (kind < 0) return;
-    if (kind == 0) {
-        const float zero[16] = {};
-        if (p.dx != nullptr) store_bf16(p.dx + (int64_t)row * p.ldg, c, p.k, zero);
-        return;
-    }
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float factor = 0.0f;
-    if (c < p.kp) {
-        w = ld_global_v4(p.q + (int64_t)row * p.kp + c);
-        factor = e8m0_value(p.sf[sf_offset(row, c / 32, p.nbp)]);
-    }
-    float v[16];
-    unpack_e4m3x4(w.x, factor, v);
-    unpack_e4m3x4(w.y, factor, v + 4);
-    unpack_e4m3x4(w.z, factor, v + 8);
-    unpack_e4m3x4(w.w, factor, v + 12);
-    float d[16] = {};
-    if (p.dx != nullptr) {
-        const uint16_t *dout = p.dout + (int64_t)row * p.ldd;
-        if constexpr (kGated) {
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (oc < p.n_out) r = first_of8(ld_global_v4(dout + oc), p.n_out - oc);
-            unpack8(r, *reinterpret_cast<float(*)[8]>(d));
-        } else {
-            const Raw16 r = load16_coherent(dout, oc, p.n_out);
-            unpack8(r.a, *reinterpret_cast<float(*)[8]>(d));
-            unpack8(r.b, *reinterpret_cast<float(*)[8]>(d + 8));
+    const int real = real_rows(p, at.band, lane);
+    if (real < 0) return;
+    const int64_t row0 = (int64_t)at.band * 128 + at.r;
+    uint4 q[4], line = make_uint4(0, 0, 0, 0);
+    Raw16 d[4];
+    if (c < p.kp && at.r < real)
+        line = ld_global_v4(p.sf + ((int64_t)at.band * (p.nbp / 4) + c / 128) * 512 + at.r * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        q[j] = d[j].a = d[j].b = make_uint4(0, 0, 0, 0);
+        if (at.r + 32 * j >= real) continue;
+        if (c < p.kp) q[j] = ld_global_v4(p.q + (row0 + 32 * j) * p.kp + c);
+        if (p.dx != nullptr) {
+            const uint16_t *dout = p.dout + (row0 + 32 * j) * p.ldd;
+            if constexpr (kGated) {
+                if (oc < p.n_out) d[j].a = first_of8(ld_global_v4(dout + oc), p.n_out - oc);
+            } else {
+                d[j] = load16_coherent(dout, oc, p.n_out);
+            }
         }
     }
-    const Act act = act_of(p.act);
-    float f[kN], g[16];
+    const Slope act = slope_of(p.act);
+    const uint32_t lines[4] = {line.x, line.y, line.z, line.w};
+    uint32_t codes = 0;
+    unsigned rows = 0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        float df;
+    for (int j = 0; j < 4; ++j) {
+        const int64_t row = row0 + 32 * j;
+        if (at.r + 32 * j >= real) {
+            if (p.offsets != nullptr && p.dx != nullptr) {   // padding rows of a group
+                const uint64_t zero[8] = {};
+                store_bf16<16>(p.dx + row * p.ldg, c, p.k, zero);
+            }
+            continue;
+        }
+        rows |= 1u << j;
+        const float factor = e8m0_value((lines[j] >> (c / 32 % 4 * 8)) & 255);
+        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        uint64_t v[8], f[8], df[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack_e4m3x4(w[i], factor, v[2 * i], v[2 * i + 1]);
+        uint64_t o[kN / 2];                              // act(x)
         if constexpr (kGated) {
-            apply(act, v[2 * i], f[i], df);
-            g[2 * i] = d[i] * v[2 * i + 1] * df;
-            g[2 * i + 1] = d[i] * f[i];
-            f[i] *= v[2 * i + 1];
+            uint64_t up[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float g0, u0, g1, u1;
+                unpack2(v[2 * i], g0, u0);
+                unpack2(v[2 * i + 1], g1, u1);
+                up[i] = pack2(u0, u1);
+                act_and_slope(act, pack2(g0, g1), f[i], df[i]);
+                o[i] = mul2(f[i], up[i]);
+            }
+            if (p.dx != nullptr) {
+                const uint32_t dw[4] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w};
+                uint64_t g[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t g2 = bf16x2_to_f32x2(dw[i]);
+                    float a0, a1, b0, b1;
+                    unpack2(mul2(mul2(g2, up[i]), df[i]), a0, a1);
+                    unpack2(mul2(g2, f[i]), b0, b1);
+                    g[2 * i] = pack2(a0, b0);
+                    g[2 * i + 1] = pack2(a1, b1);
+                }
+                store_bf16<16>(p.dx + row * p.ldg, c, p.k, g);
+            }
         } else {
-            apply(act, v[i], f[i], df);
-            g[i] = d[i] * df;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) act_and_slope(act, v[i], o[i], df[i]);
+            if (p.dx != nullptr) {
+                const uint32_t dw[8] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w, d[j].b.x, d[j].b.y, d[j].b.z, d[j].b.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) df[i] = mul2(bf16x2_to_f32x2(dw[i]), df[i]);
+                store_bf16<16>(p.dx + row * p.ldg, c, p.k, df);
+            }
+        }
+        if (p.act_q != nullptr) {
+            if (oc >= p.n_out)                           // (columns past n_out: zeros, whatever x's padding holds)
+#pragma unroll
+                for (int i = 0; i < kN / 2; ++i) o[i] = 0;
+            codes |= store_codes<kN>(p.act_q + row * p.act_kp, oc, p.act_kp, o, true) << (8 * j);
         }
     }
-    if (p.dx != nullptr) store_bf16(p.dx + (int64_t)row * p.ldg, c, p.k, g);
-    if (p.act_q != nullptr) {
-        if (oc >= p.n_out)                               // (columns past n_out: zeros, whatever x's padding holds)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) f[i] = 0.0f;
-        store_mxfp8(p.act_q, p.act_sf, row, oc, p.act_kp, p.act_nbp, f);
-    }
+    if (p.act_q != nullptr)
+        store_scales<32 / kN>(p.act_sf, at.band, at.r, oc, p.act_nbp, codes, p.offsets == nullptr ? 15u : rows);
 }
 
-cudaError_t launch_dependent(void (*kernel)(CheckpointParams, int), unsigned grid, cudaStream_t s, const CheckpointParams &p,
-                             int steps)
+cudaError_t launch_dependent(void (*kernel)(CheckpointParams, int), int64_t columns, cudaStream_t s, const CheckpointParams &p)
 {
+    const int chunks = (int)((columns + 511) / 512);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = dim3((unsigned)(rows_padded(p.m) / 128 * 4 * chunks), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, steps);
+    return cudaLaunchKernelEx(&cfg, kernel, p, chunks);
 }
-
-// Column steps of a row (padding columns of the scales included).
-int steps_of(int64_t columns) { return (int)((columns + 16 * kThreads - 1) / (16 * kThreads)); }
 
 }  // namespace
 
 cudaError_t launch_act_checkpoint(const CheckpointParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    const int steps = steps_of((int64_t)p.nbp * 32);
-    const int64_t rows = p.offsets != nullptr ? p.m : rows_padded(p.m);
     return launch_dependent(act_gated(p.act) ? act_checkpoint_kernel<true> : act_checkpoint_kernel<false>,
-                            (unsigned)(rows * steps), s, p, steps);
+                            (int64_t)p.nbp * 32, s, p);
 }
 
 cudaError_t launch_act_checkpoint_backward(const CheckpointParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    const int per = act_gated(p.act) ? 2 : 1;
-    const int steps = steps_of(std::max<int64_t>((int64_t)p.nbp * 32, (int64_t)p.act_nbp * 32 * per));
-    const int64_t rows = p.offsets != nullptr ? p.m : rows_padded(p.m);
-    return launch_dependent(per == 2 ? act_checkpoint_backward_kernel<true> : act_checkpoint_backward_kernel<false>,
-                            (unsigned)(rows * steps), s, p, steps);
+    const bool gated = act_gated(p.act);
+    // (padding columns of the activation's scales included)
+    return launch_dependent(gated ? act_checkpoint_backward_kernel<true> : act_checkpoint_backward_kernel<false>,
+                            std::max<int64_t>((int64_t)p.nbp * 32, (int64_t)p.act_nbp * 32 * (gated ? 2 : 1)), s, p);
 }
 
 }  // namespace nvfp4
