@@ -54,18 +54,32 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return d;
 }
 
-// Four E4M3 codes times a factor, as two pairs.
-__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float factor, uint64_t &a, uint64_t &b)
+// Four E4M3 codes times a factor, as two pairs: neighbours, or with kGated the even ones
+// (gates) and the odd ones (ups).
+template <bool kGated>
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, uint64_t factor, uint64_t &a, uint64_t &b)
 {
+    if constexpr (kGated) w = __byte_perm(w, 0, 0x3120);
     uint32_t lo, hi;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    const uint64_t scale = pack2(factor, factor);
-    a = mul2(pack2(f.x, f.y), scale);
-    b = mul2(pack2(g.x, g.y), scale);
+    a = mul2(pack2(f.x, f.y), factor);
+    b = mul2(pack2(g.x, g.y), factor);
 }
+
+__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Kinds of activation in the backward pass, gates by their own function.
+enum ActKind : int { kSilu, kGelu, kRest };
 
 // The activation and its slope of a pair.  With u = b (v + c v^3) (b = 1, c = 0 for SILU,
 // b = 2 sqrt(2 / pi), c = 0.044715 for GELU) both are v sigmoid(u), with slope
@@ -73,52 +87,27 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float factor, uint64_t
 // shows as a share of codes on the wrong side of a threshold: e = 2^(-u log2 e) has its
 // argument split into a whole and a fraction (one rounding of 2^-25), 1 / (1 + e) a
 // Newton step.  v is clamped where e leaves the floats, beyond which s is 0 or 1 for
-// fp32.
-struct Slope {
-    uint64_t c1, c3;     // -log2(e) b and -log2(e) b c
-    uint64_t d1, d3;     // u' = d1 + d3 v^2
-    float limit;         // |u| <= 87
-    bool sigmoid, cubic, relu;
-};
-
-__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
-
-__device__ __forceinline__ Slope slope_of(int act)
-{
-    const bool gelu = act == kActGelu || act == kActGeglu;
-    const float b = gelu ? 1.5957691216f : 1.0f, c = gelu ? 0.044715f : 0.0f;
-    Slope a;
-    a.c1 = both(-1.44269504089f * b);
-    a.c3 = both(-1.44269504089f * b * c);
-    a.d1 = both(b);
-    a.d3 = both(3.0f * b * c);
-    a.limit = gelu ? 9.9f : 87.0f;
-    a.relu = act == kActRelu;
-    a.sigmoid = act != kActRelu && act != kActNone;
-    a.cubic = gelu;
-    return a;
-}
-
-__device__ __forceinline__ float clamp_to(float v, float limit) { return fminf(fmaxf(v, -limit), limit); }
-
-// f = act(v), df = act'(v).
-__device__ __forceinline__ void act_and_slope(const Slope &a, uint64_t v, uint64_t &f, uint64_t &df)
+// fp32.  (Every minimum and maximum keeps a NaN.)
+template <int kKind>
+__device__ __forceinline__ void act_and_slope(uint64_t v, bool relu, uint64_t &f, uint64_t &df)
 {
     float v0, v1;
     unpack2(v, v0, v1);
-    if (!a.sigmoid) {
-        f = a.relu ? pack2(max_nan(v0, 0.0f), max_nan(v1, 0.0f)) : v;
-        // (NaN stays NaN)
-        df = a.relu ? pack2(v0 > 0.0f ? 1.0f : 0.0f * v0, v1 > 0.0f ? 1.0f : 0.0f * v1) : both(1.0f);
+    if constexpr (kKind == kRest) {
+        f = relu ? pack2(max_nan(v0, 0.0f), max_nan(v1, 0.0f)) : v;
+        df = relu ? pack2(v0 > 0.0f ? 1.0f : 0.0f * v0, v1 > 0.0f ? 1.0f : 0.0f * v1) : both(1.0f);
         return;
     }
+    constexpr float kLog2e = 1.44269504089f, kB = kKind == kGelu ? 1.5957691216f : 1.0f, kC = 0.044715f;
+    constexpr float kLimit = kKind == kGelu ? 9.9f : 87.0f;       // |u| < 87.1 there
     const uint64_t one = both(1.0f), minus = both(-1.0f), magic = both(0x1.8p23f);
-    const uint64_t w = pack2(clamp_to(v0, a.limit), clamp_to(v1, a.limit));
-    uint64_t c = a.c1, du = a.d1;
-    if (a.cubic) {
-        const uint64_t vv = mul2(w, w);
-        c = fma2(vv, a.c3, c);
-        du = fma2(vv, a.d3, du);
+    v0 = max_nan(v0, -kLimit);
+    v1 = max_nan(v1, -kLimit);
+    const uint64_t low = pack2(v0, v1), w = pack2(min_nan(v0, kLimit), min_nan(v1, kLimit));
+    uint64_t c = both(-kLog2e * kB), vv = 0;
+    if constexpr (kKind == kGelu) {
+        vv = mul2(w, w);
+        c = fma2(vv, both(-kLog2e * kB * kC), c);
     }
     const uint64_t t = fma2(w, c, magic);                // the whole part in the low bits
     const uint64_t frac = fma2(w, c, fma2(t, minus, magic));
@@ -135,9 +124,10 @@ __device__ __forceinline__ void act_and_slope(const Slope &a, uint64_t v, uint64
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(x1));
     const uint64_t r = pack2(r0, r1);
     const uint64_t s = fma2(mul2(r, minus), fma2(d, r, minus), r);
-    f = mul2(pack2(fmaxf(v0, -a.limit), fmaxf(v1, -a.limit)), s);
-    df = fma2(mul2(mul2(w, s), mul2(e, s)), du, s);      // 1 - s = e s
-    if (v0 != v0 || v1 != v1) f = df = v;                // (minima and maxima drop a NaN; a block is NaN as a whole)
+    f = mul2(low, s);
+    const uint64_t bend = mul2(mul2(w, s), mul2(e, s));  // v s (1 - s), 1 - s = e s
+    if constexpr (kKind == kGelu) df = fma2(bend, fma2(vv, both(3.0f * kB * kC), both(kB)), s);
+    else df = fma2(bend, one, s);
 }
 
 // Real rows of a band, of the sorted rows of an expert layer: the group that holds it (its
@@ -158,35 +148,40 @@ __device__ __forceinline__ int real_rows(const CheckpointParams &p, int band, in
     return min(128, max(0, p.counts[found] - (row - p.offsets[found])));
 }
 
-// N values as bf16 from column c on; columns past n are not written.
+// 2 N bf16 (two to a word) from column c on; columns past n are not written.
 template <int N>
-__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const uint64_t (&v)[N / 2])
+__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const uint32_t (&w)[N])
 {
-    if (c >= n) return;
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = bf16x2_of(v[i]);
     uint16_t *o = row + c;
-    if (c + N <= n) {
-        if constexpr (N == 16) {
+    if (c + 2 * N <= n) {
+        if constexpr (N == 8) {
             if ((reinterpret_cast<uintptr_t>(o) & 31) == 0) {
                 st_global_v8(o, w);
                 return;
             }
         }
 #pragma unroll
-        for (int i = 0; i < N / 8; ++i)
+        for (int i = 0; i < N / 4; ++i)
             *reinterpret_cast<uint4 *>(o + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+        for (int i = 0; i < 2 * N; ++i)
             if (c + i < n) o[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const uint64_t (&v)[N])
+{
+    uint32_t w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = bf16x2_of(v[i]);
+    store_bf16(row, c, n, w);
+}
+
 // N values of a thread (32 / N lanes a block) into codes; returns the block's scale code.
 template <int N>
-__device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const uint64_t (&v)[N / 2], bool write)
+__device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const uint64_t (&v)[N / 2])
 {
     float amax = 0.0f;
 #pragma unroll
@@ -199,7 +194,7 @@ __device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const
     for (int o = 1; o < 32 / N; o <<= 1) amax = max_nan(amax, __shfl_xor_sync(kFull, amax, o));
     const uint32_t code = mx8_code(amax);
     const float mul = __uint_as_float((254u - min(code, 253u)) << 23);   // 2^-s (a NaN block's codes mean nothing)
-    if (write && c < kp) {
+    if (c < kp) {
         uint32_t w[N / 4];
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
@@ -271,16 +266,16 @@ __global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const Check
         uint64_t v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = bf16x2_to_f32x2(w[i]);
-        codes |= store_codes<16>(p.q + row * p.kp, c, p.kp, v, true) << (8 * j);
+        codes |= store_codes<16>(p.q + row * p.kp, c, p.kp, v) << (8 * j);
         if (p.out != nullptr) {
             uint16_t *out = p.out + row * p.ldo;
             if constexpr (kGated) {
                 uint64_t o[4];
                 apply_gate(o, v, act);
-                store_bf16<8>(out, c / 2, p.n_out, o);
+                store_bf16(out, c / 2, p.n_out, o);
             } else {
                 apply_act(v, act);
-                store_bf16<16>(out, c, p.n_out, v);
+                store_bf16(out, c, p.n_out, v);
             }
         }
     }
@@ -290,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const Check
     store_scales<2>(p.sf, at.band, at.r, c, p.nbp, codes, rows);
 }
 
-template <bool kGated>
+template <bool kGated, int kKind>
 __global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks)
 {
     griddep_launch_dependents();
@@ -314,13 +309,15 @@ __global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backw
         if (p.dx != nullptr) {
             const uint16_t *dout = p.dout + (row0 + 32 * j) * p.ldd;
             if constexpr (kGated) {
-                if (oc < p.n_out) d[j].a = first_of8(ld_global_v4(dout + oc), p.n_out - oc);
+                if (oc < p.n_out) d[j].a = ld_global_v4(dout + oc);
+                if (oc + 8 > p.n_out) d[j].a = first_of8(d[j].a, p.n_out - oc);
             } else {
                 d[j] = load16_coherent(dout, oc, p.n_out);
             }
         }
     }
-    const Slope act = slope_of(p.act);
+    const bool relu = p.act == kActRelu;
+    const int shift = c / 32 % 4 * 8;
     const uint32_t lines[4] = {line.x, line.y, line.z, line.w};
     uint32_t codes = 0;
     unsigned rows = 0;
@@ -329,58 +326,52 @@ __global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backw
         const int64_t row = row0 + 32 * j;
         if (at.r + 32 * j >= real) {
             if (p.offsets != nullptr && p.dx != nullptr) {   // padding rows of a group
-                const uint64_t zero[8] = {};
-                store_bf16<16>(p.dx + row * p.ldg, c, p.k, zero);
+                const uint32_t zero[8] = {};
+                store_bf16(p.dx + row * p.ldg, c, p.k, zero);
             }
             continue;
         }
         rows |= 1u << j;
-        const float factor = e8m0_value((lines[j] >> (c / 32 % 4 * 8)) & 255);
+        const uint64_t factor = both(e8m0_value((lines[j] >> shift) & 255));
         const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-        uint64_t v[8], f[8], df[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack_e4m3x4(w[i], factor, v[2 * i], v[2 * i + 1]);
         uint64_t o[kN / 2];                              // act(x)
         if constexpr (kGated) {
-            uint64_t up[4];
+            const uint32_t dw[4] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w};
+            uint32_t g[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float g0, u0, g1, u1;
-                unpack2(v[2 * i], g0, u0);
-                unpack2(v[2 * i + 1], g1, u1);
-                up[i] = pack2(u0, u1);
-                act_and_slope(act, pack2(g0, g1), f[i], df[i]);
-                o[i] = mul2(f[i], up[i]);
+                uint64_t gate, up, f, df;
+                unpack_e4m3x4<true>(w[i], factor, gate, up);
+                act_and_slope<kKind>(gate, relu, f, df);
+                o[i] = mul2(f, up);
+                const uint64_t g2 = bf16x2_to_f32x2(dw[i]);
+                float a0, a1, b0, b1;
+                unpack2(mul2(mul2(g2, up), df), a0, a1);
+                unpack2(mul2(g2, f), b0, b1);
+                g[2 * i] = bf16x2_rn(a0, b0);
+                g[2 * i + 1] = bf16x2_rn(a1, b1);
             }
-            if (p.dx != nullptr) {
-                const uint32_t dw[4] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w};
-                uint64_t g[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint64_t g2 = bf16x2_to_f32x2(dw[i]);
-                    float a0, a1, b0, b1;
-                    unpack2(mul2(mul2(g2, up[i]), df[i]), a0, a1);
-                    unpack2(mul2(g2, f[i]), b0, b1);
-                    g[2 * i] = pack2(a0, b0);
-                    g[2 * i + 1] = pack2(a1, b1);
-                }
-                store_bf16<16>(p.dx + row * p.ldg, c, p.k, g);
-            }
+            if (p.dx != nullptr) store_bf16(p.dx + row * p.ldg, c, p.k, g);
         } else {
+            const uint32_t dw[8] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w, d[j].b.x, d[j].b.y, d[j].b.z, d[j].b.w};
+            uint32_t g[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) act_and_slope(act, v[i], o[i], df[i]);
-            if (p.dx != nullptr) {
-                const uint32_t dw[8] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w, d[j].b.x, d[j].b.y, d[j].b.z, d[j].b.w};
+            for (int i = 0; i < 4; ++i) {
+                uint64_t v[2], df[2];
+                unpack_e4m3x4<false>(w[i], factor, v[0], v[1]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) df[i] = mul2(bf16x2_to_f32x2(dw[i]), df[i]);
-                store_bf16<16>(p.dx + row * p.ldg, c, p.k, df);
+                for (int h = 0; h < 2; ++h) {
+                    act_and_slope<kKind>(v[h], relu, o[2 * i + h], df[h]);
+                    g[2 * i + h] = bf16x2_of(mul2(bf16x2_to_f32x2(dw[2 * i + h]), df[h]));
+                }
             }
+            if (p.dx != nullptr) store_bf16(p.dx + row * p.ldg, c, p.k, g);
         }
         if (p.act_q != nullptr) {
             if (oc >= p.n_out)                           // (columns past n_out: zeros, whatever x's padding holds)
 #pragma unroll
                 for (int i = 0; i < kN / 2; ++i) o[i] = 0;
-            codes |= store_codes<kN>(p.act_q + row * p.act_kp, oc, p.act_kp, o, true) << (8 * j);
+            codes |= store_codes<kN>(p.act_q + row * p.act_kp, oc, p.act_kp, o) << (8 * j);
         }
     }
     if (p.act_q != nullptr)
@@ -416,7 +407,12 @@ cudaError_t launch_act_checkpoint_backward(const CheckpointParams &p, int num_sm
     (void)num_sms;
     const bool gated = act_gated(p.act);
     // (padding columns of the activation's scales included)
-    return launch_dependent(gated ? act_checkpoint_backward_kernel<true> : act_checkpoint_backward_kernel<false>,
+    void (*kernel)(CheckpointParams, int) = p.act == kActSwiglu  ? act_checkpoint_backward_kernel<true, kSilu>
+                                            : p.act == kActGeglu ? act_checkpoint_backward_kernel<true, kGelu>
+                                            : p.act == kActSilu  ? act_checkpoint_backward_kernel<false, kSilu>
+                                            : p.act == kActGelu  ? act_checkpoint_backward_kernel<false, kGelu>
+                                                                 : act_checkpoint_backward_kernel<false, kRest>;
+    return launch_dependent(kernel,
                             std::max<int64_t>((int64_t)p.nbp * 32, (int64_t)p.act_nbp * 32 * (gated ? 2 : 1)), s, p);
 }
 
