@@ -61,8 +61,12 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, uint64_t factor, uint6
 {
     if constexpr (kGated) w = __byte_perm(w, 0, 0x3120);
     uint32_t lo, hi;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((uint16_t)w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((uint16_t)(w >> 16)));
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
     const float2 g = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     a = mul2(pack2(f.x, f.y), factor);
@@ -179,6 +183,19 @@ __device__ __forceinline__ void store_bf16(uint16_t *row, int c, int n, const ui
     store_bf16(row, c, n, w);
 }
 
+// Four fp32 to E4M3 (nearest even, saturating), the first in the lowest byte.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
 // N values of a thread (32 / N lanes a block) into codes; returns the block's scale code.
 template <int N>
 __device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const uint64_t (&v)[N / 2])
@@ -201,7 +218,7 @@ __device__ __forceinline__ uint32_t store_codes(uint8_t *q, int c, int kp, const
             float a, b, x, y;
             unpack2(mul2(v[2 * i], both(mul)), a, b);
             unpack2(mul2(v[2 * i + 1], both(mul)), x, y);
-            w[i] = cvt_e4m3x2(b, a) | (cvt_e4m3x2(y, x) << 16);
+            w[i] = e4m3x4(a, b, x, y);
         }
         if constexpr (N == 16) *reinterpret_cast<uint4 *>(q + c) = make_uint4(w[0], w[1], w[2], w[3]);
         else *reinterpret_cast<uint2 *>(q + c) = make_uint2(w[0], w[1]);
@@ -285,59 +302,60 @@ __global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const Check
     store_scales<2>(p.sf, at.band, at.r, c, p.nbp, codes, rows);
 }
 
-template <bool kGated, int kKind>
-__global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks)
+// The gradient and the activation of a warp's line.  kWhole: its 512 columns are all there,
+// dx rows are on 32-byte boundaries and both outputs wanted, so that nothing is left to
+// check per row (43 instructions an element with the checks; a third of them checks and
+// addresses).
+template <bool kGated, int kKind, bool kWhole>
+__device__ __forceinline__ void backward_line(const CheckpointParams &p, const Place &at, int real)
 {
-    griddep_launch_dependents();
-    griddep_wait();
-    const Place at = place_of(chunks);
-    const int lane = threadIdx.x & 31, c = at.c;
     constexpr int kN = kGated ? 8 : 16;
-    const int oc = kGated ? c / 2 : c;                   // the first of the activation's columns
-    const int real = real_rows(p, at.band, lane);
-    if (real < 0) return;
+    const int c = at.c, oc = kGated ? c / 2 : c;         // the first of the activation's columns
     const int64_t row0 = (int64_t)at.band * 128 + at.r;
-    uint4 q[4], line = make_uint4(0, 0, 0, 0);
-    Raw16 d[4];
-    if (c < p.kp && at.r < real)
+    uint4 line = make_uint4(0, 0, 0, 0);
+    if ((kWhole || c < p.kp) && at.r < real)
         line = ld_global_v4(p.sf + ((int64_t)at.band * (p.nbp / 4) + c / 128) * 512 + at.r * 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        q[j] = d[j].a = d[j].b = make_uint4(0, 0, 0, 0);
-        if (at.r + 32 * j >= real) continue;
-        if (c < p.kp) q[j] = ld_global_v4(p.q + (row0 + 32 * j) * p.kp + c);
-        if (p.dx != nullptr) {
-            const uint16_t *dout = p.dout + (row0 + 32 * j) * p.ldd;
-            if constexpr (kGated) {
-                if (oc < p.n_out) d[j].a = ld_global_v4(dout + oc);
-                if (oc + 8 > p.n_out) d[j].a = first_of8(d[j].a, p.n_out - oc);
-            } else {
-                d[j] = load16_coherent(dout, oc, p.n_out);
-            }
-        }
-    }
-    const bool relu = p.act == kActRelu;
-    const int shift = c / 32 % 4 * 8;
-    const uint32_t lines[4] = {line.x, line.y, line.z, line.w};
+    const uint8_t *q = p.q + row0 * p.kp + c;
+    const uint16_t *dout = p.dout + row0 * p.ldd;
+    uint16_t *dx = p.dx + row0 * p.ldg;
+    uint8_t *act_q = p.act_q + row0 * p.act_kp;
+    const bool relu = p.act == kActRelu, with_dx = kWhole || p.dx != nullptr, with_act = kWhole || p.act_q != nullptr;
+    // this lane's block of the four: its byte of each row's word, row j's to byte j
+    const uint32_t shift = c / 32 % 4, pick = shift | (4 + shift) << 4;
+    const uint32_t scales = (__byte_perm(line.x, line.y, pick) & 0xFFFFu) | __byte_perm(line.z, line.w, pick) << 16;
     uint32_t codes = 0;
     unsigned rows = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = row0 + 32 * j;
+    for (int j = 0; j < 4; ++j, q += 32 * (int64_t)p.kp, dout += 32 * p.ldd, dx += 32 * p.ldg, act_q += 32 * (int64_t)p.act_kp) {
         if (at.r + 32 * j >= real) {
-            if (p.offsets != nullptr && p.dx != nullptr) {   // padding rows of a group
+            if (p.offsets != nullptr && with_dx) {       // padding rows of a group
                 const uint32_t zero[8] = {};
-                store_bf16(p.dx + row * p.ldg, c, p.k, zero);
+                if constexpr (kWhole) st_global_v8(dx + c, zero);
+                else store_bf16(dx, c, p.k, zero);
             }
             continue;
         }
         rows |= 1u << j;
-        const uint64_t factor = both(e8m0_value((lines[j] >> shift) & 255));
-        const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        uint4 qw = make_uint4(0, 0, 0, 0);
+        Raw16 d = {qw, qw};
+        if (kWhole || c < p.kp) qw = ld_global_v4(q);
+        if constexpr (kWhole) {
+            d.a = ld_global_v4(dout + oc);
+            if constexpr (!kGated) d.b = ld_global_v4(dout + oc + 8);
+        } else if (with_dx) {
+            if constexpr (kGated) {
+                if (oc < p.n_out) d.a = ld_global_v4(dout + oc);
+                if (oc + 8 > p.n_out) d.a = first_of8(d.a, p.n_out - oc);
+            } else {
+                d = load16_coherent(dout, oc, p.n_out);
+            }
+        }
+        const uint64_t factor = both(e8m0_value((scales >> (8 * j)) & 255));
+        const uint32_t w[4] = {qw.x, qw.y, qw.z, qw.w};
         uint64_t o[kN / 2];                              // act(x)
+        uint32_t g[8];
         if constexpr (kGated) {
-            const uint32_t dw[4] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w};
-            uint32_t g[8];
+            const uint32_t dw[4] = {d.a.x, d.a.y, d.a.z, d.a.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint64_t gate, up, f, df;
@@ -351,10 +369,8 @@ __global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backw
                 g[2 * i] = bf16x2_rn(a0, b0);
                 g[2 * i + 1] = bf16x2_rn(a1, b1);
             }
-            if (p.dx != nullptr) store_bf16(p.dx + row * p.ldg, c, p.k, g);
         } else {
-            const uint32_t dw[8] = {d[j].a.x, d[j].a.y, d[j].a.z, d[j].a.w, d[j].b.x, d[j].b.y, d[j].b.z, d[j].b.w};
-            uint32_t g[8];
+            const uint32_t dw[8] = {d.a.x, d.a.y, d.a.z, d.a.w, d.b.x, d.b.y, d.b.z, d.b.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint64_t v[2], df[2];
@@ -365,17 +381,32 @@ __global__ void __launch_bounds__(kThreads, kGated ? 3 : 2) act_checkpoint_backw
                     g[2 * i + h] = bf16x2_of(mul2(bf16x2_to_f32x2(dw[2 * i + h]), df[h]));
                 }
             }
-            if (p.dx != nullptr) store_bf16(p.dx + row * p.ldg, c, p.k, g);
         }
-        if (p.act_q != nullptr) {
-            if (oc >= p.n_out)                           // (columns past n_out: zeros, whatever x's padding holds)
+        if constexpr (kWhole) st_global_v8(dx + c, g);
+        else if (with_dx) store_bf16(dx, c, p.k, g);
+        if (with_act) {
+            if (!kWhole && oc >= p.n_out)                // (columns past n_out: zeros, whatever x's padding holds)
 #pragma unroll
                 for (int i = 0; i < kN / 2; ++i) o[i] = 0;
-            codes |= store_codes<kN>(p.act_q + row * p.act_kp, oc, p.act_kp, o) << (8 * j);
+            codes |= store_codes<kN>(act_q, oc, kWhole ? INT_MAX : p.act_kp, o) << (8 * j);
         }
     }
-    if (p.act_q != nullptr)
-        store_scales<32 / kN>(p.act_sf, at.band, at.r, oc, p.act_nbp, codes, p.offsets == nullptr ? 15u : rows);
+    if (with_act) store_scales<32 / kN>(p.act_sf, at.band, at.r, oc, p.act_nbp, codes, p.offsets == nullptr ? 15u : rows);
+}
+
+template <bool kGated, int kKind>
+__global__ void __launch_bounds__(kThreads, kGated ? 6 : 4) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const Place at = place_of(chunks);
+    const int real = real_rows(p, at.band, threadIdx.x & 31);
+    if (real < 0) return;
+    const int end = (at.c & ~511) + 512;                 // of the warp's columns
+    const bool whole = end <= p.k && p.dx != nullptr && p.act_q != nullptr &&
+                       (reinterpret_cast<uintptr_t>(p.dx) & 31) == 0 && (p.ldg & 15) == 0;
+    if (whole) backward_line<kGated, kKind, true>(p, at, real);
+    else backward_line<kGated, kKind, false>(p, at, real);
 }
 
 cudaError_t launch_dependent(void (*kernel)(CheckpointParams, int), int64_t columns, cudaStream_t s, const CheckpointParams &p)
