@@ -5,8 +5,7 @@
 //   the topk highest keys among the best groups of experts,
 //   weight = scale * s, or scale * s / sum of the chosen s.
 //
-// A warp takes a token; lane i of it owns experts i, i + 32, ... (coalesced rows of
-// any alignment).
+// A warp takes a token.
 #include <algorithm>
 #include <cfloat>
 
@@ -28,6 +27,34 @@ __device__ __forceinline__ float value_of(uint16_t bits) { return __uint_as_floa
 __device__ __forceinline__ void store_value(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_value(uint16_t *p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
+// V values side by side (aligned as load_row's).
+template <int V, typename T>
+__device__ __forceinline__ void store_vector(T *o, const float (&v)[V])
+{
+    constexpr int kBytes = V * (int)sizeof(T), kWords = kBytes >= 4 ? kBytes / 4 : 1;
+    uint32_t w[kWords];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = __float_as_uint(v[i]);
+    } else if constexpr (V >= 2) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+    } else {
+        w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    }
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+            reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if constexpr (kBytes == 8) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    } else if constexpr (kBytes == 4) {
+        *reinterpret_cast<uint32_t *>(o) = w[0];
+    } else {
+        *reinterpret_cast<uint16_t *>(o) = (uint16_t)w[0];
+    }
+}
+
 // A logit as the choice sees it: -inf for NaN, +inf as the largest float.
 __device__ __forceinline__ float clean(float l) { return l > kNegInf ? fminf(l, FLT_MAX) : kNegInf; }
 
@@ -38,13 +65,16 @@ __device__ __forceinline__ uint32_t ordered(float f)
     return f > kNegInf ? (uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000)) : 0u;
 }
 
+__device__ __forceinline__ float unordered(uint32_t o)
+{
+    return o == 0u ? kNegInf : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
 __device__ __forceinline__ uint64_t ordered(double f)
 {
     const int64_t u = __double_as_longlong(f + 0.0);
     return f > (double)kNegInf ? (uint64_t)(u ^ ((u >> 63) | (int64_t)0x8000000000000000ll)) : 0ull;
 }
-
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
 
 __device__ __forceinline__ uint64_t warp_max(uint64_t v)
 {
@@ -108,29 +138,30 @@ __device__ __forceinline__ Scores<F> scores_of(const RouteParams &p, const float
 // the sum with the bias.
 constexpr float kRelSigmoid = 1.5f * 0x1p-22f, kRelSoftmax = 0x1p-20f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
 
-// The choice with keys of type F: pick[j] = lane + 32 j's expert, -1 for none.
-// False if two keys (or groups) whose order matters are too near each other for
-// fp32.  s_key: `experts` F of the warp, for groups.
-template <int V, typename T, typename F>
-__device__ __forceinline__ bool choose(const RouteParams &p, const T *row, const float (&l)[V], F *s_key, int lane,
-                                       int (&pick)[2])
+// ------------------------------------------------------------ exact choice ----
+// Keys in 64 bits, lane i owning experts i, i + 32, ...: the tokens (one in a few hundred
+// to thousands) whose order the fast choice below cannot be sure of.  pick[j]: the expert of
+// slot lane + 32 j, -1 for none.  s_key: `experts` doubles of the warp, for groups.
+template <int V, typename T>
+__device__ __noinline__ void choose_exactly(const RouteParams &p, const T *row, double *s_key, int lane, int (&pick)[2])
 {
     const bool by_logit = p.bias == nullptr;
-    const bool group_scores = p.groups > 1 && p.group_top == 2;
-    Scores<F> score = {false, F(0), F(1)};
-    if (!by_logit || group_scores) score = scores_of<V, F>(p, l);
-    const float rel = p.score == kScoreSoftmax ? kRelSoftmax : kRelSigmoid;
-    F key[V];
+    float l[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = lane + 32 * v < p.experts ? clean(value_of(row[lane + 32 * v])) : kNegInf;
+    Scores<double> score = {false, 0.0, 1.0};
+    if (!by_logit || (p.groups > 1 && p.group_top == 2)) score = scores_of<V, double>(p, l);
+    const double none = (double)kNegInf;
+    double key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        key[v] = F(l[v]);
+        key[v] = (double)l[v];
         const int i = lane + 32 * v;
         if (!by_logit && i < p.experts) {
             const float b = p.bias[i];
-            key[v] = l[v] > kNegInf && b > kNegInf ? score(F(l[v])) + F(b) : F(kNegInf);
+            key[v] = l[v] > kNegInf && b > kNegInf ? score((double)l[v]) + (double)b : none;
         }
     }
-    bool sure = true;
     if (p.groups > 1) {
         const int size = p.experts / p.groups;
         __syncwarp();
@@ -138,79 +169,42 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const T *row, const
         for (int v = 0; v < V; ++v)
             if (lane + 32 * v < p.experts) s_key[lane + 32 * v] = key[v];
         __syncwarp();
-        F top1 = F(kNegInf), top2 = F(kNegInf);
+        double top1 = none, top2 = none;
         if (lane < p.groups)
             for (int i = 0; i < size; ++i) {
-                const F k = s_key[lane * size + i];
+                const double k = s_key[lane * size + i];
                 top2 = k > top1 ? top1 : k > top2 ? k : top2;
                 top1 = k > top1 ? k : top1;
             }
-        F value = top1;
-        if (p.group_top == 2 && top1 > F(kNegInf)) {
-            if (by_logit) value = score(top1) + (top2 > F(kNegInf) ? score(top2) : F(0));
-            else if (top2 > F(kNegInf)) value = top1 + top2;
+        double value = top1;
+        if (p.group_top == 2 && top1 > none) {
+            if (by_logit) value = score(top1) + (top2 > none ? score(top2) : 0.0);
+            else if (top2 > none) value = top1 + top2;
         }
         int rank = 0;
         for (int g = 0; g < p.groups; ++g) {
-            const F other = __shfl_sync(kAll, value, g);
+            const double other = __shfl_sync(kAll, value, g);
             rank += other > value || (other == value && g < lane) ? 1 : 0;
         }
-        const bool kept = lane < p.groups && rank < p.topk_groups;
-        const unsigned mask = __ballot_sync(kAll, kept);
-        if (sizeof(F) == 4 && (!by_logit || p.group_top == 2)) {
-            // the lowest group that stays and the highest that does not
-            const float v = (float)value;
-            float low = kept ? v : INFINITY, high = lane < p.groups && !kept ? v : kNegInf;
-            low = -warp_max(-low);
-            high = warp_max(high);
-            // (a score is at most 1; two of them and three roundings)
-            const float tol = 4.0f * rel + 2.0f * kAbs + 3.0f * kRound * (fabsf(low) + fabsf(high));
-            if (high > kNegInf && !(low - high > tol)) sure = false;
-        }
+        const unsigned mask = __ballot_sync(kAll, lane < p.groups && rank < p.topk_groups);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (!((mask >> ((lane + 32 * v) / size & 31)) & 1)) key[v] = F(kNegInf);
+            if (!((mask >> ((lane + 32 * v) / size & 31)) & 1)) key[v] = none;
     }
-    using K = decltype(ordered(F(0)));
-    K k[V], best = 0;
+    uint64_t k[V], best = 0;
     int at = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         k[v] = ordered(key[v]);
         if (k[v] > best) { best = k[v]; at = v; }
     }
-    const bool check = sizeof(F) == 4 && !by_logit;
-    const int rounds = p.topk + (check && p.topk < p.experts ? 1 : 0);
     pick[0] = pick[1] = -1;
-    float last = 0.0f, last_l = 0.0f, last_b = 0.0f;
-    for (int r = 0; r < rounds; ++r) {
-        const K m = warp_max(best);
+    for (int r = 0; r < p.topk; ++r) {
+        const uint64_t m = warp_max(best);
         if (m == 0) break;
         const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)(lane + 32 * at) : kAll);
-        const bool mine = lane == (i & 31);
-        if (check) {
-            // this pick and the one before it; experts of one logit and one bias are
-            // equal in any precision (but not the first that is left out: others of
-            // its key may be behind it)
-            const float b = p.bias[i], li = clean(value_of(row[i]));
-            float kf = 0.0f;
-            if (mine)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v == at) kf = (float)key[v];
-            kf = __shfl_sync(kAll, kf, i & 31);
-            if (r > 0) {
-                const float s = fmaxf(last - last_b, 0.0f) + fmaxf(kf - b, 0.0f);
-                const float tol = rel * s + 2.0f * kAbs + 2.0f * kRound * (fabsf(last) + fabsf(kf));
-                const bool same = r < p.topk && li == last_l && b == last_b;
-                if (!same && !(last - kf > tol)) sure = false;
-            }
-            last = kf;
-            last_l = li;
-            last_b = b;
-        }
-        if (r < p.topk && lane == (r & 31)) pick[r >> 5] = i;
-        if (mine) {
+        if (lane == (r & 31)) pick[r >> 5] = i;
+        if (lane == (i & 31)) {
             best = 0;
             const int gone = at;
 #pragma unroll
@@ -220,11 +214,262 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const T *row, const
             }
         }
     }
-    return sure;
+}
+
+// ------------------------------------------------------------- fast choice ----
+
+// The experts [lane * V, lane * V + V) of a row, in vectors where `vec` (rows and V elements on
+// boundaries of up to 16 bytes, experts a multiple of V).
+template <int V, typename T>
+__device__ __forceinline__ void load_row(const T *row, int lane, int experts, bool vec, float (&l)[V])
+{
+    constexpr int kBytes = V * (int)sizeof(T);
+    const int first = lane * V;
+    if (vec) {
+        constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+        if (first < experts) {
+            if constexpr (kBytes >= 16) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 16; ++i) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(row + first + i * (16 / (int)sizeof(T)));
+                    w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+                }
+            } else if constexpr (kBytes == 8) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(row + first);
+                w[0] = q.x; w[1] = q.y;
+            } else if constexpr (kBytes == 4) {
+                w[0] = *reinterpret_cast<const uint32_t *>(row + first);
+            } else {
+                w[0] = *reinterpret_cast<const uint16_t *>(row + first);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f;
+            if constexpr (sizeof(T) == 4) f = __uint_as_float(w[v]);
+            else f = __uint_as_float(v & 1 ? w[v / 2] & 0xFFFF0000u : w[v / 2] << 16);
+            l[v] = first < experts ? clean(f) : kNegInf;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = first + v < experts ? clean(value_of(row[first + v])) : kNegInf;
+    }
+}
+
+// Descending order of V keys (Batcher's odd-even merge sort).
+template <int V>
+__device__ __forceinline__ void sort_descending(uint32_t (&k)[V])
+{
+#pragma unroll
+    for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t a = k[i + j], b = k[i + j + q];
+                        k[i + j] = max(a, b);
+                        k[i + j + q] = min(a, b);
+                    }
+}
+
+__device__ __forceinline__ float key_of(const RouteParams &p, const Scores<float> &score, float l, float b)
+{
+    return l > kNegInf && b > kNegInf ? score(l) + b : kNegInf;
+}
+
+// The two best of a group's keys, over the lanes of an aligned group of `lanes` lanes.
+struct Top2 {
+    float a, b;
+    __device__ __forceinline__ void add(float k)
+    {
+        b = fmaxf(b, fminf(a, k));
+        a = fmaxf(a, k);
+    }
+};
+
+// The choice with fp32 keys, lane i owning the V experts from i V on.  A key and its expert
+// are one word: the key's upper bits in the order of the floats, then the complement of
+// the expert, so that one maximum over the warp finds a pick, ties going to the lower
+// expert.  s_key: `experts` floats of the warp, for groups.  Each lane's words are sorted once, and a pick takes its lane's first one off.
+// What the lower bits of the keys would have decided shows between neighbours in the
+// order: false if two of them (or two groups) are too near each other for fp32, or
+// sorted by the upper bits alone against their keys.
+template <int V, typename T>
+__device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, const float (&l)[V],
+                                            const Scores<float> &score, float *s_key, int lane, int (&pick)[2],
+                                            float (&at)[2])
+{
+    constexpr uint32_t kMask = 32 * V - 1;
+    const bool by_logit = p.bias == nullptr;
+    const float rel = p.score == kScoreSoftmax ? kRelSoftmax : kRelSigmoid;
+    float key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = l[v];
+    if (!by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v < p.experts) key[v] = key_of(p, score, l[v], p.bias[lane * V + v]);
+    }
+    bool sure = true;
+    if (p.groups > 1) {
+        const int size = p.experts / p.groups, lanes = size / V;
+        // groups of whole lanes, a power of two of them: by shuffles; others through shared memory, a
+        // group per lane.  `mine`: the lane's group, `at0`: where group g's value stands, g * at0.
+        const bool whole = lanes * V == size && (lanes & (lanes - 1)) == 0;
+        Top2 top = {kNegInf, kNegInf};
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) top.add(key[v]);
+            for (int o = 1; o < lanes; o <<= 1) {
+                const float a = __shfl_xor_sync(kAll, top.a, o), b = __shfl_xor_sync(kAll, top.b, o);
+                top.b = fmaxf(fminf(top.a, a), fmaxf(top.b, b));
+                top.a = fmaxf(top.a, a);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (lane * V + v < p.experts) s_key[lane * V + v] = key[v];
+            __syncwarp();
+            if (lane < p.groups)
+                for (int i = 0; i < size; ++i) top.add(s_key[lane * size + i]);
+            __syncwarp();
+        }
+        const int mine = whole ? lane / lanes : lane, at0 = whole ? lanes : 1;
+        float value = top.a;
+        if (p.group_top == 2 && top.a > kNegInf) {
+            if (by_logit) value = score(top.a) + (top.b > kNegInf ? score(top.b) : 0.0f);
+            else if (top.b > kNegInf) value = top.a + top.b;
+        }
+        int rank = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const float other = __shfl_sync(kAll, value, g * at0);
+            rank += other > value || (other == value && g < mine) ? 1 : 0;
+        }
+        const bool here = mine < p.groups, kept = here && rank < p.topk_groups;
+        if (!by_logit || p.group_top == 2) {
+            // the lowest group that stays and the highest that does not
+            float low = kept ? value : INFINITY, high = here && !kept ? value : kNegInf;
+            low = -warp_max(-low);
+            high = warp_max(high);
+            // (a score is at most 1; two of them and three roundings)
+            const float tol = 4.0f * rel + 2.0f * kAbs + 3.0f * kRound * (fabsf(low) + fabsf(high));
+            if (high > kNegInf && !(low - high > tol)) sure = false;
+        }
+        if (whole) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (!kept) key[v] = kNegInf;
+        } else {
+            const unsigned mask = __ballot_sync(kAll, kept);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (!((mask >> ((lane * V + v) / size & 31)) & 1)) key[v] = kNegInf;
+        }
+    }
+    uint32_t k[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint32_t o = ordered(key[v]);
+        k[v] = o != 0 ? (o & ~kMask) | (kMask - (uint32_t)(lane * V + v)) : 0u;
+    }
+    sort_descending<V>(k);
+    // a bf16 logit's bits are all among the upper ones
+    const bool exact = by_logit && sizeof(T) == 2;
+    uint32_t mine[2] = {0, 0};
+    const int rounds = exact ? p.topk : p.topk + 1;
+    for (int r = 0; r < rounds; ++r) {
+        const uint32_t m = __reduce_max_sync(kAll, k[0]);
+        if (r < 32) mine[0] = lane == r ? m : mine[0];
+        else mine[1] = lane == r - 32 ? m : mine[1];
+        if (k[0] == m) {
+#pragma unroll
+            for (int v = 0; v + 1 < V; ++v) k[v] = k[v + 1];
+            k[V - 1] = 0;
+        }
+    }
+    float b[2] = {0.0f, 0.0f}, kf[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = mine[j] != 0 ? (int)(kMask - (mine[j] & kMask)) : -1;
+        at[j] = i >= 0 ? clean(value_of(row[i])) : kNegInf;
+        if (!by_logit && i >= 0) b[j] = p.bias[i];
+        kf[j] = by_logit ? at[j] : key_of(p, score, at[j], b[j]);
+        pick[j] = lane + 32 * j < p.topk ? i : -1;
+        if (p.topk < 32) break;                          // (one slot a lane, the first one left out among them)
+    }
+    if (p.topk < 32) {
+        pick[1] = -1;
+        at[1] = kNegInf;
+    }
+    if (exact) return sure;
+    if (p.topk >= 64) return false;
+    // of those left, none may share the upper bits of the first one left out
+    const uint32_t out_first = p.topk < 32 ? __shfl_sync(kAll, mine[0], p.topk) : __shfl_sync(kAll, mine[1], p.topk - 32);
+    const uint32_t out_second = __reduce_max_sync(kAll, k[0]);
+    if (out_first != 0 && ((out_first ^ out_second) & ~kMask) == 0) sure = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (j == 1 && p.topk < 32) break;
+        uint32_t next = __shfl_down_sync(kAll, mine[j], 1);
+        float next_at = __shfl_down_sync(kAll, at[j], 1), next_b = __shfl_down_sync(kAll, b[j], 1);
+        float next_kf = __shfl_down_sync(kAll, kf[j], 1);
+        if (j == 0 && p.topk >= 32) {
+            const uint32_t n1 = __shfl_sync(kAll, mine[1], 0);
+            const float a1 = __shfl_sync(kAll, at[1], 0), b1 = __shfl_sync(kAll, b[1], 0), k1 = __shfl_sync(kAll, kf[1], 0);
+            if (lane == 31) { next = n1; next_at = a1; next_b = b1; next_kf = k1; }
+        }
+        const int slot = lane + 32 * j;
+        if (slot < p.topk && next != 0) {
+            if (by_logit) {
+                if (!(at[j] >= next_at)) sure = false;
+            } else {
+                // experts of one logit and one bias are equal in any precision
+                const bool same = slot + 1 < p.topk && at[j] == next_at && b[j] == next_b;
+                const float s = fmaxf(kf[j] - b[j], 0.0f) + fmaxf(next_kf - next_b, 0.0f);
+                const float tol = rel * s + 2.0f * kAbs + 2.0f * kRound * (fabsf(kf[j]) + fabsf(next_kf));
+                if (!same && !(kf[j] - next_kf > tol)) sure = false;
+            }
+        }
+    }
+    return __all_sync(kAll, sure);
+}
+
+// Lanes that hold the first topk slots, as a power of two (32 for more).
+__device__ __forceinline__ int slot_lanes(int topk) { return topk <= 8 ? 8 : 32; }
+
+__device__ __forceinline__ float slots_sum(float v, int lanes)
+{
+    for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// Unnormalised shares of the picks, with their largest logit taken out: a softmax over
+// them, or s / e^min(max, 0) for the sigmoid, neither of which underflows in all.
+__device__ __forceinline__ void shares(bool softmax, const int (&pick)[2], const float (&at)[2], int topk, float (&u)[2])
+{
+    const float top = unordered(__reduce_max_sync(kAll, max(ordered(at[0]), topk > 32 ? ordered(at[1]) : 0u)));
+    const float m = softmax ? top : fminf(top, 0.0f);
+    u[1] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (j == 1 && topk <= 32) break;
+        if (pick[j] < 0) u[j] = 0.0f;
+        else if (softmax) u[j] = expf(at[j] - m);
+        else u[j] = at[j] > 0.0f ? 1.0f / (1.0f + expf(-at[j])) : expf(at[j] - m) / (1.0f + expf(at[j]));
+    }
+    const float sum = slots_sum(u[0] + u[1], slot_lanes(topk));
+    u[0] = pick[0] >= 0 ? u[0] / sum : 0.0f;
+    if (topk > 32) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
 }
 
 template <int V, typename T>
-__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParams p)
+__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParams p, bool vec)
 {
     extern __shared__ double s_keys[];
     griddep_launch_dependents();
@@ -234,37 +479,26 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
     if (t >= p.tokens) return;
     const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
     float l[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = lane + 32 * v < p.experts ? clean(value_of(row[lane + 32 * v])) : kNegInf;
+    load_row<V, T>(row, lane, p.experts, vec, l);
+    const bool softmax = p.score == kScoreSoftmax;
+    Scores<float> score = {softmax, 0.0f, 1.0f};
+    if (softmax && (!p.renorm || p.bias != nullptr || (p.groups > 1 && p.group_top == 2))) score = scores_of<V, float>(p, l);
     int pick[2];
-    double *s_key = s_keys + (p.groups > 1 ? warp * p.experts : 0);
-    if (!choose<V, T, float>(p, row, l, reinterpret_cast<float *>(s_key), lane, pick))
-        choose<V, T, double>(p, row, l, s_key, lane, pick);
-
-    // weights, pick by pick
     float at[2], w[2];
+    double *const s_key = s_keys + (p.groups > 1 ? warp * p.experts : 0);
+    if (!choose_fast<V, T>(p, row, l, score, reinterpret_cast<float *>(s_key), lane, pick, at)) {
+        choose_exactly<V, T>(p, row, s_key, lane, pick);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) at[j] = pick[j] >= 0 ? clean(value_of(row[pick[j]])) : kNegInf;
+        for (int j = 0; j < 2; ++j) at[j] = pick[j] >= 0 ? clean(value_of(row[pick[j]])) : kNegInf;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (pick[j] < 0) at[j] = kNegInf;
     if (p.renorm) {
-        // of the chosen alone, with their largest logit taken out: a softmax over them,
-        // or s / e^min(max, 0) for the sigmoid, neither of which underflows in all
-        const float top = warp_max(fmaxf(at[0], at[1]));
-        const float m = p.score == kScoreSoftmax ? top : fminf(top, 0.0f);
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (pick[j] < 0) w[j] = 0.0f;
-            else if (p.score == kScoreSoftmax) w[j] = expf(at[j] - m);
-            else w[j] = at[j] > 0.0f ? 1.0f / (1.0f + expf(-at[j])) : expf(at[j] - m) / (1.0f + expf(at[j]));
-            sum += w[j];
-        }
-        sum = warp_sum(sum);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) w[j] = w[j] / sum;
+        shares(softmax, pick, at, p.topk, w);
     } else {
-        const Scores<float> score = scores_of<V, float>(p, l);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) w[j] = score(at[j]);
+        w[0] = score(at[0]);
+        if (p.topk > 32) w[1] = score(at[1]);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -274,168 +508,195 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
         }
 }
 
-// Gradient.  With g_j = scale * dweights_j of pick j (expert i_j):
-//   softmax, renormalised  u = softmax over the picks:  d_j = u_j sum_k u_k (g_j - g_k)
-//   sigmoid, renormalised  u = s / sum s:               d_j = (1 - s_j) u_j sum_k u_k (g_j - g_k)
+// ---------------------------------------------------------------- gradient ----
+// With g_j = scale * dweights_j of pick j (expert i_j) and u the shares of the picks:
+//   softmax, renormalised  d_j = u_j (g_j - sum_k u_k g_k)
+//   sigmoid, renormalised  d_j = (1 - s_j) u_j (g_j - sum_k u_k g_k)
 //   sigmoid                d_j = g_j s_j (1 - s_j)
-//   softmax                picked:  s_i (G_i * rest + sum_k s_k (G_i - G_k)), others: -s_i sum_k s_k G_k
-// where G merges picks of one expert and rest is the sum of the scores of the
-// others.  Differences of gradients instead of g_j minus their mean: nothing
-// cancels where one pick has nearly all the weight.
+//   softmax                picked:  s_i (G_i - sum_k s_k G_k), others: -s_i sum_k s_k G_k
+// where G merges picks of one expert.  The gradients enter less that of the pick of the
+// largest weight (which changes nothing: the weights sum to 1, for the plain softmax with
+// the others' mass), so that nothing cancels where one pick has nearly all the weight.
 template <int V, typename T>
-__global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const RouteParams p)
+__global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const RouteParams p, bool vec)
 {
+    __shared__ __align__(16) float s_rows[kWarps][32 * V];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= p.tokens) return;
     const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
-    const bool softmax = p.score == kScoreSoftmax, dense = softmax && !p.renorm;
-    int pick[2];
-    float at[2], g[2], u[2], d[2];
+    const bool softmax = p.score == kScoreSoftmax, dense = softmax && !p.renorm, two = p.topk > 32;
+    const int lanes = slot_lanes(p.topk);
+    int pick[2] = {-1, -1};
+    float at[2] = {kNegInf, kNegInf}, g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f}, d[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int slot = lane + 32 * j;
-        const int id = slot < p.topk ? p.ids[t * p.topk + slot] : -1;
-        pick[j] = id >= 0 && id < p.experts ? id : -1;
-        at[j] = pick[j] >= 0 ? clean(value_of(row[pick[j]])) : kNegInf;
-        if (!(at[j] > kNegInf)) pick[j] = -1;
-        g[j] = pick[j] >= 0 ? p.scale * p.dw[t * p.topk + slot] : 0.0f;
+        if (slot >= p.topk) break;
+        const int id = p.ids[t * p.topk + slot];
+        const float dw = p.dw[t * p.topk + slot];
+        if (id < 0 || id >= p.experts) continue;
+        at[j] = clean(value_of(row[id]));
+        if (!(at[j] > kNegInf)) continue;
+        pick[j] = id;
+        g[j] = p.scale * dw;
     }
-    float l[V], acc[V], dot = 0.0f;
-    if (dense) {
+    float acc[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = lane + 32 * v < p.experts ? clean(value_of(row[lane + 32 * v])) : kNegInf;
+    for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+    // picks of one expert: does any slot repeat an earlier one
+    const unsigned peers0 = __match_any_sync(kAll, pick[0]);
+    bool repeated = pick[0] >= 0 && (peers0 & (peers0 - 1)) != 0;
+    if (two) repeated = true;                            // (not looked for among two slots a lane)
+    repeated = __any_sync(kAll, repeated);
+    if (p.renorm) {
+        shares(softmax, pick, at, p.topk, u);
+    } else if (dense) {
+        float l[V];
+        load_row<V, T>(row, lane, p.experts, vec, l);
+        const Scores<float> score = scores_of<V, float>(p, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = l[v] > kNegInf ? score(l[v]) : 0.0f;
+        if (repeated) {                                  // the first carries their sum
+            float merged[2] = {0.0f, 0.0f};
+            bool first[2] = {true, true};
+            for (int k = 0; k < p.topk; ++k) {
+                const int id = __shfl_sync(kAll, pick[k >> 5], k & 31);
+                const float gk = __shfl_sync(kAll, g[k >> 5], k & 31);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (id >= 0 && id == pick[j]) {
+                        merged[j] += gk;
+                        if (k < lane + 32 * j) first[j] = false;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (!first[j]) pick[j] = -1;
+                g[j] = merged[j];
+            }
+        }
+        u[0] = pick[0] >= 0 ? score(at[0]) : 0.0f;
+        if (two) u[1] = pick[1] >= 0 ? score(at[1]) : 0.0f;
+    } else {
+        if (pick[0] >= 0) d[0] = g[0] / (1.0f + expf(-at[0])) / (1.0f + expf(at[0]));
+        if (two && pick[1] >= 0) d[1] = g[1] / (1.0f + expf(-at[1])) / (1.0f + expf(at[1]));
+    }
+    float mean = 0.0f, ref = 0.0f;
+    if (p.renorm || dense) {
+        // (shares are not negative: their bits are in order)
+        const uint32_t best = __reduce_max_sync(kAll, __float_as_uint(fmaxf(u[0], u[1])));
+        const bool has0 = __float_as_uint(u[0]) == best;
+        const unsigned who = __ballot_sync(kAll, has0 || __float_as_uint(u[1]) == best);
+        ref = __shfl_sync(kAll, has0 ? g[0] : g[1], __ffs(who) - 1);
+        mean = slots_sum((u[0] > 0.0f ? u[0] * (g[0] - ref) : 0.0f) + (u[1] > 0.0f ? u[1] * (g[1] - ref) : 0.0f), lanes);
+        mean = __shfl_sync(kAll, mean, 0);
     }
     if (p.renorm) {
-        const float top = warp_max(fmaxf(at[0], at[1]));
-        const float m = softmax ? top : fminf(top, 0.0f);
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (pick[j] < 0) u[j] = 0.0f;
-            else if (softmax) u[j] = expf(at[j] - m);
-            else u[j] = at[j] > 0.0f ? 1.0f / (1.0f + expf(-at[j])) : expf(at[j] - m) / (1.0f + expf(at[j]));
-            sum += u[j];
-        }
-        sum = warp_sum(sum);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) u[j] = pick[j] >= 0 ? u[j] / sum : 0.0f;
-    } else if (dense) {
-        const Scores<float> score = scores_of<V, float>(p, l);
-        // picks of one expert: the first carries their sum
-        float merged[2] = {0.0f, 0.0f};
-        bool first[2] = {true, true};
-        for (int k = 0; k < p.topk; ++k) {
-            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31);
-            const float gk = __shfl_sync(kAll, g[k >> 5], k & 31);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (id >= 0 && id == pick[j]) {
-                    merged[j] += gk;
-                    if (k < lane + 32 * j) first[j] = false;
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (!first[j]) pick[j] = -1;
-            g[j] = merged[j];
-            u[j] = pick[j] >= 0 ? score(at[j]) : 0.0f;
-            dot += u[j] * g[j];
-        }
-        dot = warp_sum(dot);
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = score(l[v]);
-        // the others' scores, without those of the picks
-        float others = 0.0f;
-        unsigned taken = 0;
-        for (int k = 0; k < p.topk; ++k) {
-            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31);
-            if (id >= 0 && (id & 31) == lane) taken |= 1u << (id >> 5);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (!((taken >> v) & 1)) others += acc[v];
-            acc[v] = (taken >> v) & 1 ? 0.0f : -acc[v] * dot;
-        }
-        others = warp_sum(others);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) d[j] = others * g[j];
-    } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            d[j] = pick[j] >= 0 ? g[j] / (1.0f + expf(-at[j])) / (1.0f + expf(at[j])) : 0.0f;
-    }
-    if (!dense) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    }
-    if (p.renorm || dense) {
-        float sum[2] = {dense ? d[0] : 0.0f, dense ? d[1] : 0.0f};
+            if (pick[j] >= 0) {
+                d[j] = u[j] * ((g[j] - ref) - mean);
+                if (!softmax) d[j] /= 1.0f + expf(at[j]);
+            }
+    } else if (dense) {
+        // sum_k s_k G_k = ref (1 - rest) + mean, rest the mass of the others: picked ones have
+        // s_i ((G_i - ref) - mean + ref rest), others -s_i (ref (1 - rest) + mean)
+        unsigned taken[(V + 31) / 32] = {};
         for (int k = 0; k < p.topk; ++k) {
-            const float uk = __shfl_sync(kAll, u[k >> 5], k & 31);
-            const float gk = __shfl_sync(kAll, g[k >> 5], k & 31);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (uk > 0.0f) sum[j] += uk * (g[j] - gk);
+            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31) - lane * V;
+            if (id >= 0 && id < V) taken[0] |= 1u << id;
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            d[j] = pick[j] >= 0 ? u[j] * sum[j] : 0.0f;
-            if (p.renorm && !softmax && pick[j] >= 0) d[j] /= 1.0f + expf(at[j]);
-        }
-    }
-    for (int k = 0; k < p.topk; ++k) {
-        const int id = __shfl_sync(kAll, pick[k >> 5], k & 31);
-        const float dk = __shfl_sync(kAll, d[k >> 5], k & 31);
+        float others = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (id == lane + 32 * v) acc[v] += dk;
-    }
-    T *out = static_cast<T *>(p.dlogits) + t * p.ldd;
+            if (!((taken[0] >> v) & 1)) others += acc[v];
+        others = warp_sum(others);
+        const float dot = __shfl_sync(kAll, slots_sum(u[0] * g[0] + u[1] * g[1], lanes), 0);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (lane + 32 * v < p.experts) store_value(out + lane + 32 * v, acc[v]);
+        for (int v = 0; v < V; ++v) acc[v] = (taken[0] >> v) & 1 ? 0.0f : -acc[v] * dot;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (pick[j] >= 0) d[j] = u[j] * ((g[j] - ref) - mean + ref * others);
+    }
+    // the picks' gradients to their places among the lane's V
+    float *const s_row = s_rows[warp];
+    if (!repeated || dense) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_row[lane * V + v] = acc[v];
+        __syncwarp();
+        if (pick[0] >= 0) s_row[pick[0]] = d[0];
+        if (two && pick[1] >= 0) s_row[pick[1]] = d[1];
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = s_row[lane * V + v];
+    } else {                                             // in the order of the slots
+        for (int k = 0; k < p.topk; ++k) {
+            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31) - lane * V;
+            const float dk = __shfl_sync(kAll, d[k >> 5], k & 31);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (id == v) acc[v] += dk;
+        }
+    }
+    T *out = static_cast<T *>(p.dlogits) + t * p.ldd + lane * V;
+    if (vec) {
+        if (lane * V < p.experts) store_vector<V, T>(out, acc);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v < p.experts) store_value(out + v, acc[v]);
+    }
 }
 
-cudaError_t launch_dependent(void (*kernel)(RouteParams), unsigned grid, size_t smem, cudaStream_t s, const RouteParams &p)
+cudaError_t launch_dependent(void (*kernel)(RouteParams, bool), size_t smem, bool vec, cudaStream_t s, const RouteParams &p)
 {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.tokens + kWarps - 1) / kWarps), 1, 1);
     cfg.blockDim = dim3(32 * kWarps, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p, vec);
 }
 
-using Kernel = void (*)(RouteParams);
+using Kernel = void (*)(RouteParams, bool);
 
-template <typename T>
-Kernel route_kernel(int experts)
+template <typename T, int V>
+constexpr Kernel kernel_of(bool backward)
 {
-    return experts <= 32    ? moe_route_kernel<1, T>
-           : experts <= 64  ? moe_route_kernel<2, T>
-           : experts <= 128 ? moe_route_kernel<4, T>
-           : experts <= 256 ? moe_route_kernel<8, T>
-           : experts <= 512 ? moe_route_kernel<16, T>
-                            : moe_route_kernel<32, T>;
+    return backward ? moe_route_backward_kernel<V, T> : moe_route_kernel<V, T>;
+}
+
+// Experts per lane: the power of two that holds them all.
+int lane_experts(int experts)
+{
+    int v = 1;
+    while (32 * v < experts) v *= 2;
+    return v;
 }
 
 template <typename T>
-Kernel backward_kernel(int experts)
+Kernel kernel_for(int v, bool backward)
 {
-    return experts <= 32    ? moe_route_backward_kernel<1, T>
-           : experts <= 64  ? moe_route_backward_kernel<2, T>
-           : experts <= 128 ? moe_route_backward_kernel<4, T>
-           : experts <= 256 ? moe_route_backward_kernel<8, T>
-           : experts <= 512 ? moe_route_backward_kernel<16, T>
-                            : moe_route_backward_kernel<32, T>;
+    return v == 1    ? kernel_of<T, 1>(backward)
+           : v == 2  ? kernel_of<T, 2>(backward)
+           : v == 4  ? kernel_of<T, 4>(backward)
+           : v == 8  ? kernel_of<T, 8>(backward)
+           : v == 16 ? kernel_of<T, 16>(backward)
+                     : kernel_of<T, 32>(backward);
+}
+
+bool vector_rows(const void *base, int64_t ld, int size, int v, int experts)
+{
+    const int bytes = std::min(16, v * size);
+    return experts % v == 0 && reinterpret_cast<uintptr_t>(base) % bytes == 0 && ld * size % bytes == 0;
 }
 
 }  // namespace
@@ -443,16 +704,18 @@ Kernel backward_kernel(int experts)
 cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    const Kernel k = p.type == kTypeF32 ? route_kernel<float>(p.experts) : route_kernel<uint16_t>(p.experts);
+    const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
     const size_t smem = p.groups > 1 ? (size_t)kWarps * p.experts * sizeof(double) : 0;
-    return launch_dependent(k, (unsigned)(((int64_t)p.tokens + kWarps - 1) / kWarps), smem, s, p);
+    return launch_dependent(size == 4 ? kernel_for<float>(v, false) : kernel_for<uint16_t>(v, false), smem,
+                            vector_rows(p.logits, p.ldl, size, v, p.experts), s, p);
 }
 
 cudaError_t launch_route_backward(const RouteParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
-    const Kernel k = p.type == kTypeF32 ? backward_kernel<float>(p.experts) : backward_kernel<uint16_t>(p.experts);
-    return launch_dependent(k, (unsigned)(((int64_t)p.tokens + kWarps - 1) / kWarps), 0, s, p);
+    const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
+    const bool vec = vector_rows(p.logits, p.ldl, size, v, p.experts) && vector_rows(p.dlogits, p.ldd, size, v, p.experts);
+    return launch_dependent(size == 4 ? kernel_for<float>(v, true) : kernel_for<uint16_t>(v, true), 0, vec, s, p);
 }
 
 }  // namespace nvfp4
