@@ -56,7 +56,7 @@ __device__ __forceinline__ void store_vector(T *o, const float (&v)[V])
 }
 
 // A logit as the choice sees it: -inf for NaN, +inf as the largest float.
-__device__ __forceinline__ float clean(float l) { return l > kNegInf ? fminf(l, FLT_MAX) : kNegInf; }
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, kNegInf), FLT_MAX); }   // (fmaxf drops a NaN)
 
 // Unsigned integers in the order of the floats, 0 for -inf.  (-0 counts as 0.)
 __device__ __forceinline__ uint32_t ordered(float f)
@@ -293,6 +293,19 @@ struct Top2 {
     }
 };
 
+// A key and its expert as one word: the key's upper bits in the order of the floats, then the
+// complement of the expert, so that a maximum finds the highest key, ties going to the
+// lower expert.  Words of -inf are below kLowest, as is 0.
+constexpr uint32_t kLowest = 0x00800000u;
+
+template <int V>
+__device__ __forceinline__ uint32_t word_of(float key, int expert)
+{
+    constexpr uint32_t kMask = 32 * V - 1;
+    const int32_t u = __float_as_int(key + 0.0f);        // (-0 counts as 0)
+    return ((uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000)) & ~kMask) | (kMask - (uint32_t)expert);
+}
+
 // The choice with fp32 keys, lane i owning the V experts from i V on.  A key and its expert
 // are one word: the key's upper bits in the order of the floats, then the complement of
 // the expert, so that one maximum over the warp finds a pick, ties going to the lower
@@ -374,10 +387,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     }
     uint32_t k[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const uint32_t o = ordered(key[v]);
-        k[v] = o != 0 ? (o & ~kMask) | (kMask - (uint32_t)(lane * V + v)) : 0u;
-    }
+    for (int v = 0; v < V; ++v) k[v] = word_of<V>(key[v], lane * V + v);
     sort_descending<V>(k);
     // a bf16 logit's bits are all among the upper ones
     const bool exact = by_logit && sizeof(T) == 2;
@@ -396,7 +406,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     float b[2] = {0.0f, 0.0f}, kf[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int i = mine[j] != 0 ? (int)(kMask - (mine[j] & kMask)) : -1;
+        const int i = mine[j] >= kLowest ? (int)(kMask - (mine[j] & kMask)) : -1;
         at[j] = i >= 0 ? clean(value_of(row[i])) : kNegInf;
         if (!by_logit && i >= 0) b[j] = p.bias[i];
         kf[j] = by_logit ? at[j] : key_of(p, score, at[j], b[j]);
@@ -412,7 +422,10 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     // of those left, none may share the upper bits of the first one left out
     const uint32_t out_first = p.topk < 32 ? __shfl_sync(kAll, mine[0], p.topk) : __shfl_sync(kAll, mine[1], p.topk - 32);
     const uint32_t out_second = __reduce_max_sync(kAll, k[0]);
-    if (out_first != 0 && ((out_first ^ out_second) & ~kMask) == 0) sure = false;
+    if (out_first >= kLowest && ((out_first ^ out_second) & ~kMask) == 0) sure = false;
+    if (!__all_sync(kAll, sure)) return false;
+    bool apart = true;                                   // neighbours are further apart than fp32 errs
+    float tol_out = 0.0f;                                // (of the first one left out against the last pick)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (j == 1 && p.topk < 32) break;
@@ -425,7 +438,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
             if (lane == 31) { next = n1; next_at = a1; next_b = b1; next_kf = k1; }
         }
         const int slot = lane + 32 * j;
-        if (slot < p.topk && next != 0) {
+        if (slot < p.topk && next >= kLowest) {
             if (by_logit) {
                 if (!(at[j] >= next_at)) sure = false;
             } else {
@@ -433,11 +446,40 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
                 const bool same = slot + 1 < p.topk && at[j] == next_at && b[j] == next_b;
                 const float s = fmaxf(kf[j] - b[j], 0.0f) + fmaxf(next_kf - next_b, 0.0f);
                 const float tol = rel * s + 2.0f * kAbs + 2.0f * kRound * (fabsf(kf[j]) + fabsf(next_kf));
-                if (!same && !(kf[j] - next_kf > tol)) sure = false;
+                if (!same && !(kf[j] - next_kf > tol)) apart = false;
+                tol_out = tol;
             }
         }
     }
-    return __all_sync(kAll, sure);
+    if (!__all_sync(kAll, sure)) return false;
+    if (__all_sync(kAll, apart)) return true;
+    if (p.score != kScoreSigmoid || p.topk >= 32) return false;
+    // Sigmoid scores need no sum: keys in 64 bits of the picks and of the first one left out
+    // alone, if the next one is further from that one than fp32 errs.
+    const float out_kf = __shfl_sync(kAll, kf[0], p.topk), next_most = unordered(out_second | kMask);
+    tol_out = 2.0f * warp_max(tol_out);
+    if (out_first >= kLowest && out_second >= kLowest && !(out_kf - next_most > tol_out)) return false;
+    const bool here = mine[0] >= kLowest && lane <= p.topk;
+    const int expert = here ? (int)(kMask - (mine[0] & kMask)) : -1;
+    const double exact_key = here ? 1.0 / (1.0 + exp(-(double)at[0])) + (double)b[0] : (double)kNegInf;
+    int rank = 0;
+    for (int i = 0; i <= p.topk; ++i) {
+        const double other = __shfl_sync(kAll, exact_key, i);
+        const int e = __shfl_sync(kAll, expert, i);
+        rank += other > exact_key || (other == exact_key && e < expert) ? 1 : 0;
+    }
+    const float l0 = at[0];
+    pick[0] = -1;
+    at[0] = kNegInf;
+    for (int i = 0; i <= p.topk; ++i) {
+        const int r = __shfl_sync(kAll, rank, i), e = __shfl_sync(kAll, expert, i);
+        const float l = __shfl_sync(kAll, l0, i);
+        if (r == lane && lane < p.topk && e >= 0) {
+            pick[0] = e;
+            at[0] = l;
+        }
+    }
+    return true;
 }
 
 // Lanes that hold the first topk slots, as a power of two (32 for more).
@@ -466,6 +508,107 @@ __device__ __forceinline__ void shares(bool softmax, const int (&pick)[2], const
     const float sum = slots_sum(u[0] + u[1], slot_lanes(topk));
     u[0] = pick[0] >= 0 ? u[0] / sum : 0.0f;
     if (topk > 32) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
+}
+
+// The choice by logits alone where words of one prefix may be sorted against their logits:
+// the same rounds over whole logits, lane i owning experts i, i + 32, ...
+template <int V, typename T>
+__device__ __forceinline__ int choose_by_logit(const RouteParams &p, const T *row, int lane)
+{
+    uint32_t k[V], best = 0;
+    int at = 0, pick = -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        k[v] = lane + 32 * v < p.experts ? ordered(clean(value_of(row[lane + 32 * v]))) : 0u;
+        if (k[v] > best) { best = k[v]; at = v; }
+    }
+    for (int r = 0; r < p.topk; ++r) {
+        const uint32_t m = __reduce_max_sync(kAll, best);
+        if (m == 0) break;
+        const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)(lane + 32 * at) : kAll);
+        pick = lane == r ? i : pick;
+        if (lane == (i & 31)) {
+            best = 0;
+            const int gone = at;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (v == gone) k[v] = 0;
+                if (k[v] > best) { best = k[v]; at = v; }
+            }
+        }
+    }
+    return pick;
+}
+
+// Routing without bias and groups, topk below 32 (a slot a lane, the first expert left out
+// among them): the order of the logits decides, and nothing of the rest is in the
+// registers or the code (16384 tokens, top 8 of 128: 500 instructions a token in the
+// general kernel).
+template <int V, typename T>
+__global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const RouteParams p, bool vec)
+{
+    constexpr uint32_t kMask = 32 * V - 1;
+    constexpr bool kExact = sizeof(T) == 2;              // (a bf16 logit's bits are all in the word)
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const uint32_t t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (t >= (uint32_t)p.tokens) return;
+    const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
+    uint32_t k[V];
+    Scores<float> score = {p.score == kScoreSoftmax, 0.0f, 1.0f};
+    {
+        float l[V];
+        load_row<V, T>(row, lane, p.experts, vec, l);
+        if (score.softmax && !p.renorm) score = scores_of<V, float>(p, l);
+#pragma unroll
+        for (int v = 0; v < V; ++v) k[v] = word_of<V>(l[v], lane * V + v);
+    }
+    sort_descending<V>(k);
+    uint32_t mine = 0;
+    const int rounds = kExact ? p.topk : p.topk + 1;
+    for (int r = 0; r < rounds; ++r) {
+        const uint32_t m = __reduce_max_sync(kAll, k[0]);
+        mine = lane == r ? m : mine;
+        if (k[0] == m) {
+#pragma unroll
+            for (int v = 0; v + 1 < V; ++v) k[v] = k[v + 1];
+            k[V - 1] = 0;
+        }
+    }
+    int pick = mine >= kLowest ? (int)(kMask - (mine & kMask)) : -1;
+    float at = pick >= 0 ? clean(value_of(row[pick])) : kNegInf;
+    if constexpr (!kExact) {
+        // of those left, none may share the upper bits of the first one left out, and no
+        // pick may be sorted against its logit
+        const uint32_t out_first = __shfl_sync(kAll, mine, p.topk), out_second = __reduce_max_sync(kAll, k[0]);
+        const float next = __shfl_down_sync(kAll, at, 1);
+        const bool bad = (out_first >= kLowest && ((out_first ^ out_second) & ~kMask) == 0) ||
+                         (lane < p.topk && pick >= 0 && !(at >= next));
+        if (__any_sync(kAll, bad)) {
+            pick = choose_by_logit<V, T>(p, row, lane);
+            at = pick >= 0 ? clean(value_of(row[pick])) : kNegInf;
+        }
+        if (lane >= p.topk) pick = -1;
+    }
+    float w;
+    if (p.renorm) {
+        // (the first pick has the largest logit; see shares())
+        const float top = __shfl_sync(kAll, at, 0), m = score.softmax ? top : fminf(top, 0.0f);
+        float u = 0.0f;
+        if (pick >= 0) {
+            if (score.softmax) u = expf(at - m);
+            else u = at > 0.0f ? 1.0f / (1.0f + expf(-at)) : expf(at - m) / (1.0f + expf(at));
+        }
+        w = __fdividef(u, slots_sum(u, slot_lanes(p.topk)));
+    } else {
+        w = score(at);
+    }
+    if (lane < p.topk) {
+        const int64_t o = (int64_t)t * p.topk + lane;
+        p.ids[o] = pick;
+        p.weights[o] = pick >= 0 ? p.scale * w : 0.0f;
+    }
 }
 
 template <int V, typename T>
@@ -668,10 +811,12 @@ cudaError_t launch_dependent(void (*kernel)(RouteParams, bool), size_t smem, boo
 
 using Kernel = void (*)(RouteParams, bool);
 
+enum Kind { kGeneral, kPlain, kBackward };
+
 template <typename T, int V>
-constexpr Kernel kernel_of(bool backward)
+constexpr Kernel kernel_of(Kind kind)
 {
-    return backward ? moe_route_backward_kernel<V, T> : moe_route_kernel<V, T>;
+    return kind == kBackward ? moe_route_backward_kernel<V, T> : kind == kPlain ? moe_route_plain_kernel<V, T> : moe_route_kernel<V, T>;
 }
 
 // Experts per lane: the power of two that holds them all.
@@ -683,14 +828,14 @@ int lane_experts(int experts)
 }
 
 template <typename T>
-Kernel kernel_for(int v, bool backward)
+Kernel kernel_for(int v, Kind kind)
 {
-    return v == 1    ? kernel_of<T, 1>(backward)
-           : v == 2  ? kernel_of<T, 2>(backward)
-           : v == 4  ? kernel_of<T, 4>(backward)
-           : v == 8  ? kernel_of<T, 8>(backward)
-           : v == 16 ? kernel_of<T, 16>(backward)
-                     : kernel_of<T, 32>(backward);
+    return v == 1    ? kernel_of<T, 1>(kind)
+           : v == 2  ? kernel_of<T, 2>(kind)
+           : v == 4  ? kernel_of<T, 4>(kind)
+           : v == 8  ? kernel_of<T, 8>(kind)
+           : v == 16 ? kernel_of<T, 16>(kind)
+                     : kernel_of<T, 32>(kind);
 }
 
 bool vector_rows(const void *base, int64_t ld, int size, int v, int experts)
@@ -706,7 +851,8 @@ cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s)
     (void)num_sms;
     const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
     const size_t smem = p.groups > 1 ? (size_t)kWarps * p.experts * sizeof(double) : 0;
-    return launch_dependent(size == 4 ? kernel_for<float>(v, false) : kernel_for<uint16_t>(v, false), smem,
+    const Kind kind = p.bias == nullptr && p.groups == 1 && p.topk < 32 ? kPlain : kGeneral;
+    return launch_dependent(size == 4 ? kernel_for<float>(v, kind) : kernel_for<uint16_t>(v, kind), smem,
                             vector_rows(p.logits, p.ldl, size, v, p.experts), s, p);
 }
 
@@ -715,7 +861,7 @@ cudaError_t launch_route_backward(const RouteParams &p, int num_sms, cudaStream_
     (void)num_sms;
     const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
     const bool vec = vector_rows(p.logits, p.ldl, size, v, p.experts) && vector_rows(p.dlogits, p.ldd, size, v, p.experts);
-    return launch_dependent(size == 4 ? kernel_for<float>(v, true) : kernel_for<uint16_t>(v, true), 0, vec, s, p);
+    return launch_dependent(size == 4 ? kernel_for<float>(v, kBackward) : kernel_for<uint16_t>(v, kBackward), 0, vec, s, p);
 }
 
 }  // namespace nvfp4
