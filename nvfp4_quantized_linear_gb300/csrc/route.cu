@@ -139,81 +139,96 @@ __device__ __forceinline__ Scores<F> scores_of(const RouteParams &p, const float
 constexpr float kRelSigmoid = 1.5f * 0x1p-22f, kRelSoftmax = 0x1p-20f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
 
 // ------------------------------------------------------------ exact choice ----
-// Keys in 64 bits, lane i owning experts i, i + 32, ...: the tokens (one in a few hundred
-// to thousands) whose order the fast choice below cannot be sure of.  pick[j]: the expert of
-// slot lane + 32 j, -1 for none.  s_key: `experts` doubles of the warp, for groups.
-template <int V, typename T>
-__device__ __noinline__ void choose_exactly(const RouteParams &p, const T *row, double *s_key, int lane, int (&pick)[2])
+// Keys in 64 bits, for the tokens whose order the fast choice below cannot be sure of.  Calls,
+// so that their registers and code stay out of the way; p lies in constant memory
+// (copied for a call it cost every token 28 stores to local memory).
+
+// The row's keys into s_key (`experts` doubles of the warp): scores with the bias, or the
+// logits themselves where nobody asks for scores.  Returns the groups that stay.
+template <typename T>
+__device__ __noinline__ unsigned exact_keys(const RouteParams &p, const T *row, double *s_key, int lane)
+{
+    const bool by_logit = p.bias == nullptr, softmax = p.score == kScoreSoftmax;
+    const bool scores = !by_logit || (p.groups > 1 && p.group_top == 2);
+    const double none = (double)kNegInf;
+    double max = none, sum = 1.0;
+    if (softmax) {
+        float m = kNegInf;
+        for (int i = lane; i < p.experts; i += 32) m = fmaxf(m, clean(value_of(row[i])));
+        m = warp_max(m);
+        max = m > kNegInf ? (double)m : 0.0;
+        sum = 0.0;
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < p.experts; i += 32) {
+        const float l = clean(value_of(row[i]));
+        double k = (double)l;
+        if (scores && l > kNegInf) {
+            k = exp(softmax ? k - max : -k);             // (the softmax's quotient follows)
+            if (softmax) sum += k;
+            else k = 1.0 / (1.0 + k);
+        }
+        s_key[i] = k;
+    }
+    if (scores) {
+        if (softmax) sum = warp_sum(sum);
+        for (int i = lane; i < p.experts; i += 32) {
+            const float b = by_logit ? 0.0f : p.bias[i];
+            if (s_key[i] > none) s_key[i] = b > kNegInf ? (softmax ? s_key[i] / sum : s_key[i]) + (double)b : none;
+        }
+    }
+    __syncwarp();
+    if (p.groups == 1) return ~0u;
+    const int size = p.experts / p.groups;
+    double top1 = none, top2 = none;
+    if (lane < p.groups)
+        for (int i = 0; i < size; ++i) {
+            const double k = s_key[lane * size + i];
+            top2 = k > top1 ? top1 : k > top2 ? k : top2;
+            top1 = k > top1 ? k : top1;
+        }
+    const double value = p.group_top == 2 && top2 > none ? top1 + top2 : top1;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const double other = __shfl_sync(kAll, value, g);
+        rank += other > value || (other == value && g < lane) ? 1 : 0;
+    }
+    return __ballot_sync(kAll, lane < p.groups && rank < p.topk_groups);
+}
+
+// The choice by them, pick by pick the best key after the last pick in the order (keys
+// down, experts up).  Returns the experts of slots lane (low half) and lane + 32, 0xFFFF
+// for none.  About one token in a million comes here.
+template <typename T>
+__device__ __noinline__ uint32_t choose_exactly(const RouteParams &p, const T *row, double *s_key, int lane)
 {
     const bool by_logit = p.bias == nullptr;
-    float l[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = lane + 32 * v < p.experts ? clean(value_of(row[lane + 32 * v])) : kNegInf;
-    Scores<double> score = {false, 0.0, 1.0};
-    if (!by_logit || (p.groups > 1 && p.group_top == 2)) score = scores_of<V, double>(p, l);
-    const double none = (double)kNegInf;
-    double key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        key[v] = (double)l[v];
-        const int i = lane + 32 * v;
-        if (!by_logit && i < p.experts) {
-            const float b = p.bias[i];
-            key[v] = l[v] > kNegInf && b > kNegInf ? score((double)l[v]) + (double)b : none;
-        }
-    }
-    if (p.groups > 1) {
-        const int size = p.experts / p.groups;
-        __syncwarp();
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane + 32 * v < p.experts) s_key[lane + 32 * v] = key[v];
-        __syncwarp();
-        double top1 = none, top2 = none;
-        if (lane < p.groups)
-            for (int i = 0; i < size; ++i) {
-                const double k = s_key[lane * size + i];
-                top2 = k > top1 ? top1 : k > top2 ? k : top2;
-                top1 = k > top1 ? k : top1;
-            }
-        double value = top1;
-        if (p.group_top == 2 && top1 > none) {
-            if (by_logit) value = score(top1) + (top2 > none ? score(top2) : 0.0);
-            else if (top2 > none) value = top1 + top2;
-        }
-        int rank = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const double other = __shfl_sync(kAll, value, g);
-            rank += other > value || (other == value && g < lane) ? 1 : 0;
-        }
-        const unsigned mask = __ballot_sync(kAll, lane < p.groups && rank < p.topk_groups);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (!((mask >> ((lane + 32 * v) / size & 31)) & 1)) key[v] = none;
-    }
-    uint64_t k[V], best = 0;
-    int at = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        k[v] = ordered(key[v]);
-        if (k[v] > best) { best = k[v]; at = v; }
-    }
-    pick[0] = pick[1] = -1;
+    const unsigned mask = exact_keys(p, row, s_key, lane);
+    const int size = p.experts / p.groups;
+    uint32_t pick0 = 0xFFFFu, pick1 = 0xFFFFu;
+    uint64_t last = ~0ull;
+    int last_i = -1;
+#pragma unroll 1
     for (int r = 0; r < p.topk; ++r) {
+        uint64_t best = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = lane; i < p.experts; i += 32) {
+            if (!((mask >> (i / size & 31)) & 1)) continue;
+            // (by logits the order is theirs, also where the groups went by scores)
+            const uint64_t k = ordered(by_logit ? (double)clean(value_of(row[i])) : s_key[i]);
+            if ((k < last || (k == last && i > last_i)) && k > best) { best = k; at = i; }
+        }
         const uint64_t m = warp_max(best);
         if (m == 0) break;
-        const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)(lane + 32 * at) : kAll);
-        if (lane == (r & 31)) pick[r >> 5] = i;
-        if (lane == (i & 31)) {
-            best = 0;
-            const int gone = at;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (v == gone) k[v] = 0;
-                if (k[v] > best) { best = k[v]; at = v; }
-            }
-        }
+        const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)at : kAll);
+        if (lane == r) pick0 = (uint32_t)i;
+        if (lane == r - 32) pick1 = (uint32_t)i;
+        last = m;
+        last_i = i;
     }
+    return pick0 | pick1 << 16;
 }
 
 // ------------------------------------------------------------- fast choice ----
@@ -315,9 +330,10 @@ __device__ __forceinline__ uint32_t word_of(float key, int expert)
 // sorted by the upper bits alone against their keys.
 template <int V, typename T>
 __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, const float (&l)[V],
-                                            const Scores<float> &score, float *s_key, int lane, int (&pick)[2],
+                                            const Scores<float> &score, double *s_key, int lane, int (&pick)[2],
                                             float (&at)[2])
 {
+    float *const s_float = reinterpret_cast<float *>(s_key);
     constexpr uint32_t kMask = 32 * V - 1;
     const bool by_logit = p.bias == nullptr;
     const float rel = p.score == kScoreSoftmax ? kRelSoftmax : kRelSigmoid;
@@ -329,9 +345,9 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         for (int v = 0; v < V; ++v)
             if (lane * V + v < p.experts) key[v] = key_of(p, score, l[v], p.bias[lane * V + v]);
     }
-    bool sure = true;
     if (p.groups > 1) {
         const int size = p.experts / p.groups, lanes = size / V;
+        bool exact_groups = false;
         // groups of whole lanes, a power of two of them: by shuffles; others through shared memory, a
         // group per lane.  `mine`: the lane's group, `at0`: where group g's value stands, g * at0.
         const bool whole = lanes * V == size && (lanes & (lanes - 1)) == 0;
@@ -347,10 +363,10 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (lane * V + v < p.experts) s_key[lane * V + v] = key[v];
+                if (lane * V + v < p.experts) s_float[lane * V + v] = key[v];
             __syncwarp();
             if (lane < p.groups)
-                for (int i = 0; i < size; ++i) top.add(s_key[lane * size + i]);
+                for (int i = 0; i < size; ++i) top.add(s_float[lane * size + i]);
             __syncwarp();
         }
         const int mine = whole ? lane / lanes : lane, at0 = whole ? lanes : 1;
@@ -372,9 +388,14 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
             high = warp_max(high);
             // (a score is at most 1; two of them and three roundings)
             const float tol = 4.0f * rel + 2.0f * kAbs + 3.0f * kRound * (fabsf(low) + fabsf(high));
-            if (high > kNegInf && !(low - high > tol)) sure = false;
+            if (high > kNegInf && !(low - high > tol)) exact_groups = true;
         }
-        if (whole) {
+        if (exact_groups) {
+            const unsigned mask = exact_keys(p, row, s_key, lane);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (!((mask >> ((lane * V + v) / size & 31)) & 1)) key[v] = kNegInf;
+        } else if (whole) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (!kept) key[v] = kNegInf;
@@ -417,15 +438,12 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         pick[1] = -1;
         at[1] = kNegInf;
     }
-    if (exact) return sure;
+    if (exact) return true;
     if (p.topk >= 64) return false;
-    // of those left, none may share the upper bits of the first one left out
-    const uint32_t out_first = p.topk < 32 ? __shfl_sync(kAll, mine[0], p.topk) : __shfl_sync(kAll, mine[1], p.topk - 32);
+    // Slots past the picks: the first expert left out, and the next one's word.
     const uint32_t out_second = __reduce_max_sync(kAll, k[0]);
-    if (out_first >= kLowest && ((out_first ^ out_second) & ~kMask) == 0) sure = false;
-    if (!__all_sync(kAll, sure)) return false;
-    bool apart = true;                                   // neighbours are further apart than fp32 errs
-    float tol_out = 0.0f;                                // (of the first one left out against the last pick)
+    const float next_most = out_second >= kLowest ? unordered(out_second | kMask) : kNegInf;
+    bool apart = true, sure = true;                      // neighbours are in order; the next one is behind all picks
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (j == 1 && p.topk < 32) break;
@@ -438,30 +456,23 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
             if (lane == 31) { next = n1; next_at = a1; next_b = b1; next_kf = k1; }
         }
         const int slot = lane + 32 * j;
-        if (slot < p.topk && next >= kLowest) {
-            if (by_logit) {
-                if (!(at[j] >= next_at)) sure = false;
-            } else {
-                // experts of one logit and one bias are equal in any precision
-                const bool same = slot + 1 < p.topk && at[j] == next_at && b[j] == next_b;
-                const float s = fmaxf(kf[j] - b[j], 0.0f) + fmaxf(next_kf - next_b, 0.0f);
-                const float tol = rel * s + 2.0f * kAbs + 2.0f * kRound * (fabsf(kf[j]) + fabsf(next_kf));
-                if (!same && !(kf[j] - next_kf > tol)) apart = false;
-                tol_out = tol;
-            }
-        }
+        if (slot >= p.topk || next < kLowest) continue;
+        const float s = fmaxf(kf[j] - b[j], 0.0f) + fmaxf(next_kf - next_b, 0.0f);
+        const float tol = by_logit ? 0.0f : rel * s + 2.0f * kAbs + 2.0f * kRound * (fabsf(kf[j]) + fabsf(next_kf));
+        // (experts of one logit and one bias are equal in any precision)
+        if (by_logit) apart = apart && at[j] >= next_at;
+        else if (at[j] != next_at || b[j] != next_b || slot + 1 == p.topk) apart = apart && kf[j] - next_kf > tol;
+        if (slot + 1 == p.topk && out_second >= kLowest) sure = kf[j] - next_most > tol;
     }
     if (!__all_sync(kAll, sure)) return false;
     if (__all_sync(kAll, apart)) return true;
-    if (p.score != kScoreSigmoid || p.topk >= 32) return false;
-    // Sigmoid scores need no sum: keys in 64 bits of the picks and of the first one left out
-    // alone, if the next one is further from that one than fp32 errs.
-    const float out_kf = __shfl_sync(kAll, kf[0], p.topk), next_most = unordered(out_second | kMask);
-    tol_out = 2.0f * warp_max(tol_out);
-    if (out_first >= kLowest && out_second >= kLowest && !(out_kf - next_most > tol_out)) return false;
+    if (p.topk >= 32 || (!by_logit && p.score != kScoreSigmoid)) return false;
+    // The picks and the first one left out again by logits, or by keys in 64 bits (a sigmoid
+    // needs no sum): each one's rank among them.
     const bool here = mine[0] >= kLowest && lane <= p.topk;
-    const int expert = here ? (int)(kMask - (mine[0] & kMask)) : -1;
-    const double exact_key = here ? 1.0 / (1.0 + exp(-(double)at[0])) + (double)b[0] : (double)kNegInf;
+    const int expert = here ? (int)(kMask - (mine[0] & kMask)) : 32 * V;
+    double exact_key = here ? (double)at[0] : (double)kNegInf;
+    if (here && !by_logit) exact_key = 1.0 / (1.0 + exp(-exact_key)) + (double)b[0];
     int rank = 0;
     for (int i = 0; i <= p.topk; ++i) {
         const double other = __shfl_sync(kAll, exact_key, i);
@@ -474,7 +485,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     for (int i = 0; i <= p.topk; ++i) {
         const int r = __shfl_sync(kAll, rank, i), e = __shfl_sync(kAll, expert, i);
         const float l = __shfl_sync(kAll, l0, i);
-        if (r == lane && lane < p.topk && e >= 0) {
+        if (r == lane && lane < p.topk && e < 32 * V) {
             pick[0] = e;
             at[0] = l;
         }
@@ -510,32 +521,29 @@ __device__ __forceinline__ void shares(bool softmax, const int (&pick)[2], const
     if (topk > 32) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
 }
 
-// The choice by logits alone where words of one prefix may be sorted against their logits:
-// the same rounds over whole logits, lane i owning experts i, i + 32, ...
-template <int V, typename T>
+// The choice by whole logits, where words of one prefix may be sorted against them: pick by
+// pick the best after the last one in the order (logits down, experts up).  Small, as it is
+// cold when it is called.
+template <typename T>
 __device__ __forceinline__ int choose_by_logit(const RouteParams &p, const T *row, int lane)
 {
-    uint32_t k[V], best = 0;
-    int at = 0, pick = -1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        k[v] = lane + 32 * v < p.experts ? ordered(clean(value_of(row[lane + 32 * v]))) : 0u;
-        if (k[v] > best) { best = k[v]; at = v; }
-    }
+    int pick = -1, last_i = -1;
+    uint32_t last = ~0u;
+#pragma unroll 1
     for (int r = 0; r < p.topk; ++r) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll 1
+        for (int i = lane; i < p.experts; i += 32) {
+            const uint32_t k = ordered(clean(value_of(row[i])));
+            if ((k < last || (k == last && i > last_i)) && k > best) { best = k; at = i; }
+        }
         const uint32_t m = __reduce_max_sync(kAll, best);
         if (m == 0) break;
-        const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)(lane + 32 * at) : kAll);
+        const int i = (int)__reduce_min_sync(kAll, best == m ? (unsigned)at : kAll);
         pick = lane == r ? i : pick;
-        if (lane == (i & 31)) {
-            best = 0;
-            const int gone = at;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (v == gone) k[v] = 0;
-                if (k[v] > best) { best = k[v]; at = v; }
-            }
-        }
+        last = m;
+        last_i = i;
     }
     return pick;
 }
@@ -579,14 +587,26 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const Rout
     int pick = mine >= kLowest ? (int)(kMask - (mine & kMask)) : -1;
     float at = pick >= 0 ? clean(value_of(row[pick])) : kNegInf;
     if constexpr (!kExact) {
-        // of those left, none may share the upper bits of the first one left out, and no
-        // pick may be sorted against its logit
-        const uint32_t out_first = __shfl_sync(kAll, mine, p.topk), out_second = __reduce_max_sync(kAll, k[0]);
+        // words of one prefix may be sorted against their logits: the picks and the first one
+        // left out are ranked again; if the next one shares the last pick's prefix, all are
+        const uint32_t last = __shfl_sync(kAll, mine, p.topk - 1), second = __reduce_max_sync(kAll, k[0]);
         const float next = __shfl_down_sync(kAll, at, 1);
-        const bool bad = (out_first >= kLowest && ((out_first ^ out_second) & ~kMask) == 0) ||
-                         (lane < p.topk && pick >= 0 && !(at >= next));
-        if (__any_sync(kAll, bad)) {
-            pick = choose_by_logit<V, T>(p, row, lane);
+        if (second >= kLowest && ((last ^ second) & ~kMask) == 0) {
+            pick = choose_by_logit(p, row, lane);
+            at = pick >= 0 ? clean(value_of(row[pick])) : kNegInf;
+        } else if (__any_sync(kAll, lane < p.topk && pick >= 0 && !(at >= next))) {
+            const uint32_t key = pick >= 0 ? ordered(at) : 0u;
+            int rank = 0, to = -1;
+            for (int i = 0; i <= p.topk; ++i) {
+                const uint32_t other = __shfl_sync(kAll, key, i);
+                const int e = __shfl_sync(kAll, pick, i);
+                rank += other > key || (other == key && e < pick) ? 1 : 0;
+            }
+            for (int i = 0; i <= p.topk; ++i) {
+                const int r = __shfl_sync(kAll, rank, i), e = __shfl_sync(kAll, pick, i);
+                if (r == lane && e >= 0) to = e;
+            }
+            pick = to;
             at = pick >= 0 ? clean(value_of(row[pick])) : kNegInf;
         }
         if (lane >= p.topk) pick = -1;
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const Rout
 }
 
 template <int V, typename T>
-__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParams p, bool vec)
+__global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_constant__ RouteParams p, bool vec)
 {
     extern __shared__ double s_keys[];
     griddep_launch_dependents();
@@ -628,9 +648,11 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const RouteParam
     if (softmax && (!p.renorm || p.bias != nullptr || (p.groups > 1 && p.group_top == 2))) score = scores_of<V, float>(p, l);
     int pick[2];
     float at[2], w[2];
-    double *const s_key = s_keys + (p.groups > 1 ? warp * p.experts : 0);
-    if (!choose_fast<V, T>(p, row, l, score, reinterpret_cast<float *>(s_key), lane, pick, at)) {
-        choose_exactly<V, T>(p, row, s_key, lane, pick);
+    double *const s_key = s_keys + warp * p.experts;
+    if (!choose_fast<V, T>(p, row, l, score, s_key, lane, pick, at)) {
+        const uint32_t found = choose_exactly(p, row, s_key, lane);
+        pick[0] = (found & 0xFFFFu) == 0xFFFFu ? -1 : (int)(found & 0xFFFFu);
+        pick[1] = found >> 16 == 0xFFFFu ? -1 : (int)(found >> 16);
 #pragma unroll
         for (int j = 0; j < 2; ++j) at[j] = pick[j] >= 0 ? clean(value_of(row[pick[j]])) : kNegInf;
     }
@@ -850,8 +872,8 @@ cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s)
 {
     (void)num_sms;
     const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
-    const size_t smem = p.groups > 1 ? (size_t)kWarps * p.experts * sizeof(double) : 0;
     const Kind kind = p.bias == nullptr && p.groups == 1 && p.topk < 32 ? kPlain : kGeneral;
+    const size_t smem = kind == kGeneral ? (size_t)kWarps * p.experts * sizeof(double) : 0;
     return launch_dependent(size == 4 ? kernel_for<float>(v, kind) : kernel_for<uint16_t>(v, kind), smem,
                             vector_rows(p.logits, p.ldl, size, v, p.experts), s, p);
 }

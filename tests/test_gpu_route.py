@@ -88,6 +88,26 @@ def test_keys_that_fp32_cannot_tell_apart(e, groups, group_top, score):
               topk_groups=min(2, groups))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top", [(1, 1), (4, 1), (4, 2)])
+@pytest.mark.parametrize("e,topk", [(24, 3), (64, 8), (256, 8), (1000, 9), (1024, 31), (256, 40)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_logits_a_few_steps_apart(bias, e, topk, groups, group_top, score):
+    """Runs of logits that differ in their last bits, in random order: pairs, triples and many."""
+    rng = np.random.default_rng(e + topk)
+    base = np.sort(rng.standard_normal(e).astype(np.float32))[::-1].copy()
+    rows = []
+    for run in (1, 2, 3, e // 2):
+        for start in (0, 1, topk - 1, max(topk - 2, 0)):
+            l = base.copy()
+            n = min(run, e - start)
+            l[start:start + n] = l[start] * (1 + np.float32(2.0 ** -23) * rng.integers(0, 9, n).astype(np.float32))
+            rows.append(rng.permutation(l))
+    b = torch.full((e,), 0.25, device="cuda") if bias else None
+    check(torch.from_numpy(np.stack(rows)).cuda(), topk, score, b, groups=groups, group_top=group_top,
+          topk_groups=min(3, groups))
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
