@@ -83,12 +83,7 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v)
     return ((uint64_t)hi << 32) | lo;
 }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
-}
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(kAll, ordered(v))); }
 
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v)
@@ -98,45 +93,41 @@ __device__ __forceinline__ F warp_sum(F v)
     return v;
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
-
 // Scores of a row: softmax over its experts (max and sum of exponentials given) or
-// sigmoid.
-template <typename F>
+// sigmoid.  (__fdividef: good to 2 ulp below 2^126.)
 struct Scores {
     bool softmax;
-    F max, sum;
-    __device__ __forceinline__ F operator()(F l) const
+    float max, sum;
+    __device__ __forceinline__ float operator()(float l) const
     {
-        return softmax ? exp_of(l - max) / sum : F(1) / (F(1) + exp_of(-l));
+        return softmax ? __fdividef(expf(l - max), sum) : __fdividef(1.0f, 1.0f + expf(-l));
     }
 };
 
-template <int V, typename F>
-__device__ __forceinline__ Scores<F> scores_of(const RouteParams &p, const float (&l)[V])
+template <int V>
+__device__ __forceinline__ Scores scores_of(const RouteParams &p, const float (&l)[V])
 {
-    Scores<F> s = {p.score == kScoreSoftmax, F(0), F(1)};
+    Scores s = {p.score == kScoreSoftmax, 0.0f, 1.0f};
     if (s.softmax) {
         float m = kNegInf;
 #pragma unroll
         for (int v = 0; v < V; ++v) m = fmaxf(m, l[v]);
         m = warp_max(m);
-        s.max = m > kNegInf ? F(m) : F(0);
-        F sum = F(0);
+        s.max = m > kNegInf ? m : 0.0f;
+        float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum += exp_of(F(l[v]) - s.max);
+        for (int v = 0; v < V; ++v) sum += expf(l[v] - s.max);
         sum = warp_sum(sum);
-        s.sum = sum > F(0) ? sum : F(1);
+        s.sum = sum > 0.0f ? sum : 1.0f;
     }
     return s;
 }
 
-// Bounds of what the fp32 keys may be off: a score's relative error (expf 2 ulp,
-// quotient, sum; for a softmax the rounding of l - max too, at most 2^-24 of the
+// Bounds of what the fp32 keys may be off: a score's relative error (expf and quotient 2
+// ulp each, sums; for a softmax the rounding of l - max too, at most 2^-24 of the
 // distance, which the exponential takes below 2^-25 absolute) and the rounding of
-// the sum with the bias.
-constexpr float kRelSigmoid = 1.5f * 0x1p-22f, kRelSoftmax = 0x1p-20f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
+// the sum with the bias.  (Scores below 2^-120 may become 0: far below kAbs.)
+constexpr float kRelSigmoid = 1.25f * 0x1p-21f, kRelSoftmax = 0x1p-20f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
 
 // ------------------------------------------------------------ exact choice ----
 // Keys in 64 bits, for the tokens whose order the fast choice below cannot be sure of.  Calls,
@@ -206,6 +197,8 @@ __device__ __noinline__ uint32_t choose_exactly(const RouteParams &p, const T *r
     const bool by_logit = p.bias == nullptr;
     const unsigned mask = exact_keys(p, row, s_key, lane);
     const int size = p.experts / p.groups;
+    // (by logits the order is theirs, also where the groups went by scores)
+    const bool from_row = by_logit && p.groups > 1 && p.group_top == 2;
     uint32_t pick0 = 0xFFFFu, pick1 = 0xFFFFu;
     uint64_t last = ~0ull;
     int last_i = -1;
@@ -216,8 +209,7 @@ __device__ __noinline__ uint32_t choose_exactly(const RouteParams &p, const T *r
 #pragma unroll 1
         for (int i = lane; i < p.experts; i += 32) {
             if (!((mask >> (i / size & 31)) & 1)) continue;
-            // (by logits the order is theirs, also where the groups went by scores)
-            const uint64_t k = ordered(by_logit ? (double)clean(value_of(row[i])) : s_key[i]);
+            const uint64_t k = ordered(from_row ? (double)clean(value_of(row[i])) : s_key[i]);
             if ((k < last || (k == last && i > last_i)) && k > best) { best = k; at = i; }
         }
         const uint64_t m = warp_max(best);
@@ -293,7 +285,7 @@ __device__ __forceinline__ void sort_descending(uint32_t (&k)[V])
                     }
 }
 
-__device__ __forceinline__ float key_of(const RouteParams &p, const Scores<float> &score, float l, float b)
+__device__ __forceinline__ float key_of(const RouteParams &p, const Scores &score, float l, float b)
 {
     return l > kNegInf && b > kNegInf ? score(l) + b : kNegInf;
 }
@@ -328,9 +320,9 @@ __device__ __forceinline__ uint32_t word_of(float key, int expert)
 // What the lower bits of the keys would have decided shows between neighbours in the
 // order: false if two of them (or two groups) are too near each other for fp32, or
 // sorted by the upper bits alone against their keys.
-template <int V, typename T>
+template <int V, typename T, bool kTwo>
 __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, const float (&l)[V],
-                                            const Scores<float> &score, double *s_key, int lane, int (&pick)[2],
+                                            const Scores &score, double *s_key, int lane, int (&pick)[2],
                                             float (&at)[2])
 {
     float *const s_float = reinterpret_cast<float *>(s_key);
@@ -416,8 +408,8 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     const int rounds = exact ? p.topk : p.topk + 1;
     for (int r = 0; r < rounds; ++r) {
         const uint32_t m = __reduce_max_sync(kAll, k[0]);
-        if (r < 32) mine[0] = lane == r ? m : mine[0];
-        else mine[1] = lane == r - 32 ? m : mine[1];
+        mine[0] = lane == r ? m : mine[0];
+        if constexpr (kTwo) mine[1] = lane == r - 32 ? m : mine[1];
         if (k[0] == m) {
 #pragma unroll
             for (int v = 0; v + 1 < V; ++v) k[v] = k[v + 1];
@@ -432,25 +424,25 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         if (!by_logit && i >= 0) b[j] = p.bias[i];
         kf[j] = by_logit ? at[j] : key_of(p, score, at[j], b[j]);
         pick[j] = lane + 32 * j < p.topk ? i : -1;
-        if (p.topk < 32) break;                          // (one slot a lane, the first one left out among them)
-    }
-    if (p.topk < 32) {
-        pick[1] = -1;
-        at[1] = kNegInf;
+        if constexpr (!kTwo) {                           // (one slot a lane, the first one left out among them)
+            pick[1] = -1;
+            at[1] = kNegInf;
+            break;
+        }
     }
     if (exact) return true;
-    if (p.topk >= 64) return false;
+    if (kTwo && p.topk >= 64) return false;
     // Slots past the picks: the first expert left out, and the next one's word.
     const uint32_t out_second = __reduce_max_sync(kAll, k[0]);
     const float next_most = out_second >= kLowest ? unordered(out_second | kMask) : kNegInf;
     bool apart = true, sure = true;                      // neighbours are in order; the next one is behind all picks
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (j == 1 && p.topk < 32) break;
+        if (j == 1 && !kTwo) break;
         uint32_t next = __shfl_down_sync(kAll, mine[j], 1);
         float next_at = __shfl_down_sync(kAll, at[j], 1), next_b = __shfl_down_sync(kAll, b[j], 1);
         float next_kf = __shfl_down_sync(kAll, kf[j], 1);
-        if (j == 0 && p.topk >= 32) {
+        if (j == 0 && kTwo) {
             const uint32_t n1 = __shfl_sync(kAll, mine[1], 0);
             const float a1 = __shfl_sync(kAll, at[1], 0), b1 = __shfl_sync(kAll, b[1], 0), k1 = __shfl_sync(kAll, kf[1], 0);
             if (lane == 31) { next = n1; next_at = a1; next_b = b1; next_kf = k1; }
@@ -466,7 +458,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     }
     if (!__all_sync(kAll, sure)) return false;
     if (__all_sync(kAll, apart)) return true;
-    if (p.topk >= 32 || (!by_logit && p.score != kScoreSigmoid)) return false;
+    if (kTwo || (!by_logit && p.score != kScoreSigmoid)) return false;
     // The picks and the first one left out again by logits, or by keys in 64 bits (a sigmoid
     // needs no sum): each one's rank among them.
     const bool here = mine[0] >= kLowest && lane <= p.topk;
@@ -504,21 +496,22 @@ __device__ __forceinline__ float slots_sum(float v, int lanes)
 
 // Unnormalised shares of the picks, with their largest logit taken out: a softmax over
 // them, or s / e^min(max, 0) for the sigmoid, neither of which underflows in all.
+template <bool kTwo>
 __device__ __forceinline__ void shares(bool softmax, const int (&pick)[2], const float (&at)[2], int topk, float (&u)[2])
 {
-    const float top = unordered(__reduce_max_sync(kAll, max(ordered(at[0]), topk > 32 ? ordered(at[1]) : 0u)));
+    const float top = unordered(__reduce_max_sync(kAll, max(ordered(at[0]), kTwo ? ordered(at[1]) : 0u)));
     const float m = softmax ? top : fminf(top, 0.0f);
     u[1] = 0.0f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        if (j == 1 && topk <= 32) break;
+        if (j == 1 && !kTwo) break;
         if (pick[j] < 0) u[j] = 0.0f;
         else if (softmax) u[j] = expf(at[j] - m);
         else u[j] = at[j] > 0.0f ? 1.0f / (1.0f + expf(-at[j])) : expf(at[j] - m) / (1.0f + expf(at[j]));
     }
     const float sum = slots_sum(u[0] + u[1], slot_lanes(topk));
     u[0] = pick[0] >= 0 ? u[0] / sum : 0.0f;
-    if (topk > 32) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
+    if constexpr (kTwo) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
 }
 
 // The choice by whole logits, where words of one prefix may be sorted against them: pick by
@@ -564,11 +557,11 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const Rout
     if (t >= (uint32_t)p.tokens) return;
     const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
     uint32_t k[V];
-    Scores<float> score = {p.score == kScoreSoftmax, 0.0f, 1.0f};
+    Scores score = {p.score == kScoreSoftmax, 0.0f, 1.0f};
     {
         float l[V];
         load_row<V, T>(row, lane, p.experts, vec, l);
-        if (score.softmax && !p.renorm) score = scores_of<V, float>(p, l);
+        if (score.softmax && !p.renorm) score = scores_of<V>(p, l);
 #pragma unroll
         for (int v = 0; v < V; ++v) k[v] = word_of<V>(l[v], lane * V + v);
     }
@@ -631,7 +624,8 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const Rout
     }
 }
 
-template <int V, typename T>
+// kTwo: two slots a lane, for topk of 32 and more.
+template <int V, typename T, bool kTwo>
 __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_constant__ RouteParams p, bool vec)
 {
     extern __shared__ double s_keys[];
@@ -644,12 +638,12 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
     float l[V];
     load_row<V, T>(row, lane, p.experts, vec, l);
     const bool softmax = p.score == kScoreSoftmax;
-    Scores<float> score = {softmax, 0.0f, 1.0f};
-    if (softmax && (!p.renorm || p.bias != nullptr || (p.groups > 1 && p.group_top == 2))) score = scores_of<V, float>(p, l);
+    Scores score = {softmax, 0.0f, 1.0f};
+    if (softmax && (!p.renorm || p.bias != nullptr || (p.groups > 1 && p.group_top == 2))) score = scores_of<V>(p, l);
     int pick[2];
     float at[2], w[2];
     double *const s_key = s_keys + warp * p.experts;
-    if (!choose_fast<V, T>(p, row, l, score, s_key, lane, pick, at)) {
+    if (!choose_fast<V, T, kTwo>(p, row, l, score, s_key, lane, pick, at)) {
         const uint32_t found = choose_exactly(p, row, s_key, lane);
         pick[0] = (found & 0xFFFFu) == 0xFFFFu ? -1 : (int)(found & 0xFFFFu);
         pick[1] = found >> 16 == 0xFFFFu ? -1 : (int)(found >> 16);
@@ -657,16 +651,16 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
         for (int j = 0; j < 2; ++j) at[j] = pick[j] >= 0 ? clean(value_of(row[pick[j]])) : kNegInf;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < (kTwo ? 2 : 1); ++j)
         if (pick[j] < 0) at[j] = kNegInf;
     if (p.renorm) {
-        shares(softmax, pick, at, p.topk, w);
+        shares<kTwo>(softmax, pick, at, p.topk, w);
     } else {
         w[0] = score(at[0]);
-        if (p.topk > 32) w[1] = score(at[1]);
+        if constexpr (kTwo) w[1] = score(at[1]);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < (kTwo ? 2 : 1); ++j)
         if (lane + 32 * j < p.topk) {
             p.ids[t * p.topk + lane + 32 * j] = pick[j];
             p.weights[t * p.topk + lane + 32 * j] = pick[j] >= 0 ? p.scale * w[j] : 0.0f;
@@ -682,7 +676,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
 // where G merges picks of one expert.  The gradients enter less that of the pick of the
 // largest weight (which changes nothing: the weights sum to 1, for the plain softmax with
 // the others' mass), so that nothing cancels where one pick has nearly all the weight.
-template <int V, typename T>
+template <int V, typename T, bool kTwo>
 __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const RouteParams p, bool vec)
 {
     __shared__ __align__(16) float s_rows[kWarps][32 * V];
@@ -692,14 +686,14 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= p.tokens) return;
     const T *row = static_cast<const T *>(p.logits) + t * p.ldl;
-    const bool softmax = p.score == kScoreSoftmax, dense = softmax && !p.renorm, two = p.topk > 32;
+    const bool softmax = p.score == kScoreSoftmax, dense = softmax && !p.renorm;
     const int lanes = slot_lanes(p.topk);
     int pick[2] = {-1, -1};
     float at[2] = {kNegInf, kNegInf}, g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f}, d[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int slot = lane + 32 * j;
-        if (slot >= p.topk) break;
+        if (slot >= p.topk || (j == 1 && !kTwo)) break;
         const int id = p.ids[t * p.topk + slot];
         const float dw = p.dw[t * p.topk + slot];
         if (id < 0 || id >= p.experts) continue;
@@ -714,22 +708,22 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
     // picks of one expert: does any slot repeat an earlier one
     const unsigned peers0 = __match_any_sync(kAll, pick[0]);
     bool repeated = pick[0] >= 0 && (peers0 & (peers0 - 1)) != 0;
-    if (two) repeated = true;                            // (not looked for among two slots a lane)
+    if (kTwo) repeated = true;                           // (not looked for among two slots a lane)
     repeated = __any_sync(kAll, repeated);
     if (p.renorm) {
-        shares(softmax, pick, at, p.topk, u);
+        shares<kTwo>(softmax, pick, at, p.topk, u);
     } else if (dense) {
         float l[V];
         load_row<V, T>(row, lane, p.experts, vec, l);
-        const Scores<float> score = scores_of<V, float>(p, l);
+        const Scores score = scores_of<V>(p, l);
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = l[v] > kNegInf ? score(l[v]) : 0.0f;
         if (repeated) {                                  // the first carries their sum
             float merged[2] = {0.0f, 0.0f};
             bool first[2] = {true, true};
             for (int k = 0; k < p.topk; ++k) {
-                const int id = __shfl_sync(kAll, pick[k >> 5], k & 31);
-                const float gk = __shfl_sync(kAll, g[k >> 5], k & 31);
+                const int id = __shfl_sync(kAll, pick[kTwo ? k >> 5 : 0], k & 31);
+                const float gk = __shfl_sync(kAll, g[kTwo ? k >> 5 : 0], k & 31);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     if (id >= 0 && id == pick[j]) {
@@ -744,10 +738,10 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
             }
         }
         u[0] = pick[0] >= 0 ? score(at[0]) : 0.0f;
-        if (two) u[1] = pick[1] >= 0 ? score(at[1]) : 0.0f;
+        if constexpr (kTwo) u[1] = pick[1] >= 0 ? score(at[1]) : 0.0f;
     } else {
         if (pick[0] >= 0) d[0] = g[0] / (1.0f + expf(-at[0])) / (1.0f + expf(at[0]));
-        if (two && pick[1] >= 0) d[1] = g[1] / (1.0f + expf(-at[1])) / (1.0f + expf(at[1]));
+        if (kTwo && pick[1] >= 0) d[1] = g[1] / (1.0f + expf(-at[1])) / (1.0f + expf(at[1]));
     }
     float mean = 0.0f, ref = 0.0f;
     if (p.renorm || dense) {
@@ -771,7 +765,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
         // s_i ((G_i - ref) - mean + ref rest), others -s_i (ref (1 - rest) + mean)
         unsigned taken[(V + 31) / 32] = {};
         for (int k = 0; k < p.topk; ++k) {
-            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31) - lane * V;
+            const int id = __shfl_sync(kAll, pick[kTwo ? k >> 5 : 0], k & 31) - lane * V;
             if (id >= 0 && id < V) taken[0] |= 1u << id;
         }
         float others = 0.0f;
@@ -793,14 +787,14 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
         for (int v = 0; v < V; ++v) s_row[lane * V + v] = acc[v];
         __syncwarp();
         if (pick[0] >= 0) s_row[pick[0]] = d[0];
-        if (two && pick[1] >= 0) s_row[pick[1]] = d[1];
+        if (kTwo && pick[1] >= 0) s_row[pick[1]] = d[1];
         __syncwarp();
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = s_row[lane * V + v];
     } else {                                             // in the order of the slots
         for (int k = 0; k < p.topk; ++k) {
-            const int id = __shfl_sync(kAll, pick[k >> 5], k & 31) - lane * V;
-            const float dk = __shfl_sync(kAll, d[k >> 5], k & 31);
+            const int id = __shfl_sync(kAll, pick[kTwo ? k >> 5 : 0], k & 31) - lane * V;
+            const float dk = __shfl_sync(kAll, d[kTwo ? k >> 5 : 0], k & 31);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (id == v) acc[v] += dk;
@@ -836,9 +830,13 @@ using Kernel = void (*)(RouteParams, bool);
 enum Kind { kGeneral, kPlain, kBackward };
 
 template <typename T, int V>
-constexpr Kernel kernel_of(Kind kind)
+constexpr Kernel kernel_of(Kind kind, bool two)
 {
-    return kind == kBackward ? moe_route_backward_kernel<V, T> : kind == kPlain ? moe_route_plain_kernel<V, T> : moe_route_kernel<V, T>;
+    // (32 experts and fewer have no second slots, but for topk = 32 of them)
+    return kind == kBackward ? (two ? moe_route_backward_kernel<V, T, true> : moe_route_backward_kernel<V, T, false>)
+           : kind == kPlain  ? moe_route_plain_kernel<V, T>
+           : two             ? moe_route_kernel<V, T, true>
+                             : moe_route_kernel<V, T, false>;
 }
 
 // Experts per lane: the power of two that holds them all.
@@ -850,14 +848,14 @@ int lane_experts(int experts)
 }
 
 template <typename T>
-Kernel kernel_for(int v, Kind kind)
+Kernel kernel_for(int v, Kind kind, bool two)
 {
-    return v == 1    ? kernel_of<T, 1>(kind)
-           : v == 2  ? kernel_of<T, 2>(kind)
-           : v == 4  ? kernel_of<T, 4>(kind)
-           : v == 8  ? kernel_of<T, 8>(kind)
-           : v == 16 ? kernel_of<T, 16>(kind)
-                     : kernel_of<T, 32>(kind);
+    return v == 1    ? kernel_of<T, 1>(kind, two)
+           : v == 2  ? kernel_of<T, 2>(kind, two)
+           : v == 4  ? kernel_of<T, 4>(kind, two)
+           : v == 8  ? kernel_of<T, 8>(kind, two)
+           : v == 16 ? kernel_of<T, 16>(kind, two)
+                     : kernel_of<T, 32>(kind, two);
 }
 
 bool vector_rows(const void *base, int64_t ld, int size, int v, int experts)
@@ -874,7 +872,7 @@ cudaError_t launch_route(const RouteParams &p, int num_sms, cudaStream_t s)
     const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
     const Kind kind = p.bias == nullptr && p.groups == 1 && p.topk < 32 ? kPlain : kGeneral;
     const size_t smem = kind == kGeneral ? (size_t)kWarps * p.experts * sizeof(double) : 0;
-    return launch_dependent(size == 4 ? kernel_for<float>(v, kind) : kernel_for<uint16_t>(v, kind), smem,
+    return launch_dependent(size == 4 ? kernel_for<float>(v, kind, p.topk >= 32) : kernel_for<uint16_t>(v, kind, p.topk >= 32), smem,
                             vector_rows(p.logits, p.ldl, size, v, p.experts), s, p);
 }
 
@@ -883,7 +881,8 @@ cudaError_t launch_route_backward(const RouteParams &p, int num_sms, cudaStream_
     (void)num_sms;
     const int v = lane_experts(p.experts), size = p.type == kTypeF32 ? 4 : 2;
     const bool vec = vector_rows(p.logits, p.ldl, size, v, p.experts) && vector_rows(p.dlogits, p.ldd, size, v, p.experts);
-    return launch_dependent(size == 4 ? kernel_for<float>(v, kBackward) : kernel_for<uint16_t>(v, kBackward), 0, vec, s, p);
+    return launch_dependent(size == 4 ? kernel_for<float>(v, kBackward, p.topk > 32)
+                                      : kernel_for<uint16_t>(v, kBackward, p.topk > 32), 0, vec, s, p);
 }
 
 }  // namespace nvfp4
