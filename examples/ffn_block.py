@@ -6,7 +6,7 @@ Each class holds weights prepared once and runs its forward pass without an
 elementwise pass over memory between the GEMMs:
 
     DenseFFN    add_rmsnorm_quant -> GEMM + SwiGLU -> linear + residual
-    MoEFFN      router -> moe_sort -> moe_dispatch_quant -> grouped GEMM + SwiGLU
+    MoEFFN      moe_route -> moe_sort -> moe_dispatch_quant -> grouped GEMM + SwiGLU
                 -> quantizer -> grouped GEMM -> moe_combine (+ residual)
 
 The activation scales are calibrated on the first batch (``calibrate``); the
@@ -80,8 +80,7 @@ class MoEFFN:
         self.alpha2 = (1.0 / (self.gs2 * self.gw2)).expand(self.e).contiguous()
 
     def route(self, x):
-        top, ids = (x.float() @ self.router.float().T).topk(self.topk, dim=1)
-        return ids, torch.softmax(top, dim=1)
+        return nv.moe_route(x.float() @ self.router.float().T, self.topk)
 
     def __call__(self, x):
         ids, weights = self.route(x)

@@ -240,6 +240,15 @@ def _on_gpu(**tensors):
             raise ValueError(f"{name} is on another device than the tensors before it")
 
 
+def _on_current_gpu(**tensors):
+    """_on_gpu, and the device is the current one, whose stream the call goes to."""
+    _on_gpu(**tensors)
+    import torch
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, int) and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _check_linear(x, k, n_out, bias, act, residual, out, **operands):
     """The checks of linear() and mxfp4_linear(); returns (ldx, activation code, ldr, ldo)."""
     if act not in ACTIVATIONS:
@@ -732,7 +741,7 @@ def moe_route(logits, topk: int, score: str = "softmax", bias=None, groups: int 
     import torch
     kind, ld, tokens, experts, code = _logits(logits, topk, score)
     _flat(bias, "bias", "float32", experts)
-    _on_gpu(logits=logits, bias=bias)
+    _on_current_gpu(logits=logits, bias=bias)
     ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
     weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
     nvfp4_moe_route(logits, kind, ld, bias, tokens, experts, code, topk, groups, group_top, topk_groups, renormalize, scale,
@@ -754,7 +763,7 @@ def moe_route_backward(dweights, expert_ids, logits, score: str = "softmax", ren
         raise ValueError(f"expert_ids must have a row per token ({tokens}), got {tuple(expert_ids.shape)}")
     if dweights.shape != expert_ids.shape:
         raise ValueError(f"dweights must be {tuple(expert_ids.shape)} like expert_ids, got {tuple(dweights.shape)}")
-    _on_gpu(logits=logits, expert_ids=expert_ids, dweights=dweights)
+    _on_current_gpu(logits=logits, expert_ids=expert_ids, dweights=dweights)
     dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
     nvfp4_moe_route_backward(dweights, expert_ids, logits, kind, ld, tokens, experts, code, topk, renormalize, scale, dlogits,
                              experts, stream)
@@ -805,7 +814,7 @@ def act_checkpoint(x, act: str = "none", group_offsets=None, group_counts=None, 
     groups = _group_rows(group_offsets, group_counts)
     if out is not None:
         _rows_of(out, "out", m, n)
-    _on_gpu(x=x, group_offsets=group_offsets, group_counts=group_counts, out=out)
+    _on_current_gpu(x=x, group_offsets=group_offsets, group_counts=group_counts, out=out)
     if out is None and act != "none":
         out = torch.empty((m, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=x.device)[:, :n]
     q, sf = _new_mxfp8(m, k, x.device)
@@ -828,7 +837,7 @@ def act_checkpoint_backward(dout, q, sf, act: str = "none", group_offsets=None, 
     _mxfp8(q, sf, m, k)
     if dx is not None:
         _rows_of(dx, "dx", m, k)
-    _on_gpu(dout=dout, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dx=dx)
+    _on_current_gpu(dout=dout, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dx=dx)
     if dx is None:
         dx = torch.empty((m, (k + 7) // 8 * 8), dtype=torch.bfloat16, device=dout.device)[:, :k]
     act_q, act_sf = _new_mxfp8(m, n, dout.device) if recompute else (None, None)
@@ -859,7 +868,7 @@ def checkpoint_wgrad(dy, q, sf, k: int, group_offsets=None, group_counts=None, d
     elif dtype not in (None, torch.float32, torch.bfloat16):
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     _flat(workspace, "workspace", "uint8", 0)
-    _on_gpu(dy=dy, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dw=dw, workspace=workspace)
+    _on_current_gpu(dy=dy, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dw=dw, workspace=workspace)
     if dw is None:
         dw = torch.empty((max(1, groups) * n, (k + 7) // 8 * 8), dtype=dtype or torch.float32, device=dy.device)[:, :k]
     if workspace is None:

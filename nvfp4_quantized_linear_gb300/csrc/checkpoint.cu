@@ -149,7 +149,7 @@ __device__ __forceinline__ int real_rows(const CheckpointParams &p, int band, in
     const int g = part + lane;
     const int fine = lane < step && g < p.num_groups ? p.offsets[g] : INT_MAX;
     const int found = part + max(0, __popc(__ballot_sync(kFull, fine <= row)) - 1);
-    return min(128, max(0, p.counts[found] - (row - p.offsets[found])));
+    return min(min(128, p.m - row), max(0, p.counts[found] - (row - p.offsets[found])));
 }
 
 // 2 N bf16 (two to a word) from column c on; columns past n are not written.
@@ -328,7 +328,7 @@ __device__ __forceinline__ void backward_line(const CheckpointParams &p, const P
 #pragma unroll
     for (int j = 0; j < 4; ++j, q += 32 * (int64_t)p.kp, dout += 32 * p.ldd, dx += 32 * p.ldg, act_q += 32 * (int64_t)p.act_kp) {
         if (at.r + 32 * j >= real) {
-            if (p.offsets != nullptr && with_dx) {       // padding rows of a group
+            if (p.offsets != nullptr && with_dx && row0 + 32 * j < p.m) {    // padding rows of a group
                 const uint32_t zero[8] = {};
                 if constexpr (kWhole) st_global_v8(dx + c, zero);
                 else store_bf16(dx, c, p.k, zero);

@@ -23,6 +23,7 @@
 // next one's MMAs.
 #include <algorithm>
 #include <climits>
+#include <mutex>
 
 #include <cuda_bf16.h>
 
@@ -659,10 +660,12 @@ size_t wgrad_workspace_bytes(int64_t m, int64_t n, int64_t k, int groups)
 cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ldd, const uint8_t *q, void *workspace,
                          int num_sms, cudaStream_t s, const char **why)
 {
+    static std::mutex mutex;
     static int configured_device = -1;
-    static int max_pairs = 0;
-    int dev = 0;
+    static int known_pairs = 0;
+    int dev = 0, max_pairs = 0;
     cudaGetDevice(&dev);
+    std::unique_lock<std::mutex> lock(mutex);
     if (configured_device != dev) {
         cudaError_t e = cudaFuncSetAttribute(wgrad_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
@@ -682,9 +685,11 @@ cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ld
             cudaGetLastError();
             clusters = num_sms / 2;
         }
-        max_pairs = clusters;
+        known_pairs = clusters;
         configured_device = dev;
     }
+    max_pairs = known_pairs;
+    lock.unlock();
     WgradParams p = p_in;
     p.num_n_blk = (p.n + kTile - 1) / kTile;
     p.num_k_blk = (p.k + kTile - 1) / kTile;

@@ -224,6 +224,24 @@ def test_groups(counts, act):
     assert torch.equal(aq[keep], d2[1][keep]) and (aq[~keep] == 0x55).all()
 
 
+def test_rows_that_end_inside_the_last_groups_padding():
+    """A buffer shorter than the groups' padded rows: nothing past it is touched."""
+    offsets, cnt, _, _ = ref.groups_of([130, 20])
+    rows, n = 256 + 20 + 5, 40                               # the last band has 25 rows
+    guard = torch.full((rows + 200, 2 * n), 3.0, dtype=torch.bfloat16, device="cuda")
+    x, dout = bf16(rows, 2 * n, 14), bf16(rows, n, 15)
+    _, q, sf = nv.act_checkpoint(x, "swiglu", offsets, cnt)
+    nv.act_checkpoint_backward(dout, q, sf, "swiglu", offsets, cnt, dx=guard[:rows], recompute=True)
+    torch.cuda.synchronize()
+    assert (guard[rows:] == 3).all() and (guard[276:rows] == 0).all() and (guard[130:256] == 0).all()
+    # counts that claim more rows than there are
+    cnt.copy_(torch.tensor([200, 100], device="cuda"))
+    guard.fill_(3.0)
+    nv.act_checkpoint_backward(dout, q, sf, "swiglu", offsets, cnt, dx=guard[:rows])
+    torch.cuda.synchronize()
+    assert (guard[rows:] == 3).all()
+
+
 def test_captured_with_streams():
     """Replays see new data; a second stream's calls do not disturb the first's."""
     x = bf16(300, 256, 10)

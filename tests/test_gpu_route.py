@@ -52,7 +52,8 @@ def test_plain(t, e, topk, renorm, score, bf16):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("e,groups,topk_groups,topk", [(256, 8, 4, 8), (64, 8, 1, 8), (160, 5, 2, 6), (32, 32, 7, 7),
-                                                       (1024, 32, 3, 20), (6, 2, 1, 3), (96, 3, 3, 4)])
+                                                       (1024, 32, 3, 20), (6, 2, 1, 3), (96, 3, 3, 4),
+                                                       (64, 8, 1, 12), (344, 8, 4, 8), (40, 4, 2, 33)])
 @pytest.mark.parametrize("group_top", [1, 2])
 def test_groups_and_bias(e, groups, topk_groups, topk, group_top, bias, score, bf16):
     g = torch.Generator(device="cuda").manual_seed(e)
