@@ -134,22 +134,20 @@ __device__ __forceinline__ void act_and_slope(uint64_t v, bool relu, uint64_t &f
     else df = fma2(bend, one, s);
 }
 
-// Real rows of a band, of the sorted rows of an expert layer: the group that holds it (its
+// Real rows of a band of the sorted rows of an expert layer: the group that holds it (its
 // rows start on a band) and how many of its rows are tokens; padding rows follow.  -1
-// behind the last group.  Two rounds of 32 lanes find the last group that starts at or
-// before the band.
+// behind the last group.  A group per lane, all loads in flight at once.
 __device__ __forceinline__ int real_rows(const CheckpointParams &p, int band, int lane)
 {
-    if (p.offsets == nullptr) return min(128, max(0, p.m - band * 128));
-    const int row = band * 128, step = (p.num_groups + 31) / 32;
-    const int end = p.offsets[p.num_groups];
-    const int coarse = lane * step < p.num_groups ? p.offsets[lane * step] : INT_MAX;
-    if (row >= end) return -1;
-    const int part = max(0, __popc(__ballot_sync(kFull, coarse <= row)) - 1) * step;
-    const int g = part + lane;
-    const int fine = lane < step && g < p.num_groups ? p.offsets[g] : INT_MAX;
-    const int found = part + max(0, __popc(__ballot_sync(kFull, fine <= row)) - 1);
-    return min(min(128, p.m - row), max(0, p.counts[found] - (row - p.offsets[found])));
+    const int row = band * 128, rows = min(128, max(0, p.m - row));
+    if (p.offsets == nullptr) return rows;
+    int mine = -1;
+#pragma unroll 4
+    for (int g = lane; g < p.num_groups; g += 32) {
+        const int first = p.offsets[g], end = p.offsets[g + 1], count = p.counts[g];
+        if (first <= row && row < end) mine = min(rows, max(0, count - (row - first)));
+    }
+    return __reduce_max_sync(kFull, mine);
 }
 
 // 2 N bf16 (two to a word) from column c on; columns past n are not written.
@@ -243,24 +241,28 @@ __device__ __forceinline__ void store_scales(uint8_t *sf, int band, int r, int c
             (lo & 0xFFFFu) | (hi << 16);
 }
 
-// blockIdx.x = (band * 4 + quarter of its 32 lines) * chunks + chunk; a warp takes a line.
+// blockIdx.x = ((band * 4 + quarter of its 32 lines) * split + share of a line's four rows) *
+// chunks + chunk; a warp takes its line's share.
 struct Place {
     int band, r, c;                                      // the first row's line, the thread's first column
+    int j0, j1;                                          // rows r + 32 j, j0 <= j < j1
+    __device__ __forceinline__ bool has(int j) const { return j >= j0 && j < j1; }
 };
 
-__device__ __forceinline__ Place place_of(int chunks)
+__device__ __forceinline__ Place place_of(int chunks, int split)
 {
-    const unsigned unit = blockIdx.x / chunks;
-    return {(int)(unit >> 2), (int)(unit & 3) * 8 + (int)(threadIdx.x >> 5),
-            (int)(blockIdx.x % chunks) * 512 + (int)(threadIdx.x & 31) * 16};
+    const unsigned unit = blockIdx.x / chunks, line = unit / split, share = unit - line * split;
+    const int rows = 4 / split;
+    return {(int)(line >> 2), (int)(line & 3) * 8 + (int)(threadIdx.x >> 5),
+            (int)(blockIdx.x % chunks) * 512 + (int)(threadIdx.x & 31) * 16, (int)share * rows, (int)(share + 1) * rows};
 }
 
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const CheckpointParams p, int chunks)
+__global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const CheckpointParams p, int chunks, int split)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const Place at = place_of(chunks);
+    const Place at = place_of(chunks, split);
     const int lane = threadIdx.x & 31, c = at.c;
     const int real = real_rows(p, at.band, lane);
     // (without groups the rows past m get zero scales: the last band's padding)
@@ -270,14 +272,13 @@ __global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const Check
     for (int j = 0; j < 4; ++j) {
         const int64_t row = (int64_t)at.band * 128 + at.r + 32 * j;
         raw[j].a = raw[j].b = make_uint4(0, 0, 0, 0);
-        if (at.r + 32 * j < real) raw[j] = load16_coherent(p.x + row * p.ldx, c, p.k);
+        if (at.has(j) && at.r + 32 * j < real) raw[j] = load16_coherent(p.x + row * p.ldx, c, p.k);
     }
     const ActParams act = act_params(p.act);
     uint32_t codes = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const bool here = at.r + 32 * j < real;          // (the same in the whole warp)
-        if (!here) continue;
+        if (!at.has(j) || at.r + 32 * j >= real) continue;       // (the same in the whole warp)
         const int64_t row = (int64_t)at.band * 128 + at.r + 32 * j;
         const uint32_t w[8] = {raw[j].a.x, raw[j].a.y, raw[j].a.z, raw[j].a.w, raw[j].b.x, raw[j].b.y, raw[j].b.z, raw[j].b.w};
         uint64_t v[8];
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 4) act_checkpoint_kernel(const Check
     }
     unsigned rows = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) rows |= (p.offsets == nullptr || at.r + 32 * j < real ? 1u : 0u) << j;
+    for (int j = 0; j < 4; ++j) rows |= (at.has(j) && (p.offsets == nullptr || at.r + 32 * j < real) ? 1u : 0u) << j;
     store_scales<2>(p.sf, at.band, at.r, c, p.nbp, codes, rows);
 }
 
@@ -327,6 +328,7 @@ __device__ __forceinline__ void backward_line(const CheckpointParams &p, const P
     unsigned rows = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j, q += 32 * (int64_t)p.kp, dout += 32 * p.ldd, dx += 32 * p.ldg, act_q += 32 * (int64_t)p.act_kp) {
+        if (!at.has(j)) continue;
         if (at.r + 32 * j >= real) {
             if (p.offsets != nullptr && with_dx && row0 + 32 * j < p.m) {    // padding rows of a group
                 const uint32_t zero[8] = {};
@@ -391,15 +393,16 @@ __device__ __forceinline__ void backward_line(const CheckpointParams &p, const P
             codes |= store_codes<kN>(act_q, oc, kWhole ? INT_MAX : p.act_kp, o) << (8 * j);
         }
     }
-    if (with_act) store_scales<32 / kN>(p.act_sf, at.band, at.r, oc, p.act_nbp, codes, p.offsets == nullptr ? 15u : rows);
+    if (p.offsets == nullptr) rows = (1u << at.j1) - (1u << at.j0);   // (zeros for rows past m)
+    if (with_act) store_scales<32 / kN>(p.act_sf, at.band, at.r, oc, p.act_nbp, codes, rows);
 }
 
 template <bool kGated, int kKind>
-__global__ void __launch_bounds__(kThreads, kGated ? 6 : 4) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks)
+__global__ void __launch_bounds__(kThreads, kGated ? 6 : 4) act_checkpoint_backward_kernel(const CheckpointParams p, int chunks, int split)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const Place at = place_of(chunks);
+    const Place at = place_of(chunks, split);
     const int real = real_rows(p, at.band, threadIdx.x & 31);
     if (real < 0) return;
     const int end = (at.c & ~511) + 512;                 // of the warp's columns
@@ -409,42 +412,50 @@ __global__ void __launch_bounds__(kThreads, kGated ? 6 : 4) act_checkpoint_backw
     else backward_line<kGated, kKind, false>(p, at, real);
 }
 
-cudaError_t launch_dependent(void (*kernel)(CheckpointParams, int), int64_t columns, cudaStream_t s, const CheckpointParams &p)
+// Four rows a warp, two or one where that leaves an SM fewer than four blocks: a short
+// launch is a chain of memory latencies, one for each row of a warp.  Four rows / this
+// rule, us: 128 x 14336 SWIGLU 6.2 / 4.6, its gradient 7.1 / 5.9; 333 x 2072 GELU 4.3 / 3.3
+// and 6.6 / 5.0; from eight blocks an SM on rows of their own lose (512 routed tokens 9.4
+// instead of 7.9, 2048 20 instead of 16).
+cudaError_t launch_dependent(void (*kernel)(CheckpointParams, int, int), int64_t columns, int num_sms, cudaStream_t s,
+                             const CheckpointParams &p)
 {
+    const int64_t enough = 4 * (int64_t)num_sms;
     const int chunks = (int)((columns + 511) / 512);
+    const int64_t lines = rows_padded(p.m) / 128 * 4 * chunks;
+    const int split = lines >= enough ? 1 : lines * 2 >= enough ? 2 : 4;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(rows_padded(p.m) / 128 * 4 * chunks), 1, 1);
+    cfg.gridDim = dim3((unsigned)(lines * split), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, chunks);
+    return cudaLaunchKernelEx(&cfg, kernel, p, chunks, split);
 }
 
 }  // namespace
 
 cudaError_t launch_act_checkpoint(const CheckpointParams &p, int num_sms, cudaStream_t s)
 {
-    (void)num_sms;
     return launch_dependent(act_gated(p.act) ? act_checkpoint_kernel<true> : act_checkpoint_kernel<false>,
-                            (int64_t)p.nbp * 32, s, p);
+                            (int64_t)p.nbp * 32, num_sms, s, p);
 }
 
 cudaError_t launch_act_checkpoint_backward(const CheckpointParams &p, int num_sms, cudaStream_t s)
 {
-    (void)num_sms;
     const bool gated = act_gated(p.act);
     // (padding columns of the activation's scales included)
-    void (*kernel)(CheckpointParams, int) = p.act == kActSwiglu  ? act_checkpoint_backward_kernel<true, kSilu>
+    void (*kernel)(CheckpointParams, int, int) = p.act == kActSwiglu  ? act_checkpoint_backward_kernel<true, kSilu>
                                             : p.act == kActGeglu ? act_checkpoint_backward_kernel<true, kGelu>
                                             : p.act == kActSilu  ? act_checkpoint_backward_kernel<false, kSilu>
                                             : p.act == kActGelu  ? act_checkpoint_backward_kernel<false, kGelu>
                                                                  : act_checkpoint_backward_kernel<false, kRest>;
     return launch_dependent(kernel,
-                            std::max<int64_t>((int64_t)p.nbp * 32, (int64_t)p.act_nbp * 32 * (gated ? 2 : 1)), s, p);
+                            std::max<int64_t>((int64_t)p.nbp * 32, (int64_t)p.act_nbp * 32 * (gated ? 2 : 1)),
+                            num_sms, s, p);
 }
 
 }  // namespace nvfp4
