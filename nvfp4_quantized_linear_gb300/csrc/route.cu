@@ -93,6 +93,14 @@ __device__ __forceinline__ F warp_sum(F v)
     return v;
 }
 
+// Good to 1 ulp; 0 from 2^126 on.
+__device__ __forceinline__ float reciprocal(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Scores of a row: softmax over its experts (max and sum of exponentials given) or
 // sigmoid.  (__fdividef: good to 2 ulp below 2^126.)
 struct Scores {
@@ -100,7 +108,7 @@ struct Scores {
     float max, sum;
     __device__ __forceinline__ float operator()(float l) const
     {
-        return softmax ? __fdividef(expf(l - max), sum) : __fdividef(1.0f, 1.0f + expf(-l));
+        return softmax ? __fdividef(expf(l - max), sum) : reciprocal(1.0f + expf(-l));
     }
 };
 
@@ -494,24 +502,25 @@ __device__ __forceinline__ float slots_sum(float v, int lanes)
     return v;
 }
 
-// Unnormalised shares of the picks, with their largest logit taken out: a softmax over
-// them, or s / e^min(max, 0) for the sigmoid, neither of which underflows in all.
+// Shares of the picks among themselves, their largest logit `top` taken out: a softmax over them,
+// or s / e^min(top, 0) for the sigmoid, neither of which underflows in all.
+__device__ __forceinline__ float share_of(bool softmax, float at, float top)
+{
+    if (softmax) return expf(at - top);
+    if (top < 0.0f) return __fdividef(expf(at - top), 1.0f + expf(at));
+    const float t = expf(-fabsf(at));
+    return __fdividef(at > 0.0f ? 1.0f : t, 1.0f + t);
+}
+
 template <bool kTwo>
 __device__ __forceinline__ void shares(bool softmax, const int (&pick)[2], const float (&at)[2], int topk, float (&u)[2])
 {
     const float top = unordered(__reduce_max_sync(kAll, max(ordered(at[0]), kTwo ? ordered(at[1]) : 0u)));
-    const float m = softmax ? top : fminf(top, 0.0f);
-    u[1] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (j == 1 && !kTwo) break;
-        if (pick[j] < 0) u[j] = 0.0f;
-        else if (softmax) u[j] = expf(at[j] - m);
-        else u[j] = at[j] > 0.0f ? 1.0f / (1.0f + expf(-at[j])) : expf(at[j] - m) / (1.0f + expf(at[j]));
-    }
+    u[0] = pick[0] >= 0 ? share_of(softmax, at[0], top) : 0.0f;
+    u[1] = kTwo && pick[1] >= 0 ? share_of(softmax, at[1], top) : 0.0f;
     const float sum = slots_sum(u[0] + u[1], slot_lanes(topk));
-    u[0] = pick[0] >= 0 ? u[0] / sum : 0.0f;
-    if constexpr (kTwo) u[1] = pick[1] >= 0 ? u[1] / sum : 0.0f;
+    u[0] = pick[0] >= 0 ? __fdividef(u[0], sum) : 0.0f;
+    if constexpr (kTwo) u[1] = pick[1] >= 0 ? __fdividef(u[1], sum) : 0.0f;
 }
 
 // The choice by whole logits, where words of one prefix may be sorted against them: pick by
@@ -606,13 +615,8 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_plain_kernel(const Rout
     }
     float w;
     if (p.renorm) {
-        // (the first pick has the largest logit; see shares())
-        const float top = __shfl_sync(kAll, at, 0), m = score.softmax ? top : fminf(top, 0.0f);
-        float u = 0.0f;
-        if (pick >= 0) {
-            if (score.softmax) u = expf(at - m);
-            else u = at > 0.0f ? 1.0f / (1.0f + expf(-at)) : expf(at - m) / (1.0f + expf(at));
-        }
+        const float top = __shfl_sync(kAll, at, 0);      // (the first pick's logit is the largest)
+        const float u = pick >= 0 ? share_of(score.softmax, at, top) : 0.0f;
         w = __fdividef(u, slots_sum(u, slot_lanes(p.topk)));
     } else {
         w = score(at);
@@ -668,6 +672,13 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- gradient ----
+// s (1 - s) of a sigmoid.
+__device__ __forceinline__ float slope_of(float l)
+{
+    const float t = expf(-fabsf(l)), r = reciprocal(1.0f + t);
+    return t * r * r;
+}
+
 // With g_j = scale * dweights_j of pick j (expert i_j) and u the shares of the picks:
 //   softmax, renormalised  d_j = u_j (g_j - sum_k u_k g_k)
 //   sigmoid, renormalised  d_j = (1 - s_j) u_j (g_j - sum_k u_k g_k)
@@ -705,11 +716,15 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
     float acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    // picks of one expert: does any slot repeat an earlier one
-    const unsigned peers0 = __match_any_sync(kAll, pick[0]);
-    bool repeated = pick[0] >= 0 && (peers0 & (peers0 - 1)) != 0;
-    if (kTwo) repeated = true;                           // (not looked for among two slots a lane)
-    repeated = __any_sync(kAll, repeated);
+    // picks of one expert: of lanes that name it only one finds its mark (two slots a lane:
+    // not looked for)
+    float *const s_row = s_rows[warp];
+    bool repeated = kTwo;
+    if constexpr (!kTwo) {
+        if (pick[0] >= 0) reinterpret_cast<volatile int *>(s_row)[pick[0]] = lane;
+        __syncwarp();
+        repeated = __any_sync(kAll, pick[0] >= 0 && reinterpret_cast<volatile int *>(s_row)[pick[0]] != lane);
+    }
     if (p.renorm) {
         shares<kTwo>(softmax, pick, at, p.topk, u);
     } else if (dense) {
@@ -740,8 +755,8 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
         u[0] = pick[0] >= 0 ? score(at[0]) : 0.0f;
         if constexpr (kTwo) u[1] = pick[1] >= 0 ? score(at[1]) : 0.0f;
     } else {
-        if (pick[0] >= 0) d[0] = g[0] / (1.0f + expf(-at[0])) / (1.0f + expf(at[0]));
-        if (kTwo && pick[1] >= 0) d[1] = g[1] / (1.0f + expf(-at[1])) / (1.0f + expf(at[1]));
+        if (pick[0] >= 0) d[0] = g[0] * slope_of(at[0]);
+        if (kTwo && pick[1] >= 0) d[1] = g[1] * slope_of(at[1]);
     }
     float mean = 0.0f, ref = 0.0f;
     if (p.renorm || dense) {
@@ -758,7 +773,7 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
         for (int j = 0; j < 2; ++j)
             if (pick[j] >= 0) {
                 d[j] = u[j] * ((g[j] - ref) - mean);
-                if (!softmax) d[j] /= 1.0f + expf(at[j]);
+                if (!softmax) d[j] *= reciprocal(1.0f + expf(at[j]));
             }
     } else if (dense) {
         // sum_k s_k G_k = ref (1 - rest) + mean, rest the mass of the others: picked ones have
@@ -781,7 +796,6 @@ __global__ void __launch_bounds__(32 * kWarps) moe_route_backward_kernel(const R
             if (pick[j] >= 0) d[j] = u[j] * ((g[j] - ref) - mean + ref * others);
     }
     // the picks' gradients to their places among the lane's V
-    float *const s_row = s_rows[warp];
     if (!repeated || dense) {
 #pragma unroll
         for (int v = 0; v < V; ++v) s_row[lane * V + v] = acc[v];
