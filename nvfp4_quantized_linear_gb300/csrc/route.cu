@@ -8,7 +8,7 @@
 // A warp takes a token; its logits are read once.  The bytes are few (16384 tokens of 128
 // bf16 logits: 0.8 us), the instructions of picking the experts one by one bound it: 270
 // a token there (5.6 us), 1090 with sigmoid scores, a bias and 8 groups of 256 experts (4099
-// tokens: 12.6 us), where most of them are scores and groups.  A pick is one maximum over
+// tokens: 7.4 us), where most of them are scores and groups.  A pick is one maximum over
 // the warp of words that hold key and expert; a first form, two maxima a pick over unsorted
 // fp32 keys, took 15.4 and 26 us.
 #include <algorithm>
@@ -79,6 +79,11 @@ __device__ __forceinline__ uint64_t ordered(double f)
 {
     const int64_t u = __double_as_longlong(f + 0.0);
     return f > (double)kNegInf ? (uint64_t)(u ^ ((u >> 63) | (int64_t)0x8000000000000000ll)) : 0ull;
+}
+
+__device__ __forceinline__ double unordered(uint64_t o)
+{
+    return __longlong_as_double((int64_t)(o >> 63 ? o ^ 0x8000000000000000ull : ~o));
 }
 
 __device__ __forceinline__ uint64_t warp_max(uint64_t v)
@@ -201,7 +206,61 @@ __device__ __noinline__ unsigned exact_keys(const RouteParams &p, const T *row, 
     return __ballot_sync(kAll, lane < p.groups && rank < p.topk_groups);
 }
 
-// The choice by them, pick by pick the best key after the last pick in the order (keys
+// Groups whose values fp32 cannot tell apart, `low` the lowest of those that stay (bits of
+// kept) and `high` the highest of the others: the ones within tol of the border are valued
+// again in 64 bits.  Lane g has group g's value.  Returns the groups that stay.  (Most launches of
+// thousands of tokens have such a token and wait for it: 4099 x 256 in 8 groups 7.4 us, with
+// every group valued again by exact_keys() 12.6.)
+template <typename T>
+__device__ __noinline__ unsigned exact_groups(const RouteParams &p, const T *row, unsigned kept, float value, float low,
+                                              float high, float tol, int lane)
+{
+    const bool softmax = p.score == kScoreSoftmax;
+    const int size = p.experts / p.groups;
+    double max = 0.0, sum = 1.0;
+    if (softmax) {
+        float m = kNegInf;
+        for (int i = lane; i < p.experts; i += 32) m = fmaxf(m, clean(value_of(row[i])));
+        max = (double)warp_max(m);                       // (some logit is not -inf: two groups have a value)
+        sum = 0.0;
+        for (int i = lane; i < p.experts; i += 32) sum += exp((double)clean(value_of(row[i])) - max);
+        sum = warp_sum(sum);
+    }
+    const bool in = lane < p.groups, stays = (kept >> lane) & 1;
+    const unsigned near = __ballot_sync(kAll, in && !((stays ? value - high : low - value) > tol));
+    const unsigned sure = __ballot_sync(kAll, in && stays) & ~near;
+    double mine = (double)kNegInf;
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        uint64_t best = 0, second = 0;
+        for (int i = lane; i < size; i += 32) {
+            const int e = g * size + i;
+            const float l = clean(value_of(row[e])), b = p.bias != nullptr ? p.bias[e] : 0.0f;
+            double k = (double)kNegInf;
+            if (l > kNegInf && b > kNegInf) {
+                const double x = exp(softmax ? (double)l - max : -(double)l);
+                k = (softmax ? x / sum : 1.0 / (1.0 + x)) + (double)b;
+            }
+            const uint64_t o = ordered(k);
+            second = o > best ? best : o > second ? o : second;
+            best = o > best ? o : best;
+        }
+        const uint64_t first = warp_max(best);
+        const int who = __ffs(__ballot_sync(kAll, best == first)) - 1;
+        const uint64_t next = warp_max(lane == who ? second : best);
+        const double v = unordered(first) + (p.group_top == 2 && next != 0 ? unordered(next) : 0.0);
+        if (lane == g && first != 0) mine = v;
+    }
+    int rank = 0;
+    for (unsigned left = near; left != 0; left &= left - 1) {
+        const int g = __ffs(left) - 1;
+        const double other = __shfl_sync(kAll, mine, g);
+        rank += other > mine || (other == mine && g < lane) ? 1 : 0;
+    }
+    return sure | __ballot_sync(kAll, ((near >> lane) & 1) && rank < p.topk_groups - __popc(sure));
+}
+
+// The choice by exact_keys(), pick by pick the best key after the last pick in the order (keys
 // down, experts up).  Returns the experts of slots lane (low half) and lane + 32, 0xFFFF
 // for none.  About one token in a million comes here.
 template <typename T>
@@ -352,7 +411,8 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     }
     if (p.groups > 1) {
         const int size = p.experts / p.groups, lanes = size / V;
-        bool exact_groups = false;
+        bool near = false;
+        unsigned mask = 0;
         // groups of whole lanes, a power of two of them: by shuffles; others through shared memory, a
         // group per lane.  `mine`: the lane's group, `at0`: where group g's value stands, g * at0.
         const bool whole = lanes * V == size && (lanes & (lanes - 1)) == 0;
@@ -393,19 +453,19 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
             high = warp_max(high);
             // (a score is at most 1; two of them and three roundings)
             const float tol = 4.0f * rel + 2.0f * kAbs + 3.0f * kRound * (fabsf(low) + fabsf(high));
-            if (high > kNegInf && !(low - high > tol)) exact_groups = true;
+            if (high > kNegInf && !(low - high > tol)) {
+                near = true;
+                const float group = __shfl_sync(kAll, value, lane * at0 & 31);
+                const int stays = __shfl_sync(kAll, kept ? 1 : 0, lane * at0 & 31);
+                mask = exact_groups(p, row, __ballot_sync(kAll, stays && lane < p.groups), group, low, high, tol, lane);
+            }
         }
-        if (exact_groups) {
-            const unsigned mask = exact_keys(p, row, s_key, lane);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (!((mask >> ((lane * V + v) / size & 31)) & 1)) key[v] = kNegInf;
-        } else if (whole) {
+        if (whole && !near) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (!kept) key[v] = kNegInf;
         } else {
-            const unsigned mask = __ballot_sync(kAll, kept);
+            if (!near) mask = __ballot_sync(kAll, kept);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (!((mask >> ((lane * V + v) / size & 31)) & 1)) key[v] = kNegInf;

@@ -146,6 +146,18 @@ def test_extreme_logits(score):
     check(l, 3, score, renorm=False, rel=2.0 ** -14)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,group_top,topk_groups", [(1, 1, 1), (4, 1, 2), (4, 2, 2), (8, 2, 3)])
+def test_infinite_bias(groups, group_top, topk_groups, score):
+    """Experts that are always taken beside ones that never are, also as whole groups."""
+    l = logits_of(5, 32, False, 15)
+    l[1, 8:16] = -float("inf")
+    for up, down in (([3], []), ([3, 4, 20], [5]), (range(16), [20]), (range(32), []), ([31], range(24)), (range(8), range(8, 24))):
+        bias = torch.zeros(32, device="cuda")
+        bias[list(up)], bias[list(down)] = float("inf"), -float("inf")
+        check(l, 6, score, bias, groups=groups, group_top=group_top, topk_groups=topk_groups)
+
+
 def test_strides_and_alignment():
     """Rows of a wider buffer, from an odd element on."""
     for dtype in (torch.float32, torch.bfloat16):
