@@ -634,11 +634,14 @@ nvfp4_status nvfp4_act_checkpoint_backward(const void *dout_bf16, int64_t ldd, c
 /* Weight gradient of a linear from the checkpoint of its input:
  *   dw[j, c] = sum_r dy[r, j] * x[r, c]     (dW = dY^T X, the weight's [n, k])
  * on the bf16 tensor cores: every MXFP8 value of magnitude 2^-126 or more (and
- * below 2^127) is exact in bf16, products are exact and sums in fp32.  With
- * groups every expert has its own sum, over its group's real rows, stacked as
- * nvfp4_grouped_gemm's weights: dw[g * n + j, c].  What dy and x hold in
- * padding rows does not matter.  No rows: zeros.  For a gated activation in
- * front n counts gate and up columns, interleaved.
+ * below 2^127) is exact in bf16, products are exact and sums in fp32, which the
+ * tensor cores truncate: they fall short by about 4e-10 of themselves a row (an
+ * fp32 dw by that of 2048 rows at most), and sums below 2^-126 may count as 0.
+ * NaN codes and NaN blocks give NaN.  With groups every expert has its own sum,
+ * over its group's real rows, stacked as nvfp4_grouped_gemm's weights:
+ * dw[g * n + j, c].  What dy and x hold in padding rows does not matter.  No
+ * rows: zeros.  For a gated activation in front n counts gate and up columns,
+ * interleaved.
  *   dy_bf16     in   [m, ldd] bf16, n columns
  *   q, sf       in   x [m, k] in MXFP8
  *   type        an nvfp4_type: of dw

@@ -22,8 +22,8 @@
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the
 // next one's MMAs.
 //
-// 8192 rows, 28672 x 4096 in bf16: 1200 us, 1600 TFLOP/s (0.84 of cuBLAS's bf16 burst rate,
-// 0.94 of its rate under the power cap).  Without the widening, its waits kept, 1165 us.
+// 8192 rows, 28672 x 4096 in bf16: 1235 us, 1560 TFLOP/s (0.82 of cuBLAS's bf16 burst rate,
+// 0.91 of its rate under the power cap).  Without the widening, its waits kept, 1165 us.
 // What the steps before took: all widening warps on every stage 1850; a group of four for
 // each of five stages 1400; its own ring and 8-byte pieces, 8 rows apart, 1205.
 #include <algorithm>
@@ -196,6 +196,19 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t factor, uint32_t &lo
 {
     lo = widen2(__byte_perm(w, 0, 0x1404), factor);
     hi = widen2(__byte_perm(w, 0, 0x3424), factor);
+}
+
+// A top bit of a byte if one of the four codes is E4M3's NaN (0x7F with either sign), which one
+// more takes over its sign bit.  (A carry out of 0xFF may set others: two instructions a word
+// for a look that finds nothing nearly always, 1 to 2 % of the time.)
+__device__ __forceinline__ uint32_t maybe_nan(uint32_t w) { return (w + 0x01010101u) ^ w; }
+
+// NaN for those codes in the four values of widen4.
+__device__ __forceinline__ void put_nan(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t n = (w & 0x7F7F7F7Fu) + 0x01010101u;
+    lo |= (n & 0x80u ? 0x7FC0u : 0) | (n & 0x8000u ? 0x7FC00000u : 0);
+    hi |= (n & 0x800000u ? 0x7FC0u : 0) | (n & 0x80000000u ? 0x7FC00000u : 0);
 }
 
 // Adds four floats to memory without waiting for them (rounded to nearest, subnormals
@@ -385,18 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 const uint32_t band_half = (uint32_t)next & 1u;
                 uint2 w[kPieces];
-                uint32_t code[kPieces], top = 0;
+                uint32_t code[kPieces], top = 0, nans = 0;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
                     w[i] = ld_shared_v2(in_codes + stage * kCodeBytes + i * 8 * kHalf);
                     code[i] = ld_shared_u8(in_sf + stage * kSfBytes + band_half * 8 + (i & 3) * 128 + (i >> 2) * 4);
                     top = max(top, code[i]);
+                    nans |= maybe_nan(w[i].x);
+                    nans |= maybe_nan(w[i].y);
                 }
                 if (before >= 0) {
                     ok = __all_sync(~0u, mbar_wait(&empty[before], before_phase, p.err_flag, kErrTimeout, p.wait_ns));
                     if (!ok) break;
                 }
-                if (!__any_sync(~0u, top > kOneFactor)) {
+                if (!__any_sync(~0u, top > kOneFactor || (nans & 0x80808080u) != 0)) {
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         const uint32_t f = code[i] * 0x00800080u + 120 * 0x00800080u;
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         st_shared_v4(out + i * 1024, v[0], v[1], v[2], v[3]);
                     }
                 } else {
-                    // the part of a factor past bf16's range as a second one, and NaN blocks
+                    // the part of a factor past bf16's range as a second one, NaN codes and blocks
 #pragma unroll
                     for (int i = 0; i < kPieces; ++i) {
                         const uint32_t c1 = min(code[i], kOneFactor);
@@ -415,8 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t v[4];
                         widen4(w[i].x, f1, v[0], v[1]);
                         widen4(w[i].y, f1, v[2], v[3]);
-                        st_shared_v4(out + i * 1024, mul_bf16x2(v[0], f2), mul_bf16x2(v[1], f2), mul_bf16x2(v[2], f2),
-                                     mul_bf16x2(v[3], f2));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = mul_bf16x2(v[j], f2);
+                        put_nan(w[i].x, v[0], v[1]);
+                        put_nan(w[i].y, v[2], v[3]);
+                        st_shared_v4(out + i * 1024, v[0], v[1], v[2], v[3]);
                     }
                 }
                 const int valid = t.rows - next * kRows;

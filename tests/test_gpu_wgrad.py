@@ -127,6 +127,21 @@ def test_nan_blocks_show():
     assert torch.isnan(dw[:, 32:]).all() and torch.isfinite(dw[:, :32]).all()
 
 
+@pytest.mark.parametrize("scale", [127, 200])
+def test_nan_codes_show(scale):
+    """E4M3's NaN, of either sign, in any place of a word."""
+    dy, q, sf, _ = operands(70, 32, 64, 4)
+    sf.fill_(scale)
+    q.fill_(0x30)
+    for i, (row, col) in enumerate([(0, 0), (3, 9), (31, 18), (64, 27), (69, 63), (5, 36)]):
+        q[row, col] = 0x7F if i % 2 else 0xFF
+    dw = nv.checkpoint_wgrad(dy, q, sf, 64)
+    torch.cuda.synchronize()
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[[0, 9, 18, 27, 36, 63]] = True
+    assert torch.isnan(dw[:, bad]).all() and torch.isfinite(dw[:, ~bad]).all()
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("counts", [[5], [0, 0], [1, 0, 130, 128], [127, 1, 0, 64, 65, 300, 0], [64] * 9, [2100, 0, 1025]])
 @pytest.mark.parametrize("n,k", [(128, 64), (300, 300)])
