@@ -14,6 +14,7 @@ innermost stride must be 1.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -247,6 +248,17 @@ def _on_current_gpu(**tensors):
     for name, t in tensors.items():
         if t is not None and not isinstance(t, int) and t.get_device() != torch.cuda.current_device():
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _tensors_of(stream):
+    """Context in which new tensors belong to the stream that a call goes to: memory that another
+    stream's kernels may still use, or may take next, is not theirs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check_linear(x, k, n_out, bias, act, residual, out, **operands):
@@ -742,8 +754,9 @@ def moe_route(logits, topk: int, score: str = "softmax", bias=None, groups: int 
     kind, ld, tokens, experts, code = _logits(logits, topk, score)
     _flat(bias, "bias", "float32", experts)
     _on_current_gpu(logits=logits, bias=bias)
-    ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+    with _tensors_of(stream):
+        ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
     nvfp4_moe_route(logits, kind, ld, bias, tokens, experts, code, topk, groups, group_top, topk_groups, renormalize, scale,
                     ids, weights, stream)
     return ids, weights
@@ -764,7 +777,8 @@ def moe_route_backward(dweights, expert_ids, logits, score: str = "softmax", ren
     if dweights.shape != expert_ids.shape:
         raise ValueError(f"dweights must be {tuple(expert_ids.shape)} like expert_ids, got {tuple(dweights.shape)}")
     _on_current_gpu(logits=logits, expert_ids=expert_ids, dweights=dweights)
-    dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    with _tensors_of(stream):
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
     nvfp4_moe_route_backward(dweights, expert_ids, logits, kind, ld, tokens, experts, code, topk, renormalize, scale, dlogits,
                              experts, stream)
     return dlogits
@@ -815,9 +829,10 @@ def act_checkpoint(x, act: str = "none", group_offsets=None, group_counts=None, 
     if out is not None:
         _rows_of(out, "out", m, n)
     _on_current_gpu(x=x, group_offsets=group_offsets, group_counts=group_counts, out=out)
-    if out is None and act != "none":
-        out = torch.empty((m, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=x.device)[:, :n]
-    q, sf = _new_mxfp8(m, k, x.device)
+    with _tensors_of(stream):
+        if out is None and act != "none":
+            out = torch.empty((m, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=x.device)[:, :n]
+        q, sf = _new_mxfp8(m, k, x.device)
     nvfp4_act_checkpoint(x, ldx, m, n, code, group_offsets, group_counts, groups, out,
                          out.stride(0) if out is not None else 0, q, sf, stream)
     return out, q, sf
@@ -838,9 +853,10 @@ def act_checkpoint_backward(dout, q, sf, act: str = "none", group_offsets=None, 
     if dx is not None:
         _rows_of(dx, "dx", m, k)
     _on_current_gpu(dout=dout, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dx=dx)
-    if dx is None:
-        dx = torch.empty((m, (k + 7) // 8 * 8), dtype=torch.bfloat16, device=dout.device)[:, :k]
-    act_q, act_sf = _new_mxfp8(m, n, dout.device) if recompute else (None, None)
+    with _tensors_of(stream):
+        if dx is None:
+            dx = torch.empty((m, (k + 7) // 8 * 8), dtype=torch.bfloat16, device=dout.device)[:, :k]
+        act_q, act_sf = _new_mxfp8(m, n, dout.device) if recompute else (None, None)
     nvfp4_act_checkpoint_backward(dout, ldd, q, sf, m, n, ACTIVATIONS[act], group_offsets, group_counts, groups, dx,
                                   dx.stride(0), act_q, act_sf, stream)
     return dx, act_q, act_sf
@@ -869,10 +885,12 @@ def checkpoint_wgrad(dy, q, sf, k: int, group_offsets=None, group_counts=None, d
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     _flat(workspace, "workspace", "uint8", 0)
     _on_current_gpu(dy=dy, q=q, sf=sf, group_offsets=group_offsets, group_counts=group_counts, dw=dw, workspace=workspace)
-    if dw is None:
-        dw = torch.empty((max(1, groups) * n, (k + 7) // 8 * 8), dtype=dtype or torch.float32, device=dy.device)[:, :k]
-    if workspace is None:
-        workspace = torch.empty(nvfp4_checkpoint_wgrad_workspace_bytes(m, n, k, groups), dtype=torch.uint8, device=dy.device)
+    with _tensors_of(stream):
+        if dw is None:
+            dw = torch.empty((max(1, groups) * n, (k + 7) // 8 * 8), dtype=dtype or torch.float32, device=dy.device)[:, :k]
+        if workspace is None:
+            workspace = torch.empty(nvfp4_checkpoint_wgrad_workspace_bytes(m, n, k, groups), dtype=torch.uint8,
+                                    device=dy.device)
     kind = NVFP4_TYPE_F32 if dw.dtype == torch.float32 else NVFP4_TYPE_BF16
     nvfp4_checkpoint_wgrad(dy, ldd, q, sf, m, n, k, group_offsets, group_counts, groups, kind, accumulate, dw, dw.stride(0),
                            workspace, workspace.numel(), stream)

@@ -201,6 +201,34 @@ def test_captured_and_on_another_stream():
         assert_close(dw, dy, x2, 500)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_a_call_belongs_to_its_stream(handle):
+    """The stream of the call lags behind the current one, then the current one behind it."""
+    m, n, k = 4096, 256, 256
+    dy, q, sf, _ = operands(m, n, k, 12)
+    want = nv.checkpoint_wgrad(dy, q, sf, k)
+    size = nv.nvfp4_checkpoint_wgrad_workspace_bytes(m, n, k)
+    assert size >= 8 * n * k * 4
+    s = torch.cuda.Stream()
+    arg = s.cuda_stream if handle else s
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    got = nv.checkpoint_wgrad(dy, q, sf, k, stream=arg)      # its workspace is free again before it ran
+    later = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all((t == 255).all() for t in later)
+    before = [torch.empty(n, k, device="cuda") for _ in range(4)]
+    torch.cuda._sleep(20_000_000)
+    for t in before:
+        t.fill_(7.0)
+    del t, before                                            # free for the current stream's next tensors only
+    got = nv.checkpoint_wgrad(dy, q, sf, k, stream=arg)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    nv.nvfp4_device_error()
+
+
 def test_error_of_long_sums(capsys):
     """8192 rows: within the bound, and printed for the record."""
     dy, q, sf, x = operands(8192, 256, 256, 10)
