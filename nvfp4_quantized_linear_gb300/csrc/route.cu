@@ -7,7 +7,7 @@
 //
 // A warp takes a token; its logits are read once.  The bytes are few (16384 tokens of 128
 // bf16 logits: 0.8 us), the instructions of picking the experts one by one bound it: 270
-// a token there (5.6 us), 1090 with sigmoid scores, a bias and 8 groups of 256 experts (4099
+// a token there (5.6 us), 1010 with sigmoid scores, a bias and 8 groups of 256 experts (4099
 // tokens: 7.4 us), where most of them are scores and groups.  A pick is one maximum over
 // the warp of words that hold key and expert; a first form, two maxima a pick over unsorted
 // fp32 keys, took 15.4 and 26 us.
