@@ -229,6 +229,24 @@ def test_memory_of_a_call_belongs_to_its_stream(handle):
     nv.nvfp4_device_error()
 
 
+def test_calls_on_two_streams_at_once():
+    """Split rows, whole rounds of tiles and groups, interleaved."""
+    offsets, cnt, rows, _ = ref.groups_of([300, 0, 129, 1000])
+    calls = []
+    for i, (m, n, k, groups) in enumerate([(4096, 256, 256, ()), (700, 2600, 2100, ()), (rows, 512, 300, (offsets, cnt))]):
+        dy, q, sf, _ = operands(m, n, k, 20 + i)
+        calls.append((dy, q, sf, k, *groups))
+    want = [nv.checkpoint_wgrad(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[nv.checkpoint_wgrad(*calls[(i + j) % 3], stream=s) for j, s in enumerate(streams)] for i in range(9)]
+    torch.cuda.synchronize()
+    nv.nvfp4_device_error()
+    for i, pair in enumerate(got):
+        for j, dw in enumerate(pair):
+            assert torch.equal(dw, want[(i + j) % 3])
+
+
 def test_error_of_long_sums(capsys):
     """8192 rows: within the bound, and printed for the record."""
     dy, q, sf, x = operands(8192, 256, 256, 10)
