@@ -243,27 +243,35 @@ __device__ __forceinline__ void transpose_units(uint32_t (&v)[kWords], int lane)
     }
 }
 
-// A warp's 32 rows x 32 whole columns (a row per lane; o: the first row, `ld` elements apart; `rows` of
-// them are there) to memory, neighbouring lanes side by side: whole 128-byte lines.  Stored
-// a row per lane, 32-byte sectors of another line each, 117 million fp32 took 105 us, so
-// 90; added that way, 8192 routed tokens' gradients took 250 us, so 190.
-__device__ __forceinline__ void store_rows_f32(float *o, int64_t ld, int rows, uint32_t (&v)[32], int lane)
+// 32 bytes of a row, as one store where they are a sector.
+__device__ __forceinline__ void store_32_bytes(void *o, const uint32_t *v)
 {
-    transpose_units<8>(v, lane);
-    o += (lane & ~3) * ld + (lane & 3) * 8;
-    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0 && (ld & 7) == 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i, o += ld) {
-        if ((lane & ~3) + i >= rows) continue;
-        if (sectors) {
-            st_global_v8(o, *reinterpret_cast<const uint32_t(*)[8]>(v + 8 * i));
-        } else {
-            *reinterpret_cast<uint4 *>(o) = make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-            *reinterpret_cast<uint4 *>(o + 4) = make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
-        }
+    if ((reinterpret_cast<uintptr_t>(o) & 31) == 0) {
+        st_global_v8(o, *reinterpret_cast<const uint32_t(*)[8]>(v));
+    } else {
+        static_cast<uint4 *>(o)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(o)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 
+// A warp's 32 rows x 32 whole columns (a row per lane; o: the first row, `ld` elements apart; `rows` of
+// them are there) to memory, pairs of lanes side by side: a store instruction then writes 64 bytes
+// of 16 lines instead of 32 of 32, and the stores stand less in the way of the widening's
+// accesses to shared memory.  64 rows, 28672 x 4096: a row per lane 105 us in fp32 and 70 in bf16, this
+// way 83 and 61 (whole lines of fp32, twice the shuffles: 90).
+__device__ __forceinline__ void store_rows_f32(float *o, int64_t ld, int rows, uint32_t (&v)[32], int lane)
+{
+    transpose_units<16>(v, lane);
+    o += (lane & ~1) * ld + (lane & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i, o += ld) {
+        if ((lane & ~1) + i >= rows) continue;
+        store_32_bytes(o, v + 16 * i);
+        store_32_bytes(o + 8, v + 16 * i + 8);
+    }
+}
+
+// Added to memory: whole lines (8192 routed tokens' gradients, parts of 1024 rows: 224 us, a row per lane 252).
 __device__ __forceinline__ void add_rows_f32(float *o, int64_t ld, int rows, uint32_t (&v)[32], int lane)
 {
     transpose_units<4>(v, lane);
@@ -273,24 +281,17 @@ __device__ __forceinline__ void add_rows_f32(float *o, int64_t ld, int rows, uin
         if ((lane & ~7) + i < rows) red_add_v4(o, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
-// bf16: 64 bytes per lane, in whole sectors where the row allows it (two lanes
-// side by side instead: 67 us where this takes 63).
-__device__ __forceinline__ void store_row_bf16(uint16_t *o, const uint32_t (&v)[32])
+// The same in bf16.
+__device__ __forceinline__ void store_rows_bf16(uint16_t *o, int64_t ld, int rows, const uint32_t (&v)[32], int lane)
 {
-    const bool sectors = (reinterpret_cast<uintptr_t>(o) & 31) == 0;
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 2; ++i, o += 16) {
-        uint32_t w[8];
+    for (int j = 0; j < 16; ++j) w[j] = bf16x2_rn(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+    transpose_units<8>(w, lane);
+    o += (lane & ~1) * ld + (lane & 1) * 16;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            w[j] = bf16x2_rn(__uint_as_float(v[16 * i + 2 * j]), __uint_as_float(v[16 * i + 2 * j + 1]));
-        if (sectors) {
-            st_global_v8(o, w);
-        } else {
-            *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4 *>(o + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-    }
+    for (int i = 0; i < 2; ++i, o += ld)
+        if ((lane & ~1) + i < rows) store_32_bytes(o, w + 8 * i);
 }
 
 // The first `cols` (< 32) of 32 columns of one thread's row: where a row ends inside them.
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (c + 32 > p.dw_cols) {
                         if (lane < rows) store_row_end(p, at + lane * p.ldw, p.dw_cols - c, v, add);
                     } else if (p.type != kTypeF32) {
-                        if (lane < rows) store_row_bf16(static_cast<uint16_t *>(p.dw) + at + lane * p.ldw, v);
+                        store_rows_bf16(static_cast<uint16_t *>(p.dw) + at, p.ldw, rows, v, lane);
                     } else if (add) {
                         add_rows_f32(static_cast<float *>(p.dw) + at, p.ldw, rows, v, lane);
                     } else {
