@@ -635,8 +635,9 @@ nvfp4_status nvfp4_act_checkpoint_backward(const void *dout_bf16, int64_t ldd, c
  *   dw[j, c] = sum_r dy[r, j] * x[r, c]     (dW = dY^T X, the weight's [n, k])
  * on the bf16 tensor cores: every MXFP8 value of magnitude 2^-126 or more (and
  * below 2^127) is exact in bf16, products are exact and sums in fp32, which the
- * tensor cores truncate: they fall short by about 4e-10 of themselves a row (an
- * fp32 dw by that of 2048 rows at most), and sums below 2^-126 may count as 0.
+ * tensor cores truncate: 2048 rows of one sign fall short by 2e-6 of their sum,
+ * 8192 by 1.2e-5.  Longer sums are made of parts of at most 2048 rows (a bf16 dw:
+ * 8192), added in fp32 rounded to nearest.  Sums below 2^-126 may count as 0.
  * NaN codes and NaN blocks give NaN.  With groups every expert has its own sum,
  * over its group's real rows, stacked as nvfp4_grouped_gemm's weights:
  * dw[g * n + j, c].  What dy and x hold in padding rows does not matter.  No

@@ -73,11 +73,14 @@ static_assert(kStages % kSlots == 0, "a group's stages are its own");
 static_assert(kPieces == 8 && kRows == 64, "a thread's rows are eight apart");
 constexpr uint16_t kBothCtas = 0x3;
 
-// Rows of one sum on the tensor cores where dw is fp32: their accumulator is truncated, not
-// rounded, at every step of 16 rows, and falls short by about 4e-10 of itself per row (8192 rows:
-// 3.5e-6); further parts are added to dw in memory, rounded to nearest.  A bf16 dw is rounded to
-// 2^-9 anyway and takes all rows at once.
-constexpr int kPartRows = 2048, kAllRows = INT_MAX;
+// Rows of one sum on the tensor cores, whose accumulator is truncated, not rounded, at every step
+// of 16 rows: a sum of one sign falls short by 2.1e-6 of itself after 2048 rows, 1.2e-5 after
+// 8192, 1.9e-4 after 65536 (of both signs by 6e-7, 3.5e-6).  The parts of a longer sum are added in the other accumulator, in fp32 and rounded to nearest, which holds the
+// tensor cores up for a drain a part: 8192 rows, 28672 x 4096 in bf16 1250 us with parts of 8192
+// rows, 1265 with 4096, 1315 with 2048, 1397 with 1024.  A bf16 gradient is rounded to 2^-9 and takes
+// the longest; an fp32 one's parts cost no more than its stores (16384 rows, 8192 x 4096: 744 us, added to
+// dw in memory 752).
+constexpr int kPartRows = 2048, kPartRowsBf16 = 8192;
 
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -115,6 +118,19 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr)
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
+}
+
+// v += 32 columns of TMEM.
+__device__ __forceinline__ void tmem_add_32cols(uint32_t taddr, uint32_t (&v)[32])
+{
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t u[16];
+        tmem_ld_16cols(taddr + h, u);
+        tmem_ld_wait_regs(u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[h + i] = __float_as_uint(__uint_as_float(u[i]) + __uint_as_float(v[h + i]));
+    }
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -472,15 +488,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t.rows == 0 && p.accumulate) continue;
             const int n0 = t.n0 + (int)rank * kHalf + q * 32;
             const int64_t plane = ((int64_t)t.group * p.n + n0) * p.ldw;
-            for (int r0 = 0; r0 == 0 || r0 < t.rows; r0 += p.part_rows) {
-                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile + col0;
+            // (held: the sum of the parts so far stays in accumulator buf, the next ones come in the other)
+            const bool held = t.rows > p.part_rows;
+            for (int left = t.rows; ok; left -= p.part_rows) {
+                const bool begun = left < t.rows, last = left <= p.part_rows;
+                const int part = held && begun ? buf ^ 1 : buf;
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + part * kTile + col0;
+                const uint32_t sum = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile + col0;
                 if (t.rows > 0) {
-                    ok = __all_sync(~0u, mbar_wait(&tmem_full[buf], phase[buf], p.err_flag, kErrTimeout, p.wait_ns));
+                    ok = __all_sync(~0u, mbar_wait(&tmem_full[part], phase[part], p.err_flag, kErrTimeout, p.wait_ns));
                     if (!ok) break;
-                    phase[buf] ^= 1;
+                    phase[part] ^= 1;
                     tc_fence_after_sync();
                 }
-                const bool add = p.accumulate || r0 > 0;
+                if (held && !begun) continue;
 #pragma unroll 1
                 for (int ch = 0; ch < kEpiCols / 32; ++ch) {
                     const int c = t.k0 + col0 + ch * 32;
@@ -489,6 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t.rows > 0) {
                         tmem_ld_32cols(acc + ch * 32, v);
                         tmem_ld_wait_regs(v);
+                        if (held) {
+                            tmem_add_32cols(sum + ch * 32, v);
+                            if (!last) {
+                                tmem_st_32cols(sum + ch * 32, v);
+                                continue;
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0;
@@ -496,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int rows = p.n - n0;
                     const int64_t at = plane + c;
                     if (c + 32 > p.dw_cols) {
-                        if (lane < rows) store_row_end(p, at + lane * p.ldw, p.dw_cols - c, v, add);
+                        if (lane < rows) store_row_end(p, at + lane * p.ldw, p.dw_cols - c, v, p.accumulate);
                     } else if (p.type != kTypeF32) {
                         store_rows_bf16(static_cast<uint16_t *>(p.dw) + at, p.ldw, rows, v, lane);
-                    } else if (add) {
+                    } else if (p.accumulate) {
                         add_rows_f32(static_cast<float *>(p.dw) + at, p.ldw, rows, v, lane);
                     } else {
                         store_rows_f32(static_cast<float *>(p.dw) + at, p.ldw, rows, v, lane);
@@ -507,14 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 if (t.rows > 0) {
+                    if (held) tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {
-                        if (rank == 0) mbar_arrive(&tmem_empty[buf]);
-                        else mbar_arrive_remote(leader_empty + buf * (uint32_t)sizeof(uint64_t));
+                        for (int b = 0; b < 2; ++b) {
+                            if (b != part && !(held && last)) continue;
+                            if (rank == 0) mbar_arrive(&tmem_empty[b]);
+                            else mbar_arrive_remote(leader_empty + b * (uint32_t)sizeof(uint64_t));
+                        }
                     }
-                    buf ^= 1;
+                    if (!held) buf ^= 1;
                 }
+                if (last) break;
             }
         }
     } else if (warp == 0 && lane == 0) {
@@ -557,11 +590,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int tile = walk.first(); tile < walk.tiles && ok; tile = walk.next()) {
             const WTile t = tile_of(p, tile, table);
-            for (int part = 0; part < t.rows && ok; part += p.part_rows) {
+            const int first = buf;
+            const bool held = t.rows > p.part_rows;      // (as in the epilogue)
+            for (int left = t.rows; left > 0 && ok; left -= p.part_rows) {
+                if (held && left < t.rows) buf = first ^ 1;
                 ok = __all_sync(~0u, mbar_wait(&tmem_empty[buf], acc_phase[buf] ^ 1, p.err_flag, kErrTimeout, p.wait_ns));
                 if (!ok) break;
                 tc_fence_after_sync();
-                const int rows = min(p.part_rows, t.rows - part);
+                const int rows = min(p.part_rows, left);
                 for (int r0 = 0; r0 < rows; r0 += kRows) {
                     ok = __all_sync(~0u, mbar_wait(&ready[slot], phase, p.err_flag, kErrTimeout, p.wait_ns));
                     if (!ok) break;
@@ -584,6 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc_phase[buf] ^= 1;
                 buf ^= 1;
             }
+            if (held) buf = first;
         }
         if (issuer) tc_commit_pair(mma_done);
         __syncwarp();
@@ -728,7 +765,7 @@ cudaError_t launch_wgrad(const WgradParams &p_in, const uint16_t *dy, int64_t ld
         p.dw = workspace;
         p.ldw = p.dw_cols = (int32_t)padded_cols(p.k);
     }
-    p.part_rows = p.type == kTypeF32 ? kPartRows : kAllRows;
+    p.part_rows = p.type == kTypeF32 ? kPartRows : kPartRowsBf16;
     // (no rows: the maps are not read)
     const void *dy_base = p.m > 0 ? static_cast<const void *>(dy) : p.dw, *q_base = p.m > 0 ? q : p.dw;
     const uint64_t rows = p.m > 0 ? (uint64_t)p.m : 1;
