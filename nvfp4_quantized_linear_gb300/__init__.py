@@ -733,7 +733,7 @@ def moe_combine_backward(dout, y, weights, dest, group_offsets, group_counts, dy
     return dy, dweights
 
 
-def _logits(logits, topk, score):
+def _logits(logits, score):
     """(type, row stride, tokens, experts, score code) of a router's logits."""
     if score not in SCORES:
         raise ValueError(f"unknown score {score!r}, not one of {', '.join(SCORES)}")
@@ -742,7 +742,11 @@ def _logits(logits, topk, score):
     if got not in ("float32", "bfloat16"):
         raise ValueError(f"logits must be float32 or bfloat16, got {got}")
     tokens, experts = logits.shape
-    return NVFP4_TYPE_F32 if got == "float32" else NVFP4_TYPE_BF16, max(ld, experts), tokens, experts, SCORES[score]
+    if tokens <= 1:
+        ld = max(ld, experts)                                # (a stride that nothing is read by)
+    elif ld < experts:
+        raise ValueError(f"logits has overlapping rows: row stride {ld}, {experts} experts")
+    return NVFP4_TYPE_F32 if got == "float32" else NVFP4_TYPE_BF16, ld, tokens, experts, SCORES[score]
 
 
 def moe_route(logits, topk: int, score: str = "softmax", bias=None, groups: int = 1, group_top: int = 1,
@@ -751,7 +755,7 @@ def moe_route(logits, topk: int, score: str = "softmax", bias=None, groups: int 
     fp32), both [tokens, topk], as moe_sort and moe_combine take them.  bias (fp32 [experts])
     takes part in the choice only; score is a key of SCORES."""
     import torch
-    kind, ld, tokens, experts, code = _logits(logits, topk, score)
+    kind, ld, tokens, experts, code = _logits(logits, score)
     _flat(bias, "bias", "float32", experts)
     _on_current_gpu(logits=logits, bias=bias)
     with _tensors_of(stream):
@@ -769,7 +773,7 @@ def moe_route_backward(dweights, expert_ids, logits, score: str = "softmax", ren
     if expert_ids.dim() != 2:
         raise ValueError(f"expert_ids must be [tokens, topk], got {tuple(expert_ids.shape)}")
     topk = expert_ids.shape[1]
-    kind, ld, tokens, experts, code = _logits(logits, topk, score)
+    kind, ld, tokens, experts, code = _logits(logits, score)
     _flat(expert_ids, "expert_ids", "int32", 0)
     _flat(dweights, "dweights", "float32", 0)
     if expert_ids.shape[0] != tokens:
