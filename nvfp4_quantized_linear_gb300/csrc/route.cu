@@ -518,8 +518,18 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     if (kTwo && p.topk >= 64) return false;
     // Slots past the picks: the first expert left out, and the next one's word.
     const uint32_t out_second = __reduce_max_sync(kAll, k[0]);
-    const float next_most = out_second >= kLowest ? unordered(out_second | kMask) : kNegInf;
-    bool apart = true, sure = true;                      // neighbours are in order; the next one is behind all picks
+    if (out_second >= kLowest) {
+        // It and all behind it are below every pick: below the lowest pick's key, which within one
+        // prefix need not be the last slot's.  (Their scores are at most the row's highest.)
+        const float next_most = unordered(out_second | kMask);
+        float lowest = lane < p.topk ? kf[0] : INFINITY;
+        if (kTwo && lane + 32 < p.topk) lowest = fminf(lowest, kf[1]);
+        lowest = -warp_max(-lowest);
+        const float most = score.softmax ? __fdividef(1.0f, score.sum) : 1.0f;
+        const float tol = by_logit ? 0.0f : 2.0f * rel * most + 2.0f * kAbs + 2.0f * kRound * (fabsf(lowest) + fabsf(next_most));
+        if (!(lowest - next_most > tol)) return false;
+    }
+    bool apart = true;                                   // neighbours are in order
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         if (j == 1 && !kTwo) break;
@@ -538,9 +548,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         // (experts of one logit and one bias are equal in any precision)
         if (by_logit) apart = apart && at[j] >= next_at;
         else if (at[j] != next_at || b[j] != next_b || slot + 1 == p.topk) apart = apart && kf[j] - next_kf > tol;
-        if (slot + 1 == p.topk && out_second >= kLowest) sure = kf[j] - next_most > tol;
     }
-    if (!__all_sync(kAll, sure)) return false;
     if (__all_sync(kAll, apart)) return true;
     if (kTwo) return false;
     // The picks and the first one left out again by logits, or by keys in 64 bits: each one's
