@@ -141,11 +141,21 @@ __device__ __forceinline__ Scores scores_of(const RouteParams &p, const float (&
     return s;
 }
 
-// Bounds of what the fp32 keys may be off: a score's relative error (expf and quotient 2
-// ulp each, sums; for a softmax the rounding of l - max too, at most 2^-24 of the
-// distance, which the exponential takes below 2^-25 absolute) and the rounding of
-// the sum with the bias.  (Scores below 2^-120 may become 0: far below kAbs.)
-constexpr float kRelSigmoid = 1.25f * 0x1p-21f, kRelSoftmax = 0x1p-20f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
+// Bounds of what the fp32 keys may be off, in units of 2^-24 of a score.
+//   sigmoid  expf 4 (2 ulp), the sum 1, its reciprocal 2: less than 10
+//   softmax  expf 4 and the quotient 4; the sum of V exponentials a lane and of the lanes V + 4,
+//            their expf 4; the rounding of l - max, 2^-24 of its distance: in the sum at
+//            most the mean distance, below ln(32 V) < 7 (an entropy), in the score itself less
+//            than 2^-25 absolute, which kAbs holds: less than V + 24
+// Besides the rounding of the sum with the bias.  (Scores below 2^-120 may become 0: far
+// below kAbs.)
+constexpr float kRelSigmoid = 10 * 0x1p-24f, kAbs = 0x1p-24f, kRound = 0x1p-24f;
+
+template <int V>
+__device__ __forceinline__ float relative_error(bool softmax)
+{
+    return softmax ? (V + 24) * 0x1p-24f : kRelSigmoid;
+}
 
 // ------------------------------------------------------------ exact choice ----
 // Keys in 64 bits, for the tokens whose order the fast choice below cannot be sure of.  Calls,
@@ -411,7 +421,7 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
     float *const s_float = reinterpret_cast<float *>(s_key);
     constexpr uint32_t kMask = 32 * V - 1;
     const bool by_logit = p.bias == nullptr;
-    const float rel = p.score == kScoreSoftmax ? kRelSoftmax : kRelSigmoid;
+    const float rel = relative_error<V>(score.softmax);
     float key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = l[v];

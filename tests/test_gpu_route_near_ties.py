@@ -67,3 +67,18 @@ def test_left_out_expert_with_a_large_score(e, topk):
             target[1] = 24 * 2.0 ** -24
             logits, bias = biased(l, target, "softmax")
             check(logits, topk, "softmax", bias)
+
+
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (2, 1)])
+@pytest.mark.parametrize("e", [64, 256, 512, 1024])
+def test_sums_of_exponentials_that_round_one_way(e, groups, topk_groups):
+    """One score near 1 and others equal, their exponential just off half a step of the sum: the fp32
+    sum of a lane's exponentials is off by its length in half steps, and all scores with it."""
+    for c0, _ in rounding_one_way(e, 12):
+        l = np.full(e, -c0, np.float32)
+        l[0] = 0.0
+        for delta in (-2.0, -1.0, -0.5, 0.5, 1.0, 2.0):
+            target = np.full(e, -1.0)
+            target[0], target[e - 1] = 0.0, delta * 2.0 ** -24
+            logits, bias = biased(l, target, "softmax")
+            check(logits, 1, "softmax", bias, groups=groups, topk_groups=topk_groups)
