@@ -233,22 +233,19 @@ __device__ __noinline__ ExactSoftmax exact_softmax(const RouteParams &p, const T
     return {max, warp_sum(sum)};
 }
 
-// Groups whose values fp32 cannot tell apart, `low` the lowest of those that stay (bits of
-// kept) and `high` the highest of the others: the ones within tol of the border are valued
-// again in 64 bits.  Lane g has group g's value.  Returns the groups that stay.  (Most launches of
+// Groups whose values fp32 cannot tell apart: of `kept` those that may be below the best of
+// the others, and the others that may be above the lowest of `kept`, are valued again in 64 bits
+// (`near`: both; bit g is group g).  Returns the groups that stay.  (Most launches of
 // thousands of tokens have such a token and wait for it: 4099 x 256 in 8 groups 7.4 us, with
 // every group valued again by exact_keys() 12.6.)
 template <typename T>
-__device__ __noinline__ unsigned exact_groups(const RouteParams &p, const T *row, unsigned kept, float value, float low,
-                                              float high, float tol, int lane)
+__device__ __noinline__ unsigned exact_groups(const RouteParams &p, const T *row, unsigned kept, unsigned near, int lane)
 {
     const bool softmax = p.score == kScoreSoftmax;
     const int size = p.experts / p.groups;
     ExactSoftmax of = {0.0, 1.0};
-    if (softmax) of = exact_softmax(p, row, lane);       // (two groups have a value: some logit is not -inf)
-    const bool in = lane < p.groups, stays = (kept >> lane) & 1;
-    const unsigned near = __ballot_sync(kAll, in && !((stays ? value - high : low - value) > tol));
-    const unsigned sure = __ballot_sync(kAll, in && stays) & ~near;
+    if (softmax) of = exact_softmax(p, row, lane);       // (a group has a value: some logit is not -inf)
+    const unsigned sure = kept & ~near;
     double mine = (double)kNegInf;
     for (unsigned left = near; left != 0; left &= left - 1) {
         const int g = __ffs(left) - 1;
@@ -468,17 +465,23 @@ __device__ __forceinline__ bool choose_fast(const RouteParams &p, const T *row, 
         }
         const bool here = mine < p.groups, kept = here && rank < p.topk_groups;
         if (!by_logit || p.group_top == 2) {
+            // What a value may be off: its two scores (together at most 2, the softmax's 1), and three
+            // roundings that go by the keys it is made of, which may cancel; nothing is known of
+            // values past the floats but their side.
+            const float keys = by_logit ? 2.0f : fmaxf(fabsf(top.a), p.group_top == 2 && top.b > kNegInf ? fabsf(top.b) : 0.0f);
+            const float off = 2.0f * rel + 2.0f * kAbs + 8.0f * kRound * keys;
+            float least = value - off, most = value + off;
+            if (!(top.a > kNegInf)) least = most = kNegInf;
+            else if (value == INFINITY) { least = 0x1.fp127f; most = INFINITY; }
+            else if (value == kNegInf) { least = kNegInf; most = -0x1.fp127f; }
             // the lowest group that stays and the highest that does not
-            float low = kept ? value : INFINITY, high = here && !kept ? value : kNegInf;
-            low = -warp_max(-low);
-            high = warp_max(high);
-            // (a score is at most 1; two of them and three roundings)
-            const float tol = 4.0f * rel + 2.0f * kAbs + 3.0f * kRound * (fabsf(low) + fabsf(high));
-            if (high > kNegInf && !(low - high > tol)) {
+            const float low = -warp_max(kept ? -least : kNegInf), high = warp_max(here && !kept ? most : kNegInf);
+            if (high > kNegInf && !(low > high)) {
                 near = true;
-                const float group = __shfl_sync(kAll, value, lane * at0 & 31);
-                const int stays = __shfl_sync(kAll, kept ? 1 : 0, lane * at0 & 31);
-                mask = exact_groups(p, row, __ballot_sync(kAll, stays && lane < p.groups), group, low, high, tol, lane);
+                const int unsure = kept ? !(least > high) : here && !(low > most);
+                const int state = __shfl_sync(kAll, (kept ? 1 : 0) | unsure << 1, lane * at0 & 31);
+                const bool in = lane < p.groups;
+                mask = exact_groups(p, row, __ballot_sync(kAll, in && (state & 1)), __ballot_sync(kAll, in && (state & 2)), lane);
             }
         }
         if (whole && !near) {

@@ -82,3 +82,30 @@ def test_sums_of_exponentials_that_round_one_way(e, groups, topk_groups):
             target[0], target[e - 1] = 0.0, delta * 2.0 ** -24
             logits, bias = biased(l, target, "softmax")
             check(logits, 1, "softmax", bias, groups=groups, topk_groups=topk_groups)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [16.0, 1024.0, 2.0 ** 20])
+@pytest.mark.parametrize("e,groups", [(64, 8), (96, 3), (256, 8)])
+def test_biases_that_cancel_in_a_group(e, groups, size, score):
+    """A group's two highest keys are a large bias and its negative: the sum is far smaller than their roundings."""
+    g = torch.Generator(device="cuda").manual_seed(e)
+    l = torch.randn(400, e, device="cuda", generator=g) * 2.0 ** -13 * size / 1024
+    bias = torch.full((groups, e // groups), -float("inf"), device="cuda")
+    bias[:, 1], bias[:, 3] = size, -size
+    check(l, 4, score, bias.reshape(-1), groups=groups, group_top=2, topk_groups=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [32, 96])
+def test_groups_of_the_lowest_bias_stand_before_empty_ones(e, score):
+    """Masks of the type's lowest value: two such keys add up to -inf in fp32, and yet they are keys."""
+    l = torch.randn(6, 4, e // 4, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    bias = torch.zeros(4, e // 4, device="cuda")
+    l[:, [1, 3]] = -float("inf")
+    l[4, 0] = -float("inf")
+    l[5, 0, 1:] = -float("inf")
+    bias[2] = torch.finfo(torch.float32).min
+    check(l.reshape(6, e), e // 4 + 4, score, bias.reshape(-1), groups=4, group_top=2, topk_groups=2)
+    bias[2, 0] = -torch.finfo(torch.float32).min
+    check(l.reshape(6, e), e // 4 + 4, score, bias.reshape(-1), groups=4, group_top=2, topk_groups=2)
