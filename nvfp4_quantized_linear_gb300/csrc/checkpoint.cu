@@ -391,9 +391,11 @@ __device__ __forceinline__ void backward_line(const CheckpointParams &p, const P
         if constexpr (kWhole) st_global_v8(dx + c, g);
         else if (with_dx) store_bf16(dx, c, p.k, g);
         if (with_act) {
-            if (!kWhole && oc >= p.n_out)                // (columns past n_out: zeros, whatever x's padding holds)
+            if (!kWhole && oc + kN > p.n_out) {          // (columns past n_out: zeros, whatever x's padding holds)
 #pragma unroll
-                for (int i = 0; i < kN / 2; ++i) o[i] = 0;
+                for (int i = 0; i < kN / 2; ++i)
+                    o[i] = oc + 2 * i >= p.n_out ? 0 : oc + 2 * i + 1 >= p.n_out ? o[i] & 0xFFFFFFFFull : o[i];
+            }
             codes |= store_codes<kN>(act_q, oc, kWhole ? INT_MAX : p.act_kp, o) << (8 * j);
         }
     }
