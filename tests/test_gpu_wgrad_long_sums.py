@@ -99,3 +99,13 @@ def test_the_last_part_before_the_most_rows(dtype):
     got = gradient(dy, q, sf, k, (offsets, offsets[1:].contiguous()), dtype).double()
     tol = 192 * 4 * 2.0 ** -22                               # (of at most 192 products of up to 4; zeros add nothing)
     assert bool(((got - want).abs() <= tol + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0)).all())
+
+
+@pytest.mark.parametrize("n,k", [(256, 256), (300, 333)])
+def test_parts_keep_the_error_of_an_fp32_gradient(n, k):
+    """One group of 8192 rows of both signs: off by 6e-7 with parts of 2048 rows, 3.5e-6 in one sum."""
+    offsets, cnt, rows, _ = ref.groups_of([8192])
+    dy, q, sf = operands(rows, n, k, 6)
+    want = dy[:8192].double().T @ torch.from_numpy(ref.decode(q, sf, rows, k)[:8192]).cuda()
+    got = gradient(dy, q, sf, k, (offsets, cnt))
+    assert float((got.double() - want).norm() / want.norm()) <= 1.5e-6
