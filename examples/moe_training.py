@@ -12,7 +12,8 @@ activation's gradient writes it again, in MXFP8, for the second weight's gradien
                activation) -> checkpoint_wgrad of W2 -> times W1, checkpoint_wgrad of W1 -> moe_combine
                (the dispatch's gradient), moe_route_backward
 
-The products with the transposed weights run in bf16 (torch.matmul per expert), on the master weights.
+The products with the transposed weights run in bf16 on the master weights, by torch.matmul in a loop over the experts on the
+host, which reads the groups' offsets and counts back: the other operators can be captured into a graph, this step as a whole not.
 """
 from __future__ import annotations
 
