@@ -20,10 +20,10 @@
 //                of its own: three slots, six stages of copies) and clearing the rows
 //                past a group's last one in both operands (they may hold anything)
 // Two accumulators of 256 columns fill TMEM, so a tile's epilogue runs under the
-// next one's MMAs.
+// next one's MMAs; a long sum, made of parts, takes both.
 //
-// 8192 rows, 28672 x 4096 in bf16: 1235 us, 1560 TFLOP/s (0.82 of cuBLAS's bf16 burst rate,
-// 0.91 of its rate under the power cap).  Without the widening, its waits kept, 1165 us.
+// 8192 rows, 28672 x 4096 in bf16: 1250 us, 1540 TFLOP/s (0.81 of cuBLAS's bf16 burst rate,
+// 0.90 of its rate under the power cap).  Without the widening, its waits kept, 1165 us.
 // What the steps before took: all widening warps on every stage 1850; a group of four for
 // each of five stages 1400; its own ring and 8-byte pieces, 8 rows apart, 1205.
 #include <algorithm>
