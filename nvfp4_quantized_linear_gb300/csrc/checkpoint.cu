@@ -93,8 +93,9 @@ enum ActKind : int { kSilu, kGelu, kRest };
 // b = 2 sqrt(2 / pi), c = 0.044715 for GELU) both are v sigmoid(u), with slope
 // s + v s (1 - s) u'.  The codes of act(v) sit 2^-4 apart, so an error of the value
 // shows as a share of codes on the wrong side of a threshold: e = 2^(-u log2 e) has its
-// argument split into a whole and a fraction (one rounding of 2^-25), 1 / (1 + e) a
-// Newton step.  v is clamped where e leaves the floats, beyond which s is 0 or 1 for
+// argument split into a whole and a fraction (argument reduction in two steps of fused
+// arithmetic, the whole by adding 1.5 * 2^23; one rounding of 2^-25), 1 / (1 + e) a step of
+// Newton and Raphson's iteration.  v is clamped where e leaves the floats, beyond which s is 0 or 1 for
 // fp32.  (Every minimum and maximum keeps a NaN.)
 template <int kKind>
 __device__ __forceinline__ void act_and_slope(uint64_t v, bool relu, uint64_t &f, uint64_t &df)
